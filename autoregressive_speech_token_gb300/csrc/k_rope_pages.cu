@@ -1,0 +1,256 @@
+// sd_rope_init and sd_rope_write_pages: rotary positions with one or several axes,
+// fused with the write of keys and values into a cache's pages.
+//
+// Pair i of a head, (x_i, x_{i+hd/2}), turns by pos[axis(i)] theta^(-2i/hd).  The
+// frequency is kept as a 64-bit fraction of a turn: position times fraction modulo
+// 2^64 is the angle of any position without a long reduction (one integer
+// product; 64-bit floats would be needed otherwise).  Its upper 32 bits, taken
+// to the nearest quarter turn, leave |r| <= 1/8 turn, which fp32 holds to 2^-28
+// of a turn, and sincospif of it gives cos and sin to about their last bit.
+//
+// The call moves its data once and is bound by memory.  A block takes a few tokens:
+// their sines and cosines are formed once, in shared memory, for all heads,
+// while the block's first loads are in flight; then each thread rotates 8 pairs
+// of one head per step with 16-byte loads and stores.
+#include <cmath>
+
+#include "pages_dev.cuh"
+
+namespace sd {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RopeArgs {
+    sd_rope rope;
+    const int32_t *pos, *slot;
+    const void *q, *k, *v;
+    void* q_out;
+    sd_pages c;
+    FastDiv by_ps;
+    int64_t pos_stride, q_stride, qo_stride, kv_stride, slots;
+    int32_t n, H, rotate;
+};
+
+// 8 consecutive elements as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f;
+            if constexpr (std::is_same<T, __half>::value)
+                f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            else
+                f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+struct e4m3_t { uint8_t v; };
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3)
+                         << (16 * (i & 1));
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+}
+
+template <typename T, typename TC, int HD>
+__global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__ RopeArgs a, int tokens) {
+    constexpr int kHalf = HD / 2, kChunks = kHalf / 8;   // 8-pair chunks of a head
+    pdl_trigger();
+    pdl_wait();
+    extern __shared__ float s_cs[];                        // [tokens][cos kHalf | sin kHalf]
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * tokens;
+    const int nt = min(tokens, a.n - t0);
+    if (a.rotate) {
+        for (int i = tid; i < nt * kHalf; i += kThreads) {
+            const int t = i / kHalf, p = i - t * kHalf;
+            const int64_t pos = a.pos[a.rope.axis[p] * a.pos_stride + t0 + t];
+            const uint32_t turn = (uint32_t)((uint64_t)pos * a.rope.turn[p] >> 32);
+            const uint32_t quarter = (turn + (1u << 29)) >> 30;
+            float s, c;
+            sincospif((float)(int32_t)(turn - (quarter << 30)) * 0x1p-31f, &s, &c);
+            // a quarter turn takes (c, s) to (-s, c)
+            const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
+            s_cs[t * HD + p] = (quarter & 2) ? -cc : cc;
+            s_cs[t * HD + kHalf + p] = (quarter & 2) ? -ss : ss;
+        }
+        __syncthreads();
+    }
+    const int per = (a.H + 2 * a.c.n_kv_head) * kChunks;  // work items of a token: q, k and v heads
+    for (int i = tid; i < nt * per; i += kThreads) {
+        const int t = i / per, j = i - t * per;
+        const int head = j / kChunks, d = (j - head * kChunks) * 8;
+        const int64_t tok = t0 + t;
+        const int32_t slot = a.slot[tok];
+        if (slot < 0 || slot >= a.slots) continue;
+        float x[8], y[8];
+        const bool is_q = head < a.H, is_k = !is_q && head < a.H + a.c.n_kv_head;
+        const int g = is_q ? head : is_k ? head - a.H : head - a.H - a.c.n_kv_head;
+        const T* src = is_q ? static_cast<const T*>(a.q) + tok * a.q_stride
+                            : static_cast<const T*>(is_k ? a.k : a.v) + tok * a.kv_stride;
+        src += g * HD + d;
+        load8(src, x);
+        load8(src + kHalf, y);
+        if (a.rotate && (is_q || is_k)) {
+            const float* cs = s_cs + t * HD + d;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float c = cs[e], s = cs[kHalf + e];
+                const float u = x[e] * c - y[e] * s, w = x[e] * s + y[e] * c;
+                x[e] = u;
+                y[e] = w;
+            }
+        }
+        if (is_q) {
+            T* dst = static_cast<T*>(a.q_out) + tok * a.qo_stride + g * HD + d;
+            store8(dst, x);
+            store8(dst + kHalf, y);
+        } else {
+            const uint32_t page = a.by_ps.div((uint32_t)slot);
+            const int64_t off = page * a.c.page_stride + (slot - page * a.by_ps.d) * a.c.pos_stride +
+                                g * a.c.head_stride + d;
+            if constexpr (sizeof(TC) == 1) {
+                const float* sp = is_k ? a.c.k_scale_dev : a.c.v_scale_dev;
+                const float sc = sp ? sp[g] : 1.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = x[e] / sc;
+                    y[e] = y[e] / sc;
+                }
+            }
+            TC* dst = static_cast<TC*>(is_k ? a.c.k_dev : a.c.v_dev) + off;
+            store8(dst, x);
+            store8(dst + kHalf, y);
+        }
+    }
+}
+
+template <typename T, typename TC>
+cudaError_t launch_hd(const RopeArgs& a, cudaStream_t st) {
+    // Two tokens a block; one where that leaves SMs without a block.
+    const int tokens = a.n > 512 ? 2 : 1;
+    const dim3 grid((a.n + tokens - 1) / tokens);
+    const size_t smem = sizeof(float) * tokens * a.c.head_dim;
+    return a.c.head_dim == 64 ? launch_k(k_rope_pages<T, TC, 64>, grid, dim3(kThreads), smem, st, a, tokens)
+                              : launch_k(k_rope_pages<T, TC, 128>, grid, dim3(kThreads), smem, st, a, tokens);
+}
+template <typename T>
+cudaError_t launch_cache(const RopeArgs& a, cudaStream_t st) {
+    return a.c.dtype == SD_F16 ? launch_hd<T, __half>(a, st)
+           : a.c.dtype == SD_BF16 ? launch_hd<T, __nv_bfloat16>(a, st) : launch_hd<T, e4m3_t>(a, st);
+}
+
+}  // namespace
+}  // namespace sd
+
+extern "C" {
+
+int sd_rope_init(int32_t head_dim, double theta, int32_t n_axes, const int32_t* pairs, int32_t interleaved,
+                 sd_rope* out) {
+    using namespace sd;
+    static const char* who = "sd_rope_init";
+    if (!out) return op_fail(SD_ERR_INVALID_ARG, "%s: out is NULL", who);
+    if (head_dim != 64 && head_dim != 128)
+        return op_fail(SD_ERR_UNSUPPORTED, "%s: head_dim %d is not 64 or 128", who, head_dim);
+    const int half = head_dim / 2;
+    if (!(theta > 1.0) || !std::isfinite(theta)) return op_fail(SD_ERR_INVALID_ARG, "%s: theta %g", who, theta);
+    if (n_axes < 1 || n_axes > 4 || (n_axes > 1 && !pairs))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: %d axes (1 to 4), pairs %s", who, n_axes, pairs ? "given" : "NULL");
+    int left[4] = {half, 0, 0, 0};
+    if (pairs) {
+        int64_t sum = 0;
+        for (int a = 0; a < n_axes; ++a) {
+            if (pairs[a] < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: pairs[%d] = %d", who, a, pairs[a]);
+            left[a] = pairs[a];
+            sum += pairs[a];
+        }
+        if (sum != half) return op_fail(SD_ERR_INVALID_ARG, "%s: the axes' pairs do not add up to head_dim/2", who);
+    }
+    *out = sd_rope{};
+    out->head_dim = head_dim;
+    out->n_axes = n_axes;
+    for (int i = 0, a = 0; i < half; ++i) {
+        while (!left[a]) a = (a + 1) % n_axes;
+        out->axis[i] = (uint8_t)a;
+        --left[a];
+        if (interleaved) a = (a + 1) % n_axes;
+        // turns per position, below 1/6, in units of 2^-64: exact scaling of a double
+        out->turn[i] = (uint64_t)ldexp(pow(theta, -2.0 * i / head_dim) / 6.283185307179586476925286766559, 64);
+    }
+    return SD_OK;
+}
+
+int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos_stride, const int32_t* slot_dev,
+                        int32_t n, int32_t dtype, const void* q_dev, int64_t q_stride, void* q_out_dev,
+                        int64_t q_out_stride, int32_t n_head, const void* k_dev, const void* v_dev, int64_t kv_stride,
+                        const sd_pages* cache, void* stream) {
+    using namespace sd;
+    static const char* who = "sd_rope_write_pages";
+    RopeArgs a;
+    if (int rc = check_pages(who, cache, &a.c)) return rc;
+    const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
+    if (!b) return op_fail(SD_ERR_INVALID_ARG, "%s: type %d is not SD_F32, SD_F16 or SD_BF16", who, dtype);
+    if (n < 0 || n_head < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: n %d, n_head %d", who, n, n_head);
+    if (!slot_dev || !k_dev || !v_dev || (rope && !pos_dev))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: NULL argument", who);
+    if ((n_head > 0) != (q_dev != nullptr) || (n_head > 0) != (q_out_dev != nullptr))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: q_dev and q_out_dev come with n_head > 0, and only then", who);
+    if (!aligned16(k_dev) || !aligned16(v_dev) || !aligned16(q_dev) || !aligned16(q_out_dev) ||
+        !stride16(kv_stride, b) || !stride16(q_stride, b) || !stride16(q_out_stride, b))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: pointers and row strides must be multiples of 16 bytes", who);
+    if (q_dev && q_dev == q_out_dev && q_stride != q_out_stride)
+        return op_fail(SD_ERR_INVALID_ARG, "%s: q_out_dev is q_dev with another stride", who);
+    if (rope) {
+        if (rope->head_dim != a.c.head_dim || rope->n_axes < 1 || rope->n_axes > 4)
+            return op_fail(SD_ERR_INVALID_ARG, "%s: rope is for head_dim %d, the cache has %d", who, rope->head_dim,
+                           a.c.head_dim);
+        for (int i = 0; i < rope->head_dim / 2; ++i)
+            if (rope->axis[i] >= rope->n_axes) return op_fail(SD_ERR_INVALID_ARG, "%s: rope is not initialised", who);
+        a.rope = *rope;
+    }
+    if (n == 0) return SD_OK;
+    a.pos = pos_dev; a.slot = slot_dev; a.q = q_dev; a.k = k_dev; a.v = v_dev; a.q_out = q_out_dev;
+    a.pos_stride = pos_stride; a.q_stride = q_stride; a.qo_stride = q_out_stride; a.kv_stride = kv_stride;
+    a.slots = (int64_t)a.c.n_pages * a.c.page_size; a.n = n; a.H = n_head; a.rotate = rope != nullptr;
+    a.by_ps = FastDiv((uint32_t)a.c.page_size);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == SD_F32 ? launch_cache<float>(a, st)
+                          : dtype == SD_F16 ? launch_cache<__half>(a, st) : launch_cache<__nv_bfloat16>(a, st);
+    if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    return SD_OK;
+}
+
+}  // extern "C"

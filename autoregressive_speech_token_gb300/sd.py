@@ -28,7 +28,8 @@ MAX_CODEBOOKS = 16
 EXPORTS = ["sd_create", "sd_load_weights", "sd_prefill", "sd_prefill_shared", "sd_prefill_embeds", "sd_step", "sd_frame", "sd_set_forced_codes", "sd_set_ladder",
            "sd_decode_n", "sd_get_logits", "sd_reset", "sd_destroy", "sd_last_error", "sd_get_info",
            "sd_qmat_create", "sd_qmat_destroy", "sd_qmat_dequant", "sd_qmat_gemv", "sd_qmat_gemm", "sd_qmat_gemm16", "sd_qmat_gemm_tc", "sd_sample_rows", "sd_sample_rows_ladder",
-           "sd_attend_rows", "sd_attend_rows_static"]
+           "sd_attend_rows", "sd_attend_rows_static", "sd_page_plan", "sd_rope_init", "sd_rope_write_pages",
+           "sd_attn_ws_create", "sd_attn_ws_destroy", "sd_attend_pages", "sd_attend_cross"]
 
 
 class SdError(RuntimeError):
@@ -77,6 +78,61 @@ class Info(C.Structure):
                 ("prefill", C.c_int32), ("persistent_clusters", C.c_int32), ("cluster_size", C.c_int32)]
 
 
+# element types of the paged cache and of the attention over it
+F32, F16, BF16, E4M3 = 1, 2, 3, 4
+DTYPES = {"f32": F32, "f16": F16, "bf16": BF16, "e4m3": E4M3}
+_TORCH = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16, "torch.float8_e4m3fn": E4M3}
+
+
+def dtype_of(t) -> int:
+    """SD_F32 ... SD_E4M3 of a torch tensor."""
+    try:
+        return _TORCH[str(t.dtype)]
+    except KeyError:
+        raise TypeError(f"no element type for {t.dtype}") from None
+
+
+class Pages(C.Structure):
+    """sd_pages: the pages of one layer's cache."""
+    _fields_ = [(n, C.c_void_p) for n in ("k_dev", "v_dev", "k_scale_dev", "v_scale_dev")] + \
+               [(n, C.c_int64) for n in ("page_stride", "head_stride", "pos_stride")] + \
+               [(n, C.c_int32) for n in ("dtype", "n_pages", "page_size", "n_kv_head", "head_dim", "reserved")]
+
+    @classmethod
+    def of(cls, k, v, k_scale=None, v_scale=None) -> "Pages":
+        """k, v: tensors [n_pages][n_kv_head][page_size][head_dim] (transposed views give other orders); k_scale,
+        v_scale: fp32 [n_kv_head].  The tensors stay referenced by the result."""
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            raise ValueError("k and v need one shape, stride and type, with contiguous elements")
+        P, g, ps, hd = k.shape
+        p = cls(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), *k.stride()[:3], dtype_of(k), P, ps, g, hd, 0)
+        p.held = (k, v, k_scale, v_scale)
+        return p
+
+
+class Rope(C.Structure):
+    """sd_rope: rotary frequencies and the axis of each pair."""
+    _fields_ = [("turn", C.c_uint64 * 64), ("axis", C.c_uint8 * 64), ("head_dim", C.c_int32), ("n_axes", C.c_int32)]
+
+
+class States(C.Structure):
+    """sd_states: an encoder's keys and values."""
+    _fields_ = [(n, C.c_void_p) for n in ("k_dev", "v_dev", "len_dev")] + \
+               [(n, C.c_int64) for n in ("batch_stride", "head_stride", "pos_stride")] + \
+               [(n, C.c_int32) for n in ("dtype", "B", "n_pos", "n_kv_head", "head_dim", "reserved")]
+
+    @classmethod
+    def of(cls, k, v, length=None) -> "States":
+        """k, v: tensors [B][n_pos][n_kv_head][head_dim] (transposed views give other orders); length: int32 [B].
+        The tensors stay referenced by the result."""
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            raise ValueError("k and v need one shape, stride and type, with contiguous elements")
+        B, n, g, hd = k.shape
+        s = cls(_ptr(k), _ptr(v), _ptr(length), k.stride(0), k.stride(2), k.stride(1), dtype_of(k), B, n, g, hd, 0)
+        s.held = (k, v, length)
+        return s
+
+
 _lib = None
 
 
@@ -118,6 +174,16 @@ def load_library(path: str | None = None):
         "sd_sample_rows_ladder": ([vp, vp, i32, i32, C.POINTER(SamplerLadder), vp, vp, vp, vp], C.c_int),
         "sd_attend_rows": ([vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp], C.c_int),
         "sd_attend_rows_static": ([vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp], C.c_int),
+        "sd_page_plan": ([vp, vp, i32, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp], C.c_int),
+        "sd_rope_init": ([i32, C.c_double, i32, i32p, i32, C.POINTER(Rope)], C.c_int),
+        "sd_rope_write_pages": ([C.POINTER(Rope), vp, i64, vp, i32, i32, vp, i64, vp, i64, i32, vp, vp, i64,
+                                 C.POINTER(Pages), vp], C.c_int),
+        "sd_attn_ws_create": ([i32, C.POINTER(vp)], C.c_int),
+        "sd_attn_ws_destroy": ([vp], None),
+        "sd_attend_pages": ([vp, C.POINTER(Pages), vp, i32, vp, i32, i32, vp, i64, i32, C.c_float, vp, i64, vp, vp],
+                            C.c_int),
+        "sd_attend_cross": ([vp, C.POINTER(States), i32, vp, i64, i64, i32, i32, C.c_float, vp, i64, i64, vp, vp],
+                            C.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -337,7 +403,77 @@ def sd_attend_rows_static(q_dev, k_dev, v_dev, B, H, Hkv, hd, n_ctx, n, nsplit, 
                                                 nsplit, _ptr(out_dev), stream), None)
 
 
+def sd_page_plan(len_dev, new_dev, R: int, free_dev, n_free: int, page_size: int, table_dev, table_stride: int,
+                 rows: int, total_dev, start_dev, slot_dev, pos_dev, req_dev, info_dev, stream=None) -> None:
+    _check(load_library().sd_page_plan(_ptr(len_dev), _ptr(new_dev), R, _ptr(free_dev), n_free, page_size,
+                                       _ptr(table_dev), table_stride, rows, _ptr(total_dev), _ptr(start_dev),
+                                       _ptr(slot_dev), _ptr(pos_dev), _ptr(req_dev), _ptr(info_dev), stream), None)
+
+
+def sd_rope_init(head_dim: int, theta: float, pairs=None, interleaved: bool = False) -> Rope:
+    """sd_rope_init: pairs = the number of pairs of each axis (None: one axis)."""
+    r = Rope()
+    n = 1 if pairs is None else len(pairs)
+    a = None if pairs is None else _p(_arr(pairs, np.int32), C.c_int32)
+    _check(load_library().sd_rope_init(head_dim, theta, n, a, int(interleaved), C.byref(r)), None)
+    return r
+
+
+def sd_rope_write_pages(rope, pos_dev, pos_stride: int, slot_dev, n: int, dtype: int, q_dev, q_stride: int, q_out_dev,
+                        q_out_stride: int, n_head: int, k_dev, v_dev, kv_stride: int, cache: Pages,
+                        stream=None) -> None:
+    _check(load_library().sd_rope_write_pages(rope, _ptr(pos_dev), pos_stride, _ptr(slot_dev), n, dtype, _ptr(q_dev),
+                                              q_stride, _ptr(q_out_dev), q_out_stride, n_head, _ptr(k_dev),
+                                              _ptr(v_dev), kv_stride, cache, stream), None)
+
+
+def sd_attn_ws_create(device: int = -1) -> int:
+    h = C.c_void_p()
+    _check(load_library().sd_attn_ws_create(device, C.byref(h)), None)
+    return h.value
+
+
+def sd_attn_ws_destroy(ws: int) -> None:
+    if ws:
+        load_library().sd_attn_ws_destroy(ws)
+
+
+def sd_attend_pages(ws, cache: Pages, table_dev, table_stride: int, len_dev, R: int, dtype: int, q_dev, q_stride: int,
+                    n_head: int, scale: float, out_dev, out_stride: int, lse_dev=None, stream=None) -> None:
+    """ws: a handle of sd_attn_ws_create or an AttnWorkspace."""
+    _check(load_library().sd_attend_pages(getattr(ws, "handle", ws), cache, _ptr(table_dev), table_stride,
+                                          _ptr(len_dev), R, dtype, _ptr(q_dev), q_stride, n_head, scale,
+                                          _ptr(out_dev), out_stride, _ptr(lse_dev), stream), None)
+
+
+def sd_attend_cross(ws, states: States, dtype: int, q_dev, q_batch: int, q_stride: int, Lq: int, n_head: int,
+                    scale: float, out_dev, out_batch: int, out_stride: int, lse_dev=None, stream=None) -> None:
+    """ws: a handle of sd_attn_ws_create or an AttnWorkspace."""
+    _check(load_library().sd_attend_cross(getattr(ws, "handle", ws), states, dtype, _ptr(q_dev), q_batch, q_stride, Lq,
+                                          n_head, scale, _ptr(out_dev), out_batch, out_stride, _ptr(lse_dev), stream),
+           None)
+
+
 # ------------------------------------------------------------------ convenience wrapper
+
+class AttnWorkspace:
+    """A workspace of sd_attend_pages and sd_attend_cross, freed with the object: one for each stream."""
+
+    def __init__(self, device: int = -1):
+        self.handle = None
+        self.handle = sd_attn_ws_create(device)
+
+    def close(self):
+        if self.handle:
+            sd_attn_ws_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
 
 class Decoder:
     """One decode context: weights, KV cache and captured step graphs."""

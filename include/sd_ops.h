@@ -155,6 +155,155 @@ int sd_attend_rows_static(const float* q_dev, const uint16_t* k_dev, const uint1
                           int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n, int32_t nsplit, float* out_dev,
                           void* stream);
 
+/* ---- Requests of different lengths: a cache in pages, and attention to an
+ * encoder's states.  These entries have no counterpart in the pages; they are
+ * the forms of the step's rotary write and attention for callers that serve
+ * requests of their own lengths (the contexts of sd.h keep one position counter
+ * for all rows) or that attend to states other than the own past (the T3's
+ * conditioning).  All of them are stream-ordered: they queue their kernel on
+ * `stream` and return; nothing is allocated, copied or waited for, so they may be
+ * captured into a graph.  They run on the calling thread's current device (the
+ * attention entries: on their workspace's device); the stream and every pointer
+ * belong to that device.  Return values report arguments and launches. */
+
+/* Element types.  E4M3 is a cache type only. */
+enum { SD_F32 = 1, SD_F16 = 2, SD_BF16 = 3, SD_E4M3 = 4 };
+
+/* The pages of one layer's cache.  Element d of position j of a page, for kv
+ * head g, is at page * page_stride + g * head_stride + j * pos_stride + d
+ * (elements, the same for k_dev and v_dev).  All three strides 0: the order
+ * [page][kv_head][pos][dim], as in the contexts' cache; [page][pos][kv_head][dim]
+ * and pages of all layers in one pool are given by their strides.  Pointers are
+ * 16-byte aligned and strides multiples of 16 bytes.  dtype SD_F16, SD_BF16, or
+ * SD_E4M3 (stored value times k_scale_dev[g] / v_scale_dev[g]; NULL: 1; the scale
+ * pointers are NULL for the other types).  head_dim is 64 or 128, page_size 1 to
+ * 65536, n_pages * page_size at most 2^31 - 1. */
+typedef struct sd_pages {
+    void* k_dev;
+    void* v_dev;
+    const float* k_scale_dev;
+    const float* v_scale_dev;
+    int64_t page_stride, head_stride, pos_stride;
+    int32_t dtype, n_pages, page_size, n_kv_head, head_dim, reserved;
+} sd_pages;
+
+/* Block tables and slot maps of a step from the requests' lengths.  Request r
+ * (0 <= r < R) has len_dev[r] positions in the cache and brings new_dev[r] >= 0
+ * new tokens.  The pages it needs beyond the ceil(len / page_size) it has are
+ * taken from free_dev[n_free], in request order, first to last, and written to
+ * its row of table_dev [R][table_stride]; the row's other entries stay.  Outputs:
+ *   total_dev[R]     len + new
+ *   start_dev[R + 1] new tokens of the requests before r; [R]: of all
+ *   slot_dev[rows]   of new token i of the step: page id * page_size + place in
+ *                    the page; -1 behind the last token
+ *   pos_dev[rows]    its position in its request (0 behind the last token)
+ *   req_dev[rows]    its request (-1 behind the last token)
+ *   info_dev[4]      new tokens; pages taken; what went wrong (bits); longest total
+ * `rows` is the capacity of the step, known to the host.  Bits of info_dev[2]:
+ *   1 more than `rows` new tokens (the first `rows` are mapped, and the pages
+ *     that begin with a later token stay out of the table);
+ *   2 the free list is too short (info_dev[1] says how many pages are needed;
+ *     the table entries without a page are -1, as are their tokens' slots);
+ *   4 a request is longer than its table row (the tokens behind it: slot -1, and
+ *     no page is taken for them);
+ *   8 a negative length or count (read as 0).
+ * A table entry that a token falls into and that is negative gives slot -1.
+ * Calling again with the same inputs gives the same outputs: the new lengths
+ * take effect when the caller passes total_dev as len_dev of the next step.
+ * Counts are held in 64 bits and limited to 2^31 - 1 where they are stored.
+ * free_dev may be NULL when n_free is 0; slot_dev, pos_dev and req_dev when rows
+ * is 0.  The buffers must not overlap. */
+int sd_page_plan(const int32_t* len_dev, const int32_t* new_dev, int32_t R, const int32_t* free_dev, int32_t n_free,
+                 int32_t page_size, int32_t* table_dev, int32_t table_stride, int32_t rows, int32_t* total_dev,
+                 int32_t* start_dev, int32_t* slot_dev, int32_t* pos_dev, int32_t* req_dev, int32_t* info_dev,
+                 void* stream);
+
+/* Rotary frequencies: pair i (elements i and i + head_dim/2, NEOX) turns by
+ * pos[axis[i]] * theta^(-2i/head_dim) radians.  turn[i] holds theta^(-2i/head_dim)
+ * / (2 pi) in units of 2^-64 of a turn, so that a position times it, modulo 2^64, is
+ * the angle without a reduction error at any position. */
+typedef struct sd_rope {
+    uint64_t turn[64];
+    uint8_t axis[64];
+    int32_t head_dim, n_axes;
+} sd_rope;
+
+/* Fill *out (host memory) for head_dim 64 or 128, theta > 1, and n_axes (1 to 4)
+ * position axes: pairs[a] of the head_dim/2 pairs belong to axis a (time, height,
+ * width, ...).  interleaved 0: the first pairs[0] pairs are axis 0's, the next
+ * pairs[1] axis 1's, and so on; otherwise the axes take turns pair by pair, an
+ * axis without pairs left being passed over.  pairs may be NULL for one axis. */
+int sd_rope_init(int32_t head_dim, double theta, int32_t n_axes, const int32_t* pairs, int32_t interleaved,
+                 sd_rope* out);
+
+/* Rotate n tokens' queries and keys and write keys and values into the pages
+ * (journal section 3.13's write at n_past, for tokens of any request): token i,
+ * with positions pos_dev[a * pos_stride + i] on axis a (any int32), goes to slot
+ * slot_dev[i].  A token whose slot is negative or not below n_pages * page_size is
+ * skipped: nothing of it is written.  q_dev [n][n_head][head_dim] (rows q_stride
+ * elements apart) is rotated to q_out_dev (rows q_out_stride apart; may be q_dev
+ * with the same stride); q_dev NULL: no queries (n_head 0).  k_dev / v_dev
+ * [n][n_kv_head][head_dim], rows kv_stride apart: parts of one fused projection's
+ * rows are given by their strides.  dtype (q, k, v and q_out): SD_F32, SD_F16 or
+ * SD_BF16.  Pointers are 16-byte aligned, strides multiples of 16 bytes.  rope
+ * NULL: nothing is rotated (pos_dev NULL; q_out is a copy of q).  Rotated in
+ * fp32 and rounded once; SD_E4M3: value / scale, limited to +-448.  Slots of
+ * a call are distinct (of two tokens with one slot either may remain). */
+int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos_stride, const int32_t* slot_dev,
+                        int32_t n, int32_t dtype, const void* q_dev, int64_t q_stride, void* q_out_dev,
+                        int64_t q_out_stride, int32_t n_head, const void* k_dev, const void* v_dev,
+                        int64_t kv_stride, const sd_pages* cache, void* stream);
+
+/* Workspace of the attention entries below: the partial results of split
+ * lengths, a fixed few MB, allocated here on `device` (-1: the current one).
+ * Calls with one workspace, replays of graphs that captured one among them, must
+ * not overlap: one workspace for each stream. */
+typedef struct sd_attn_ws sd_attn_ws;
+int sd_attn_ws_create(int32_t device, sd_attn_ws** out);
+void sd_attn_ws_destroy(sd_attn_ws* ws);
+
+/* Attention of one new token per request over the paged cache: with g = h /
+ * (n_head / n_kv_head) and len = len_dev[r],
+ *   out[r][h] = sum_{j < len} softmax_j(scale * q[r][h] . K[g][j]) V[g][j],
+ * position j in page table_dev[r * table_stride + j / page_size].  len 0 (or
+ * negative) gives zeros; a len beyond table_stride * page_size is limited to it; the
+ * positions of a page id outside [0, n_pages) are left out, as if masked.
+ * Nothing behind len is used, whatever it holds.  dtype (q and out): SD_F32
+ * (with an SD_F16 or SD_E4M3 cache), SD_F16 or SD_BF16.  q_dev [R][n_head][head_dim]
+ * with rows q_stride elements apart, out_dev the same with out_stride; pointers
+ * are 16-byte aligned, strides multiples of 16 bytes.  lse_dev [R][n_head] (may be
+ * NULL): the natural logarithm of the softmax's denominator, -inf for len 0.
+ * n_head is a multiple of n_kv_head.  q enters the products with at least 22
+ * bits (all of them for 16-bit types), probabilities with 22 (16 for SD_BF16 caches);
+ * sums and statistics are fp32. */
+int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
+                    const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride,
+                    int32_t n_head, float scale, void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
+
+/* Keys and values of an encoder's states, [B][n_pos][n_kv_head][head_dim] by
+ * default (all three strides 0); other orders by their strides (elements,
+ * multiples of 16 bytes; pointers 16-byte aligned).  len_dev[b] states of row b
+ * are used (limited to [0, n_pos]; NULL: n_pos).  dtype SD_F16 or SD_BF16. */
+typedef struct sd_states {
+    const void* k_dev;
+    const void* v_dev;
+    const int32_t* len_dev;
+    int64_t batch_stride, head_stride, pos_stride;
+    int32_t dtype, B, n_pos, n_kv_head, head_dim, reserved;
+} sd_states;
+
+/* Cross attention: every query i < Lq of row b attends to all len[b] states of its
+ * row, whatever Lq is,
+ *   out[b][i][h] = sum_{j < len} softmax_j(scale * q[b][i][h] . K[b][g][j]) V[b][g][j].
+ * q_dev [B][Lq][n_head][head_dim]: batch rows q_batch elements apart (unused for B
+ * 1), queries q_stride apart; out_dev the same with out_batch, out_stride.  A row
+ * without states gives zeros.  States behind len are not used, whatever they hold.
+ * dtype (q and out): SD_F32 (with SD_F16 states), SD_F16 or SD_BF16.  lse_dev
+ * [B][Lq][n_head] (may be NULL) as in sd_attend_pages. */
+int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, const void* q_dev, int64_t q_batch,
+                    int64_t q_stride, int32_t Lq, int32_t n_head, float scale, void* out_dev, int64_t out_batch,
+                    int64_t out_stride, float* lse_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
