@@ -194,12 +194,12 @@ def load_library(path: str | None = None):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     raise TypeError(f"expected a device pointer, got {type(x)}")
 
 

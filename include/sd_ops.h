@@ -266,7 +266,7 @@ void sd_attn_ws_destroy(sd_attn_ws* ws);
  * (n_head / n_kv_head) and len = len_dev[r],
  *   out[r][h] = sum_{j < len} softmax_j(scale * q[r][h] . K[g][j]) V[g][j],
  * position j in page table_dev[r * table_stride + j / page_size].  len 0 (or
- * negative) gives zeros; a len beyond table_stride * page_size is limited to it; the
+ * negative) gives zeros; a len beyond table_stride * page_size (or 2^31 - 1024) is limited to it; the
  * positions of a page id outside [0, n_pages) are left out, as if masked.
  * Nothing behind len is used, whatever it holds.  dtype (q and out): SD_F32
  * (with an SD_F16 or SD_E4M3 cache), SD_F16 or SD_BF16.  q_dev [R][n_head][head_dim]
