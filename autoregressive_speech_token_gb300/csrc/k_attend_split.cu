@@ -99,6 +99,8 @@ struct Shape {
     static constexpr int kCols = kRow / 16;                     // 16-byte columns
     static constexpr int kStage = 2 * kChunk * kRow;            // K and V of 16 positions
     static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 5 : 6;
+    // What beginning and ending a unit costs (about 4 us), in tiles: the share of a block counts it
+    static constexpr int kLead = 96 * 1024 / (kWarps * kStage);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kMerge = kWarps * kSplitRows * (HD + 2) * 4;
     static constexpr int kSmem = kRing + kMerge;
@@ -131,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
     const int64_t U = RT * a.Hkv;                                         // units of a row b
 
     auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
-    auto tiles = [&](int len) { return max((len + kTile - 1) / kTile, 1); };
+    // tiles of a unit, the first kLead of them empty
+    auto tiles = [&](int len) { return (len + kTile - 1) / kTile + S::kLead; };
 
     // ---- this block's share of all tiles
     int64_t mine = 0;
@@ -180,8 +183,17 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         const int nt = tiles(len);
         const int64_t in_b = t - base;
         const int64_t u = in_b / nt;
-        const int i0 = (int)(in_b - u * nt);
-        const int i1 = (int)min((int64_t)nt, i0 + (t_end - t));
+        const int64_t u0 = base + u * nt;                                  // the unit's tiles [u0, u0 + nt)
+        const int64_t next = min(u0 + nt, t_end);
+        // blocks with a part of its tiles (an empty unit: the block with its last empty tile)
+        const int64_t real = min(u0 + S::kLead, u0 + nt - 1);
+        const int c_lo = (int)(real / per), c_hi = (int)((u0 + nt - 1) / per);
+        if (next <= real) {                                                // only empty tiles here
+            t = next;
+            continue;
+        }
+        const int i0 = (int)max(t - u0 - S::kLead, (int64_t)0);
+        const int i1 = (int)(next - u0) - S::kLead;
         const int g = (int)(u / RT);
         const int64_t m0 = (u - g * RT) * kSplitRows;
         const int rows = (int)min((int64_t)kSplitRows, M - m0);
@@ -386,8 +398,6 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
             }
         }
         __syncthreads();
-        const int64_t u0 = base + u * nt;                                  // the unit's tiles [u0, u0 + nt)
-        const int c_lo = (int)(u0 / per), c_hi = (int)((u0 + nt - 1) / per);
         const float vs = a.v_scale ? __ldcg(a.v_scale + g) : 1.f;
         auto put = [&](int r, int d, float val, float mm, float ll) {
             const int64_t m = m0 + r, qi = m / G;
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
             if (d == 0 && a.lse)
                 a.lse[((int64_t)b * a.Lq + qi) * a.H + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - S::kShift) * kLn2;
         };
-        float* rec = a.part + (int64_t)(2 * blockIdx.x + (u0 >= t_begin ? 1 : 0)) * kSplitRecord;
+        float* rec = a.part + (int64_t)(2 * blockIdx.x + (real >= t_begin ? 1 : 0)) * kSplitRecord;
         for (int x = tid; x < rows * HD; x += kThreads) {
             const int r = x / HD, d = x % HD;
             float mm = -INFINITY, ll = 0.f, val = 0.f;
@@ -448,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
             }
         }
         __syncthreads();
-        t += i1 - i0;
+        t = next;
         if (t - base == nt * U) {
             base = t;
             ++b;
