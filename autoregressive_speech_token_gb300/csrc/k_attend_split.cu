@@ -3,14 +3,14 @@
 //
 // A unit is (row b, kv head g, tile of up to 8 query rows of that head's group);
 // a row is (query i, head of the group).  Its positions are cut into tiles of
-// 64, and the tiles of all units, laid end to end, are dealt evenly to the
+// 64 or 128, and the tiles of all units, laid end to end, are dealt evenly to the
 // resident blocks: every block streams the same number of bytes whatever the
 // lengths are, and no host needs to know them.  A unit that ends up in several
 // blocks is joined by the last of them to arrive, in block order (results do not
 // depend on the order of arrival).
 //
 // The kernel is bound by the key and value bytes.  Each of a block's four warps
-// streams its own 16 positions of a tile through a ring of cp.async stages and
+// streams its own 16 or 32 positions of a tile through a ring of cp.async stages and
 // keeps its own running maximum and sum, so that the loop has no block-wide
 // barrier.  Scores are mma.sync products (m16n8k16): a decode step's 8 rows fill
 // half of the 16 rows of the instruction, and the other half holds the rows'
@@ -23,8 +23,7 @@
 namespace sd {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kChunk = 16, kTile = kChunk * kWarps;
-constexpr int kMinTiles = 1;                 // tiles of a block at least
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -78,6 +77,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
         lo = *reinterpret_cast<const uint32_t*>(&l);
     }
 }
+// a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division costs a few hundred cycles)
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // high and low product; an infinite high product has no low one (0 * inf)
 __device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? hi + lo : hi; }
 
@@ -97,8 +100,10 @@ struct Shape {
     static constexpr bool kBf = KV == SD_BF16, kE4 = KV == SD_E4M3;
     static constexpr int kRow = HD * (kE4 ? 1 : 2);             // bytes of a position's row
     static constexpr int kCols = kRow / 16;                     // 16-byte columns
-    static constexpr int kStage = 2 * kChunk * kRow;            // K and V of 16 positions
-    static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 5 : 6;
+    static constexpr int kChunk = kRow >= 256 ? 16 : 32;        // positions of a warp's step: independent products hide
+    static constexpr int kTile = kChunk * kWarps;               // each other's latency, registers allow 16 rows of 256 bytes
+    static constexpr int kStage = 2 * kChunk * kRow;            // K and V of a step
+    static constexpr int kStages = kStage >= 8192 ? 3 : 5;
     // What beginning and ending a unit costs (about 4 us), in tiles: the share of a block counts it
     static constexpr int kLead = 96 * 1024 / (kWarps * kStage);
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -115,7 +120,7 @@ struct Shape {
 template <int HD, int KV>
 __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(const __grid_constant__ AttendArgs a) {
     using S = Shape<HD, KV>;
-    constexpr int kSteps = HD / 16, kOut = HD / 8, kSt = S::kStages;
+    constexpr int kSteps = HD / 16, kOut = HD / 8, kSt = S::kStages, kChunk = S::kChunk, kTile = S::kTile;
     pdl_trigger();
     pdl_wait();
     extern __shared__ __align__(128) unsigned char smem[];
@@ -139,40 +144,55 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
     // ---- this block's share of all tiles
     int64_t mine = 0;
     for (int b = tid; b < a.B; b += kThreads) mine += tiles(length(b));
+    // inclusive sums over the threads: of a row each where B <= kThreads
+    int64_t sum = mine;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (lane == 31) s_sum[warp] = sum;
     __syncthreads();
     int64_t T = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) T += s_sum[w];
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) sum += s_sum[w];
+        T += s_sum[w];
+    }
     T *= U;
-    const int64_t per = max((T + gridDim.x - 1) / gridDim.x, (int64_t)kMinTiles);
+    const int64_t per = max(quot(T + gridDim.x - 1, gridDim.x), (int64_t)1);
     const int64_t t_begin = blockIdx.x * per, t_end = min(T, t_begin + per);
     if (t_begin >= t_end) return;
     // the row b that holds tile t_begin, and the first tile of that row
-    for (int64_t b0 = 0, before = 0; b0 < a.B; b0 += kThreads) {
-        const int64_t b = b0 + tid;
-        const int64_t n = b < a.B ? tiles(length((int)b)) * U : 0;
-        int64_t x = n;
+    if (a.B <= kThreads) {
+        if ((sum - mine) * U <= t_begin && t_begin < sum * U) {
+            s_b = tid;
+            s_base = (sum - mine) * U;
+        }
+    } else {
+        for (int64_t b0 = 0, before = 0; b0 < a.B; b0 += kThreads) {
+            const int64_t b = b0 + tid;
+            const int64_t n = b < a.B ? tiles(length((int)b)) * U : 0;
+            int64_t x = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = x;
+            __syncthreads();
+            int64_t base = before;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) base += s_sum[w];
+                before += s_sum[w];
+            }
+            if (n && base + x - n <= t_begin && t_begin < base + x) {
+                s_b = (int)b;
+                s_base = base + x - n;
+            }
+            if (before > t_begin) break;
         }
-        __syncthreads();
-        if (lane == 31) s_sum[warp] = x;
-        __syncthreads();
-        int64_t base = before;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) base += s_sum[w];
-            before += s_sum[w];
-        }
-        if (n && base + x - n <= t_begin && t_begin < base + x) {
-            s_b = (int)b;
-            s_base = base + x - n;
-        }
-        if (before > t_begin) break;
     }
     __syncthreads();
     int b = s_b;
@@ -182,63 +202,23 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         const int len = length(b);
         const int nt = tiles(len);
         const int64_t in_b = t - base;
-        const int64_t u = in_b / nt;
+        const int64_t u = quot(in_b, nt);
         const int64_t u0 = base + u * nt;                                  // the unit's tiles [u0, u0 + nt)
         const int64_t next = min(u0 + nt, t_end);
         // blocks with a part of its tiles (an empty unit: the block with its last empty tile)
         const int64_t real = min(u0 + S::kLead, u0 + nt - 1);
-        const int c_lo = (int)(real / per), c_hi = (int)((u0 + nt - 1) / per);
+        const int c_lo = (int)quot(real, per), c_hi = (int)quot(u0 + nt - 1, per);
         if (next <= real) {                                                // only empty tiles here
             t = next;
             continue;
         }
         const int i0 = (int)max(t - u0 - S::kLead, (int64_t)0);
         const int i1 = (int)(next - u0) - S::kLead;
-        const int g = (int)(u / RT);
+        const int g = (int)quot(u, RT);
         const int64_t m0 = (u - g * RT) * kSplitRows;
         const int rows = (int)min((int64_t)kSplitRows, M - m0);
 
-        // ---- queries: rows 0-7 of the A operand the rounded rows, rows 8-15 what the rounding left
-        uint32_t qa[kSteps][4];
-        float row_scale = a.scale * kLog2e * (a.k_scale ? __ldcg(a.k_scale + g) : 1.f);
-        {
-            float2 x[kSteps][2];
-            const bool live = row < rows;
-            const int64_t m = m0 + (live ? row : 0), qi = m / G;
-            const int64_t at = b * a.q_batch + qi * a.q_stride + ((int64_t)g * G + (m - qi * G)) * HD;
-            float mx = 0.f;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int d = 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e);
-                    x[k][e] = live ? load2(a.q, at + d, a.dtype) : make_float2(0.f, 0.f);
-                    mx = fmaxf(mx, fmaxf(fabsf(x[k][e].x), fabsf(x[k][e].y)));
-                }
-            float down = 1.f;
-            if (!S::kBf && a.dtype != SD_F16) {
-                // wider exponents than fp16's: the row by a power of two to a largest element in [1, 2)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
-                if (mx > 0.f && mx < INFINITY) {
-                    down = __uint_as_float((uint32_t)(254 - e) << 23);
-                    row_scale *= __uint_as_float((uint32_t)e << 23);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qa[k][2 * e], qa[k][2 * e + 1]);
-        }
-
-        float o[kOut][4];
-#pragma unroll
-        for (int n = 0; n < kOut; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        float mrow = -INFINITY, lrow = 0.f;
-
-        // ---- this warp's chunks: positions (i * 4 + warp) * 16 ... for i in [i0, i1)
+        // ---- this warp's chunks: positions (i * 4 + warp) * kChunk ... for i in [i0, i1)
         int n = 0;
         {
             const int first = i0 * kTile + warp * kChunk;
@@ -253,16 +233,32 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
                        ? id * a.page_stride + (int64_t)((uint32_t)p - page * a.by_ps.d) * a.pos_stride + head : -1;
         };
         auto page_of = [&](int c) -> int {                                 // of this lane's position of chunk c
-            const int p = (i0 + c) * kTile + warp * kChunk + (lane & 15);
+            const int p = (i0 + c) * kTile + warp * kChunk + (lane & (kChunk - 1));
             return a.table && c < n && p < len ? __ldcg(a.table + (int64_t)b * a.table_stride + a.by_ps.div((uint32_t)p)) : -1;
         };
-        int id = page_of(0);
-        auto issue = [&](int c) {
-            const int p = (i0 + c) * kTile + warp * kChunk + (lane & 15);
-            int64_t off = p < len ? offset(p, id) : -1;
-            id = page_of(c + 1);
-            const uint32_t live = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
-            const uint32_t dst = ring + (c % kSt) * S::kStage;
+        int ids[kSt];                                                     // page ids, a ring ahead of the copies
+#pragma unroll
+        for (int c = 0; c < kSt; ++c) ids[c] = page_of(c);
+        // ---- queries of this lane: a row, 4 elements of each 16
+        float2 x[kSteps][2];
+        {
+            const bool live = row < rows;
+            const int64_t m = m0 + (live ? row : 0), qi = quot(m, G);
+            const int64_t at = b * a.q_batch + qi * a.q_stride + ((int64_t)g * G + (m - qi * G)) * HD;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e);
+                    x[k][e] = live ? load2(a.q, at + d, a.dtype) : make_float2(0.f, 0.f);
+                }
+        }
+        auto issue = [&](int c, int slot) {
+            const int p = (i0 + c) * kTile + warp * kChunk + (lane & (kChunk - 1));
+            const int64_t off = p < len ? offset(p, ids[slot]) : -1;
+            ids[slot] = page_of(c + kSt);
+            const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
+            const uint32_t dst = ring + slot * S::kStage;
 #pragma unroll
             for (int r0 = 0; r0 < kChunk; r0 += 32 / S::kCols) {
                 const int r = r0 + lane / S::kCols, col = lane % S::kCols;
@@ -279,48 +275,85 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         for (int s = 0; s < kSt; ++s) live[s] = 0;
 #pragma unroll
         for (int c = 0; c < kSt - 1; ++c) {
-            if (c < n) live[c] = issue(c);
+            if (c < n) live[c] = issue(c, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        // ---- rows 0-7 of the A operand: the rounded rows; rows 8-15: what the rounding left
+        uint32_t qa[kSteps][4];
+        float row_scale = a.scale * kLog2e * (a.k_scale ? __ldcg(a.k_scale + g) : 1.f);
+        {
+            float down = 1.f;
+            if (!S::kBf && a.dtype != SD_F16) {
+                // wider exponents than fp16's: the row by a power of two to a largest element in [1, 2)
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fmaxf(fabsf(x[k][e].x), fabsf(x[k][e].y)));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
+                if (mx > 0.f && mx < INFINITY) {
+                    down = __uint_as_float((uint32_t)(254 - e) << 23);
+                    row_scale *= __uint_as_float((uint32_t)e << 23);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qa[k][2 * e], qa[k][2 * e + 1]);
+        }
+        float o[kOut][4];
+#pragma unroll
+        for (int n = 0; n < kOut; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        float mrow = -INFINITY, lrow = 0.f;
+
         for (int c0 = 0; c0 < n; c0 += kSt) {
 #pragma unroll
             for (int s = 0; s < kSt; ++s) {
                 const int c = c0 + s;
                 if (c >= n) break;
                 __syncwarp();
-                if (c + kSt - 1 < n) live[(s + kSt - 1) % kSt] = issue(c + kSt - 1);
+                if (c + kSt - 1 < n) live[(s + kSt - 1) % kSt] = issue(c + kSt - 1, (s + kSt - 1) % kSt);
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
                 __syncwarp();
                 const uint32_t kb = ring + s * S::kStage, vb = kb + kChunk * S::kRow;
                 const int mi = lane >> 3, mr = lane & 7;
 
-                float sc[2][4] = {};
+                constexpr int kN = kChunk / 8, kH = kChunk / 16;          // products of 8, halves of 16 positions
+                float sc[kN][4] = {};
                 if constexpr (!S::kE4) {
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        uint32_t f[4];
-                        ldm4(kb + S::at((mi >> 1) * 8 + mr, 2 * k + (mi & 1)), f);
-                        mma<S::kBf>(sc[0], qa[k], f[0], f[1]);
-                        mma<S::kBf>(sc[1], qa[k], f[2], f[3]);
-                    }
+                    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) {
+                            uint32_t f[4];
+                            ldm4(kb + S::at(16 * h + (mi >> 1) * 8 + mr, 2 * k + (mi & 1)), f);
+                            mma<S::kBf>(sc[2 * h], qa[k], f[0], f[1]);
+                            mma<S::kBf>(sc[2 * h + 1], qa[k], f[2], f[3]);
+                        }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < kSteps; k += 2) {
-                        uint32_t f[4];
-                        ldm4(kb + S::at((mi & 1) * 8 + mr, k + (mi >> 1)), f);
+                    for (int k = 0; k < kSteps; k += 2)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            mma<false>(sc[0], qa[k + e], half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e] >> 16));
-                            mma<false>(sc[1], qa[k + e], half2_of_e4m3(f[2 * e + 1]), half2_of_e4m3(f[2 * e + 1] >> 16));
+                        for (int h = 0; h < kH; ++h) {
+                            uint32_t f[4];
+                            ldm4(kb + S::at(16 * h + (mi & 1) * 8 + mr, k + (mi >> 1)), f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mma<false>(sc[2 * h], qa[k + e], half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e] >> 16));
+                                mma<false>(sc[2 * h + 1], qa[k + e], half2_of_e4m3(f[2 * e + 1]),
+                                           half2_of_e4m3(f[2 * e + 1] >> 16));
+                            }
                         }
-                    }
                 }
                 // this lane's scores: row `row`, positions 8j + 2 quad and the next
-                float p[2][2], mx = -INFINITY;
+                float p[kN][2], mx = -INFINITY;
                 const uint32_t lv = live[s] >> (2 * quad);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kN; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float x = add_low(sc[j][e], sc[j][2 + e]) * row_scale;
@@ -341,35 +374,39 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
                     mrow = mn;
                 }
                 const float ref = mrow == -INFINITY ? 0.f : mrow - S::kShift;
-                uint32_t pa[4];
+                uint32_t pa[kH][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < kN; ++j) {
                     const float p0 = ex2(p[j][0] - ref), p1 = ex2(p[j][1] - ref);
                     lrow += p0 + p1;
-                    split2<S::kBf>(p0, p1, pa[2 * j], pa[2 * j + 1]);
+                    split2<S::kBf>(p0, p1, pa[j / 2][2 * (j & 1)], pa[j / 2][2 * (j & 1) + 1]);
                 }
                 if constexpr (!S::kE4) {
 #pragma unroll
-                    for (int x = 0; x < kOut; x += 2) {
-                        uint32_t f[4];
-                        ldm4t(vb + S::at((mi & 1) * 8 + mr, x + (mi >> 1)), f);
-                        mma<S::kBf>(o[x], pa, f[0], f[1]);
-                        mma<S::kBf>(o[x + 1], pa, f[2], f[3]);
-                    }
+                    for (int h = 0; h < kH; ++h)
+#pragma unroll
+                        for (int x = 0; x < kOut; x += 2) {
+                            uint32_t f[4];
+                            ldm4t(vb + S::at(16 * h + (mi & 1) * 8 + mr, x + (mi >> 1)), f);
+                            mma<S::kBf>(o[x], pa[h], f[0], f[1]);
+                            mma<S::kBf>(o[x + 1], pa[h], f[2], f[3]);
+                        }
                 } else {
                     // a transposed matrix of byte pairs: even dimensions in the low bytes, odd ones in the high
 #pragma unroll
-                    for (int x = 0; x < kOut; x += 4) {
-                        uint32_t f[4];
-                        ldm4t(vb + S::at((mi & 1) * 8 + mr, x / 2 + (mi >> 1)), f);
+                    for (int h = 0; h < kH; ++h)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            mma<false>(o[x + 2 * e], pa, half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)),
-                                       half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)));
-                            mma<false>(o[x + 2 * e + 1], pa, half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
-                                       half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431)));
+                        for (int x = 0; x < kOut; x += 4) {
+                            uint32_t f[4];
+                            ldm4t(vb + S::at(16 * h + (mi & 1) * 8 + mr, x / 2 + (mi >> 1)), f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                mma<false>(o[x + 2 * e], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)),
+                                           half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)));
+                                mma<false>(o[x + 2 * e + 1], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
+                                           half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431)));
+                            }
                         }
-                    }
                 }
             }
         }
@@ -400,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         __syncthreads();
         const float vs = a.v_scale ? __ldcg(a.v_scale + g) : 1.f;
         auto put = [&](int r, int d, float val, float mm, float ll) {
-            const int64_t m = m0 + r, qi = m / G;
+            const int64_t m = m0 + r, qi = quot(m, G);
             const int64_t h = (int64_t)g * G + (m - qi * G);
             store1(a.out, b * a.o_batch + qi * a.o_stride + h * HD + d, a.dtype, ll == 0.f ? 0.f : val * vs / ll);
             if (d == 0 && a.lse)
@@ -430,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         }
         if (c_lo != c_hi) {
             // ---- the last block of the unit to arrive joins the records in block order
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
+                __threadfence();
                 s_last = atomicAdd(a.cnt + c_lo, 1) == c_hi - c_lo;
                 __threadfence();
             }
@@ -471,7 +508,7 @@ cudaError_t launch_one(const AttendArgs& a, int sms, cudaStream_t st) {
     using S = Shape<HD, KV>;
     // no more blocks than tiles there can be
     const int64_t RT = ((int64_t)a.Lq * (a.H / a.Hkv) + kSplitRows - 1) / kSplitRows;
-    const int64_t most = std::min<int64_t>((int64_t)1 << 30, (int64_t)a.B * RT * a.Hkv) * (a.max_len / kTile + 1);
+    const int64_t most = std::min<int64_t>((int64_t)1 << 30, (int64_t)a.B * RT * a.Hkv) * (a.max_len / S::kTile + 1);
     const int grid = (int)std::min<int64_t>(kSplitBlocksPerSm * sms, most);
     return launch_k(k_attend_split<HD, KV>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
 }
