@@ -8,6 +8,7 @@ struct sd_attn_ws {
     int device = 0, sms = 0;
     float* part = nullptr;
     int* cnt = nullptr;
+    int* err = nullptr;              // pinned: a kernel's expired wait
 };
 
 namespace sd {
@@ -23,7 +24,7 @@ struct AttendArgs {
     int32_t B, Lq, H, Hkv, n_pages, table_stride, max_len, dtype, kv_dtype;
     float scale;
     float* part;
-    int* cnt;
+    int *cnt, *err;
 };
 
 constexpr int kSplitBlocksPerSm = 2;                              // at most
@@ -33,6 +34,8 @@ constexpr int kSplitRecord = kSplitRows * (128 + 2);              // floats of a
 constexpr int kMaxPositions = INT32_MAX - 1023;                   // of a row: tile arithmetic stays within int32
 
 cudaError_t prepare_attend_split();                               // shared-memory limits on the current device
+cudaError_t prepare_attend_tc();
+cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t st, bool* taken);
 cudaError_t launch_attend_split(const AttendArgs& a, int hd, int sms, cudaStream_t st);
 
 }  // namespace sd

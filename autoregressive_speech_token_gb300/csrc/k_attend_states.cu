@@ -6,6 +6,8 @@
 namespace sd {
 namespace {
 
+constexpr int kTcQueries = 48;
+
 int check_q(const char* who, int dtype, int kv_dtype, const void* q, int64_t q_stride, const void* out,
             int64_t out_stride, int n_head, int n_kv, float scale) {
     const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
@@ -23,9 +25,18 @@ int check_q(const char* who, int dtype, int kv_dtype, const void* q, int64_t q_s
 int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream) {
     DeviceScope scope(ws->device);
     if (scope.err != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(scope.err));
+    if (*static_cast<volatile int*>(ws->err))
+        return op_fail(SD_ERR_TIMEOUT, "%s: a wait of an earlier call on this workspace expired", who);
     a.part = ws->part;
     a.cnt = ws->cnt;
-    const cudaError_t e = launch_attend_split(a, hd, ws->sms, reinterpret_cast<cudaStream_t>(stream));
+    a.err = ws->err;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    // Tensor-core tiles of 128 queries of a head: queries, keys and values of one 16-bit type, and enough queries
+    bool taken = false;
+    if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && a.Lq >= kTcQueries)
+        e = launch_attend_tc(a, hd, ws->sms, st, &taken);
+    if (!taken) e = launch_attend_split(a, hd, ws->sms, st);
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return SD_OK;
 }
@@ -55,7 +66,10 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     // on the legacy stream, and waited for: the first call may be on any stream
     if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * sizeof(int));
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+    if (e == cudaSuccess) e = cudaHostAlloc(&ws->err, sizeof(int), cudaHostAllocDefault);
+    if (e == cudaSuccess) *ws->err = 0;
     if (e == cudaSuccess) e = prepare_attend_split();
+    if (e == cudaSuccess) e = prepare_attend_tc();
     if (e != cudaSuccess) {
         sd_attn_ws_destroy(ws);
         return op_fail(e == cudaErrorMemoryAllocation ? SD_ERR_OOM : SD_ERR_CUDA, "sd_attn_ws_create: %s",
@@ -70,6 +84,7 @@ void sd_attn_ws_destroy(sd_attn_ws* ws) {
     sd::DeviceScope scope(ws->device);
     cudaFree(ws->part);
     cudaFree(ws->cnt);
+    cudaFreeHost(ws->err);
     delete ws;
 }
 

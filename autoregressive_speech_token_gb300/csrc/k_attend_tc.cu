@@ -1,0 +1,546 @@
+// Cross attention of many queries on the 5th-generation tensor cores: TMA loads,
+// tcgen05 products with scores, probabilities and results in tensor memory.
+//
+// A work item is a pair of query tiles (128 queries of one head each) of one (row b,
+// kv head g), against all of that row's positions in tiles of 128.  One block per
+// SM walks the items; per position tile j and query tile i
+//   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
+//   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
+//   O_i += P_i V_j (fp32, head_dim columns)
+// One thread issues all products, one all loads.  Two warpgroups each own one query
+// tile, a thread per query: running maximum and sum need no exchange between
+// threads, and while one warpgroup forms P of its tile the tensor cores work on the
+// other's.  The reference m_i of the exponentials moves only when the maximum has
+// grown by more than 2^8 (probabilities stay below 2^8, sums are fp32): results in
+// tensor memory are seldom rescaled, and then by the same thread, which knows
+// from S_i(j)'s completion that P_i V_(j-1) is complete (products of one thread
+// complete in order).
+//
+// Rounding P to 16 bits is off by half a step of the output's own type and averages
+// out over the positions; the sum uses the unrounded values.  fp16 probabilities
+// carry a factor 2^7 to stay above the subnormal step.
+//
+// Every wait is bounded: on expiry the block records the error, lets its own copies
+// and products finish (bounded), frees its tensor memory and returns.
+#include <cuda.h>
+
+#include "attend_dev.cuh"
+
+namespace sd {
+namespace {
+
+constexpr int kM = 128, kN = 128;                    // queries and positions of a tile
+constexpr int kSoftWarps = 8, kThreads = 32 * (kSoftWarps + 4);    // 2 softmax warpgroups; products, loads, 2 idle warps
+constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Registers of a thread: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72 (a softmax thread holds a row of 128 scores)
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
+constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
+constexpr long long kWaitClocks = 4000000000ll;      // about two seconds
+
+struct alignas(128) TcArgs {
+    CUtensorMap q, k, v;
+    AttendArgs a;
+    int32_t nq, pairs;                                // query tiles of a head, pairs of a (b, g)
+    int64_t items;
+};
+
+template <int HD>
+struct Cfg {
+    static constexpr int kPanel = kN * 128;                       // 128 rows of 64 elements, 128-byte swizzle
+    static constexpr int kTileBytes = kPanel * (HD / 64);         // a Q, K or V tile
+    static constexpr int kStages = HD == 128 ? 5 : 11;            // K and V tiles in flight
+    static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+    static constexpr uint32_t kO = 256;                           // tensor memory: S0, S1, O0, O1
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mb_init(uint32_t mb, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mb_expect(uint32_t mb, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mb_arrive(uint32_t mb) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory");
+}
+__device__ __forceinline__ bool mb_try(uint32_t mb, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(mb), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Bounded; gives up early once another warp of the block has given up.
+__device__ __forceinline__ bool mb_wait_slow(uint32_t mb, uint32_t parity, volatile int* bad) {
+    const long long t0 = clock64();
+    while (!mb_try(mb, parity)) {
+        if (*bad) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            *bad = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+    return mb_try(mb, parity) || mb_wait_slow(mb, parity, bad);
+}
+// The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+    return __all_sync(0xffffffffu, mb_wait(mb, parity, bad));
+}
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int h, int r, int b, uint32_t mb) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(r), "r"(b), "r"(mb) : "memory");
+}
+// Shared-memory descriptor of a 128-byte-swizzled operand: 8-row groups 1024 bytes apart; `lead` is the
+// distance of the next 64 columns for an operand read along its rows (V), unused otherwise.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lead >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t mb) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mb) : "memory");
+}
+__device__ __forceinline__ void tm_ld32(uint32_t addr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld16(uint32_t addr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+          "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Ties 16 loaded registers to the point behind the wait: nothing that uses them moves before it.
+__device__ __forceinline__ void after_wait(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+template <int HD, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant__ TcArgs t) {
+    using C = Cfg<HD>;
+    constexpr int kSt = C::kStages;
+    constexpr float kShift = BF ? 0.f : 7.f;
+    constexpr uint32_t kType = BF ? 1u : 0u;
+    // fp32 result, A and B of one type, M = 128; scores: N = 128, both K-major; results: N = HD, V read along its rows
+    constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+    constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+    extern __shared__ unsigned char smraw[];
+    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_ofull[2], s_tail;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_bad;
+    const AttendArgs& a = t.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sm = (smem_u32(smraw) + 1023u) & ~1023u;
+    const uint32_t ring = sm + 2 * C::kTileBytes;
+
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < kSt; ++s) {
+            mb_init(smem_u32(&s_full[s]), 1);
+            mb_init(smem_u32(&s_empty[s]), 1);
+        }
+        mb_init(smem_u32(&s_qfull), 1);
+        mb_init(smem_u32(&s_qempty), 1);
+        mb_init(smem_u32(&s_tail), 1);
+        for (int i = 0; i < 2; ++i) {
+            mb_init(smem_u32(&s_sfull[i]), 1);
+            mb_init(smem_u32(&s_pfull[i]), kM);
+            mb_init(smem_u32(&s_ofull[i]), 1);
+        }
+        s_bad = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tm_before();
+    __syncthreads();
+    tm_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* bad = &s_bad;
+    pdl_trigger();
+    pdl_wait();
+
+    const int G = a.H / a.Hkv;
+    const int per_g = G * t.nq;                                    // query tiles of a (b, g)
+    struct Item {
+        int b, g, len, tiles, first, two;
+    };
+    auto item = [&](int64_t w) {
+        Item it;
+        const int64_t bg = w / t.pairs;
+        it.b = (int)(bg / a.Hkv);
+        it.g = (int)(bg - (int64_t)it.b * a.Hkv);
+        it.first = (int)(w - bg * t.pairs) * 2;
+        it.two = it.first + 1 < per_g;
+        it.len = min(max(a.len ? __ldcg(a.len + it.b) : a.max_len, 0), a.max_len);
+        it.tiles = (it.len + kN - 1) / kN;
+        return it;
+    };
+
+    if (warp >= kSoftWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == kLoadWarp) {
+        // ------------------------------------------------ loads (lane 0), and zeros behind a row's last position
+        uint32_t n = 0, nq = 0, tail_n = 0;                        // tiles loaded, items; the last zeroed tile's number
+        bool tails = false;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
+            const Item it = item(w);
+            if (!it.tiles) continue;
+            if (nq > 0) ok = warp_wait(smem_u32(&s_qempty), (nq - 1) & 1, bad);
+            if (!ok) break;
+            if (lane == 0) {
+                mb_expect(smem_u32(&s_qfull), (it.two ? 2 : 1) * C::kTileBytes);
+                for (int i = 0; i <= it.two; ++i) {
+                    const int x = it.first + i, h = it.g * G + x / t.nq, r = (x % t.nq) * kM;
+                    for (int p = 0; p < HD / 64; ++p)
+                        tma4(sm + i * C::kTileBytes + p * C::kPanel, &t.q, p * 64, h, r, it.b, smem_u32(&s_qfull));
+                }
+            }
+            ++nq;
+            for (int j = 0; j < 2 * it.tiles && ok; ++j, ++n) {
+                const uint32_t s = n % kSt, turn = n / kSt;
+                if (turn > 0) ok = warp_wait(smem_u32(&s_empty[s]), (turn - 1) & 1, bad);
+                if (!ok) break;
+                const uint32_t dst = ring + s * C::kTileBytes, mb = smem_u32(&s_full[s]);
+                if (lane == 0) {
+                    mb_expect(mb, C::kTileBytes);
+                    for (int p = 0; p < HD / 64; ++p)
+                        tma4(dst + p * C::kPanel, (j & 1) ? &t.v : &t.k, p * 64, it.g, (j >> 1) * kN, it.b, mb);
+                }
+                const int rest = it.len - (it.tiles - 1) * kN;
+                if (j == 2 * it.tiles - 1 && rest < kN) {
+                    // values behind the row's last position: 0 x anything must be 0
+                    ok = warp_wait(mb, turn & 1, bad);
+                    // one tail at a time: the products of the one before are complete (if its stage was loaded
+                    // again since, that has been waited for)
+                    if (ok && tails && tail_n + kSt > n)
+                        ok = warp_wait(smem_u32(&s_empty[tail_n % kSt]), (tail_n / kSt) & 1, bad);
+                    if (!ok) { ++n; break; }
+                    for (int x = lane; x < (kN - rest) * 8 * (HD / 64); x += 32) {
+                        const int p = x / ((kN - rest) * 8), y = x - p * (kN - rest) * 8;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * C::kPanel + rest * 128 + y * 16), "r"(0) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(smem_u32(&s_tail));
+                    tails = true;
+                    tail_n = n;
+                }
+            }
+        }
+        if (!ok) {                                                 // bounded: this block's own copies
+            for (uint32_t x = n > kSt ? n - kSt : 0; x < n; ++x) {
+                const long long t0 = clock64();
+                while (!mb_try(smem_u32(&s_full[x % kSt]), (x / kSt) & 1) && clock64() - t0 < kWaitClocks) {}
+            }
+            if (nq > 0) {
+                const long long t0 = clock64();
+                while (!mb_try(smem_u32(&s_qfull), (nq - 1) & 1) && clock64() - t0 < kWaitClocks) {}
+            }
+        }
+      } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            // -------------------------------------------- products
+            uint32_t n = 0, nq = 0, ntail = 0, np[2] = {0, 0}, no[2] = {0, 0};
+            bool ok = true, any = false;
+            for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
+                const Item it = item(w);
+                if (!it.tiles) continue;
+                ok = mb_wait(smem_u32(&s_qfull), nq & 1, bad) && mb_wait(smem_u32(&s_full[n % kSt]), (n / kSt) & 1, bad);
+                if (!ok) break;
+                ++nq;
+                tm_after();
+                auto scores = [&](int i, uint32_t stage) {
+                    const uint32_t q0 = sm + i * C::kTileBytes, k0 = ring + stage * C::kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        const uint32_t off = (k / 4) * C::kPanel + (k % 4) * 32;
+                        mma_ss(tmem + i * kN, sdesc(q0 + off, 16), sdesc(k0 + off, 16), kIdescS, k > 0);
+                    }
+                    commit(smem_u32(&s_sfull[i]));
+                    any = true;
+                };
+                for (int i = 0; i <= it.two; ++i) scores(i, n % kSt);
+                commit(smem_u32(&s_empty[n % kSt]));
+                if (it.tiles == 1) commit(smem_u32(&s_qempty));
+                ++n;
+                const bool tail = it.len % kN != 0;
+                for (int j = 0; j < it.tiles && ok; ++j) {
+                    const uint32_t sv = n % kSt, pv = (n / kSt) & 1, sk = (n + 1) % kSt, pk = ((n + 1) / kSt) & 1;
+                    const bool more = j + 1 < it.tiles;
+                    ok = mb_wait(smem_u32(&s_full[sv]), pv, bad);
+                    if (ok && !more && tail) ok = mb_wait(smem_u32(&s_tail), ntail++ & 1, bad);
+                    for (int i = 0; i <= it.two && ok; ++i) {
+                        ok = mb_wait(smem_u32(&s_pfull[i]), np[i] & 1, bad);
+                        if (!ok) break;
+                        ++np[i];
+                        tm_after();
+                        const uint32_t v0 = ring + sv * C::kTileBytes;
+#pragma unroll
+                        for (int k = 0; k < kN / 16; ++k)
+                            mma_ts(tmem + C::kO + i * HD, tmem + i * kN + k * 8, sdesc(v0 + k * 2048, C::kPanel), kIdescO, j > 0 || k > 0);
+                        if (more) {
+                            if (i == 0) ok = mb_wait(smem_u32(&s_full[sk]), pk, bad);
+                            if (!ok) break;
+                            scores(i, sk);
+                        } else {
+                            commit(smem_u32(&s_ofull[i]));
+                            ++no[i];
+                        }
+                    }
+                    if (!ok) break;
+                    commit(smem_u32(&s_empty[sv]));
+                    ++n;
+                    if (more) {
+                        commit(smem_u32(&s_empty[sk]));
+                        ++n;
+                        if (j + 2 == it.tiles) commit(smem_u32(&s_qempty));
+                    }
+                }
+            }
+            if (!ok && any) {                                      // bounded: products in flight
+                commit(smem_u32(&s_ofull[0]));
+                const long long t0 = clock64();
+                while (!mb_try(smem_u32(&s_ofull[0]), no[0] & 1) && clock64() - t0 < kWaitClocks) {}
+            }
+        }
+        __syncwarp();
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // ------------------------------------------------ softmax: a thread per query
+        const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + i * kN, to = tmem + lanes + C::kO + i * HD;
+        const float sl = a.scale * kLog2e;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
+            const Item it = item(w);
+            if (i && !it.two) continue;
+            const int x = it.first + i, h = it.g * G + x / t.nq, qi = (x % t.nq) * kM + r;
+            float m = -INFINITY, ref = 0.f, l = 0.f;
+            for (int j = 0; j < it.tiles; ++j) {
+                ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
+                if (!ok) break;
+                ++ns;
+                tm_after();
+                float s[kN];
+#pragma unroll
+                for (int c = 0; c < kN; c += 32) tm_ld32(ts + c, s + c);
+                tm_wait_ld();
+#pragma unroll
+                for (int c = 0; c < kN; c += 16) after_wait(s + c);
+                const int rest = it.len - j * kN;
+                if (rest < kN) {
+#pragma unroll
+                    for (int c = 0; c < kN; ++c) s[c] = c < rest ? s[c] : -INFINITY;
+                }
+                float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+                for (int c = 4; c < kN; c += 4) {
+                    m0 = fmaxf(m0, s[c]);
+                    m1 = fmaxf(m1, s[c + 1]);
+                    m2 = fmaxf(m2, s[c + 2]);
+                    m3 = fmaxf(m3, s[c + 3]);
+                }
+                const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
+                const bool grow = mx > (m == -INFINITY ? -INFINITY : m + kSlack);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
+                    if (grow) m = mx;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < HD; c += 16) {
+                            float o[16];
+                            tm_ld16(to + c, o);
+                            tm_wait_ld();
+                            after_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
+                        }
+                        tm_wait_st();
+                    }
+                    ref = m == -INFINITY ? 0.f : m - kShift;
+                }
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < kN; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float p0 = ex2(fmaf(s[c + 2 * e], sl, -ref)), p1 = ex2(fmaf(s[c + 2 * e + 1], sl, -ref));
+                        l0 += p0;
+                        l1 += p1;
+                        p[e] = pack2<BF>(p0, p1);
+                    }
+                    tm_st16(ts + c / 2, p);
+                }
+                l += l0 + l1;
+                tm_wait_st();
+                tm_before();
+                mb_arrive(smem_u32(&s_pfull[i]));
+            }
+            if (!ok) break;
+            // ---- the result
+            float inv = 0.f;
+            if (it.tiles) {
+                ok = warp_wait(smem_u32(&s_ofull[i]), no & 1, bad);
+                if (!ok) break;
+                ++no;
+                tm_after();
+                inv = 1.f / l;
+            }
+            uint16_t* out = static_cast<uint16_t*>(a.out) + it.b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD;
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+                float o[16];
+                if (it.tiles) {
+                    tm_ld16(to + c, o);
+                    tm_wait_ld();
+                    after_wait(o);
+                }
+                if (qi < a.Lq) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            u[y] = l == 0.f ? 0u : pack2<BF>(o[e + 2 * y] * inv, o[e + 2 * y + 1] * inv);
+                        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                }
+            }
+            tm_before();
+            if (a.lse && qi < a.Lq)
+                a.lse[((int64_t)it.b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+        }
+    }
+    tm_before();
+    __syncthreads();
+    tm_after();
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (tid == 0 && s_bad) *a.err = SD_ERR_TIMEOUT;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (EncodeFn) nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// [batch][row][head][hd] of 16-bit elements by strides: boxes of 128 rows of 64 elements of one head
+bool map4(CUtensorMap* map, bool bf, const void* base, int hd, int heads, int rows, int batch, int64_t head_stride,
+          int64_t row_stride, int64_t batch_stride) {
+    EncodeFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
+    // the stride of a dimension of one element is not used: any legal value
+    const cuuint64_t strides[3] = {heads > 1 ? (cuuint64_t)head_stride * 2 : (cuuint64_t)hd * 2,
+                                   rows > 1 ? (cuuint64_t)row_stride * 2 : (cuuint64_t)hd * 2,
+                                   batch > 1 ? (cuuint64_t)batch_stride * 2 : (cuuint64_t)hd * 2};
+    const cuuint32_t box[4] = {64, 1, 128, 1}, one[4] = {1, 1, 1, 1};
+    return enc(map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims,
+               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, bool BF>
+cudaError_t launch_tc(const TcArgs& t, int grid, cudaStream_t st) {
+    return launch_k(k_attend_tc<HD, BF>, dim3(grid), dim3(kThreads), Cfg<HD>::kSmem, st, t);
+}
+template <int HD, bool BF>
+cudaError_t prepare_tc() {
+    return cudaFuncSetAttribute(k_attend_tc<HD, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t prepare_attend_tc() {
+    cudaError_t e = prepare_tc<64, false>();
+    if (e == cudaSuccess) e = prepare_tc<128, false>();
+    if (e == cudaSuccess) e = prepare_tc<64, true>();
+    if (e == cudaSuccess) e = prepare_tc<128, true>();
+    return e;
+}
+
+// *taken false: strides that a tensor map cannot hold, nothing launched
+cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t st, bool* taken) {
+    TcArgs t;
+    const bool bf = a.dtype == SD_BF16;
+    *taken = map4(&t.q, bf, a.q, hd, a.H, a.Lq, a.B, hd, a.q_stride, a.q_batch) &&
+             map4(&t.k, bf, a.k, hd, a.Hkv, a.max_len, a.B, a.head_stride, a.pos_stride, a.batch_stride) &&
+             map4(&t.v, bf, a.v, hd, a.Hkv, a.max_len, a.B, a.head_stride, a.pos_stride, a.batch_stride);
+    if (!*taken) return cudaSuccess;
+    t.a = a;
+    t.nq = (a.Lq + kM - 1) / kM;
+    const int64_t pairs = ((int64_t)(a.H / a.Hkv) * t.nq + 1) / 2;
+    t.pairs = (int32_t)pairs;
+    t.items = (int64_t)a.B * a.Hkv * pairs;
+    const int grid = (int)std::min<int64_t>(sms, t.items);
+    if (hd == 64) return bf ? launch_tc<64, true>(t, grid, st) : launch_tc<64, false>(t, grid, st);
+    return bf ? launch_tc<128, true>(t, grid, st) : launch_tc<128, false>(t, grid, st);
+}
+
+}  // namespace sd
