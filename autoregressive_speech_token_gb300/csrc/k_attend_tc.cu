@@ -101,13 +101,36 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead) {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lead >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
            (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
+// One product; A, B (descriptors) and the tensor-memory address of P advance by constants inside the
+// statement, so that the issuing thread keeps one base of each in registers.
+template <int kAdvA, int kAdvB>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; add.s64 x, %1, %5; add.s64 y, %2, %6; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kAdvA), "n"(kAdvB) : "memory");
 }
+template <int kAdvA, int kAdvB>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{ .reg .pred p; .reg .b64 y; .reg .b32 x; setp.ne.b32 p, %4, 0; add.s32 x, %1, %5; add.s64 y, %2, %6; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p; }"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(kAdvA), "n"(kAdvB) : "memory");
+}
+// S = Q K^T: 16 columns of the head a step, 32 bytes within a 64-column panel
+template <int HD, int kPanel, int K = 0>
+__device__ __forceinline__ void score_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    if constexpr (K < HD / 16) {
+        constexpr int kAdv = (K / 4) * (kPanel >> 4) + (K % 4) * 2;
+        mma_ss<kAdv, kAdv>(d, a, b, idesc, K > 0);
+        score_steps<HD, kPanel, K + 1>(d, a, b, idesc);
+    }
+}
+// O += P V: 16 positions a step, 8 columns of P, 16 rows of V
+template <int K, int kEnd>
+__device__ __forceinline__ void result_steps(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (K < kEnd) {
+        mma_ts<K * 8, K * (2048 >> 4)>(d, a, b, idesc, acc);
+        result_steps<K + 1, kEnd>(d, a, b, idesc, 1);
+    }
 }
 __device__ __forceinline__ void commit(uint32_t mb) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mb) : "memory");
@@ -152,6 +175,27 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     if constexpr (BF) {
@@ -173,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
     constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     extern __shared__ unsigned char smraw[];
-    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_ofull[2], s_tail;
+    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_tail;
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad;
     const AttendArgs& a = t.a;
@@ -195,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
         mb_init(smem_u32(&s_tail), 1);
         for (int i = 0; i < 2; ++i) {
             mb_init(smem_u32(&s_sfull[i]), 1);
-            mb_init(smem_u32(&s_pfull[i]), kM);
+            mb_init(smem_u32(&s_pfull[i][0]), kM / 32);
+            mb_init(smem_u32(&s_pfull[i][1]), kM / 32);
             mb_init(smem_u32(&s_ofull[i]), 1);
         }
         s_bad = 0;
@@ -291,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
       } else if (warp == kMmaWarp) {
         if (lane == 0) {
             // -------------------------------------------- products
+            // descriptors: a tile or a K step further is an addition (addresses / 16 stay within their 14 bits)
+            const uint64_t qdesc = sdesc(sm, 16), kdesc = sdesc(ring, 16), vdesc = sdesc(ring, C::kPanel);
             uint32_t n = 0, nq = 0, ntail = 0, np[2] = {0, 0}, no[2] = {0, 0};
             bool ok = true, any = false;
             for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
@@ -301,12 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                 ++nq;
                 tm_after();
                 auto scores = [&](int i, uint32_t stage) {
-                    const uint32_t q0 = sm + i * C::kTileBytes, k0 = ring + stage * C::kTileBytes;
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        const uint32_t off = (k / 4) * C::kPanel + (k % 4) * 32;
-                        mma_ss(tmem + i * kN, sdesc(q0 + off, 16), sdesc(k0 + off, 16), kIdescS, k > 0);
-                    }
+                    const uint64_t q = qdesc + (uint32_t)(i * (C::kTileBytes >> 4)), kd = kdesc + stage * (uint32_t)(C::kTileBytes >> 4);
+score_steps<HD, C::kPanel>(tmem + i * kN, q, kd, kIdescS);
                     commit(smem_u32(&s_sfull[i]));
                     any = true;
                 };
@@ -321,14 +364,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                     ok = mb_wait(smem_u32(&s_full[sv]), pv, bad);
                     if (ok && !more && tail) ok = mb_wait(smem_u32(&s_tail), ntail++ & 1, bad);
                     for (int i = 0; i <= it.two && ok; ++i) {
-                        ok = mb_wait(smem_u32(&s_pfull[i]), np[i] & 1, bad);
+                        // the products of P's first half begin while its second half is formed
+                        const uint64_t vd = vdesc + sv * (uint32_t)(C::kTileBytes >> 4);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            ok = mb_wait(smem_u32(&s_pfull[i][half]), np[i] & 1, bad);
+                            if (!ok) break;
+                            tm_after();
+const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
+                            if (half == 0) result_steps<0, kN / 32>(o, p, vd, kIdescO, j > 0);
+                            else result_steps<kN / 32, kN / 16>(o, p, vd, kIdescO, 1);
+                        }
                         if (!ok) break;
                         ++np[i];
-                        tm_after();
-                        const uint32_t v0 = ring + sv * C::kTileBytes;
-#pragma unroll
-                        for (int k = 0; k < kN / 16; ++k)
-                            mma_ts(tmem + C::kO + i * HD, tmem + i * kN + k * 8, sdesc(v0 + k * 2048, C::kPanel), kIdescO, j > 0 || k > 0);
                         if (more) {
                             if (i == 0) ok = mb_wait(smem_u32(&s_full[sk]), pk, bad);
                             if (!ok) break;
@@ -388,13 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                 }
                 float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-                for (int c = 4; c < kN; c += 4) {
-                    m0 = fmaxf(m0, s[c]);
-                    m1 = fmaxf(m1, s[c + 1]);
-                    m2 = fmaxf(m2, s[c + 2]);
-                    m3 = fmaxf(m3, s[c + 3]);
+                for (int c = 4; c + 8 <= kN; c += 8) {
+                    m0 = max3(m0, s[c], s[c + 1]);
+                    m1 = max3(m1, s[c + 2], s[c + 3]);
+                    m2 = max3(m2, s[c + 4], s[c + 5]);
+                    m3 = max3(m3, s[c + 6], s[c + 7]);
                 }
-                const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl;
+                m0 = max3(m0, s[kN - 4], s[kN - 3]);
+                m1 = max3(m1, s[kN - 2], s[kN - 1]);
+                const float mx = fmaxf(max3(m0, m1, m2), m3) * sl;
                 const bool grow = mx > (m == -INFINITY ? -INFINITY : m + kSlack);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
@@ -415,23 +465,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                     }
                     ref = m == -INFINITY ? 0.f : m - kShift;
                 }
-                float l0 = 0.f, l1 = 0.f;
+                float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+                const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(-ref, -ref);
 #pragma unroll
                 for (int c = 0; c < kN; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(s[c + 2 * e], sl, -ref)), p1 = ex2(fmaf(s[c + 2 * e + 1], sl, -ref));
-                        l0 += p0;
-                        l1 += p1;
-                        p[e] = pack2<BF>(p0, p1);
+                        float2 x = fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, ref2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        if (e & 1) l1 = add2(l1, x); else l0 = add2(l0, x);
+                        p[e] = pack2<BF>(x.x, x.y);
                     }
                     tm_st16(ts + c / 2, p);
+                    if (c == kN / 2 - 32 || c == kN - 32) {
+                        tm_wait_st();
+                        tm_before();
+                        __syncwarp();
+                        if (lane == 0) mb_arrive(smem_u32(&s_pfull[i][c == kN - 32]));
+                    }
                 }
-                l += l0 + l1;
-                tm_wait_st();
-                tm_before();
-                mb_arrive(smem_u32(&s_pfull[i]));
+                l += (l0.x + l0.y) + (l1.x + l1.y);
             }
             if (!ok) break;
             // ---- the result
