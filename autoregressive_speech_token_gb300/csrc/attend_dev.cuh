@@ -1,5 +1,7 @@
 // Shared by the kernels behind sd_attend_pages and sd_attend_cross.
 #pragma once
+#include <cuda.h>
+
 #include "pages_dev.cuh"
 
 // Partial results of the split kernel: two records a block, one arrival counter.
@@ -27,7 +29,6 @@ struct AttendArgs {
     int *cnt, *err;
 };
 
-constexpr int kSplitBlocksPerSm = 2;                              // at most
 constexpr int kSplitRows = 8;                                     // query rows of a unit
 constexpr int kSplitRecord = kSplitRows * (128 + 2);              // floats of a partial record
 
@@ -37,5 +38,73 @@ cudaError_t prepare_attend_split();                               // shared-memo
 cudaError_t prepare_attend_tc();
 cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t st, bool* taken);
 cudaError_t launch_attend_split(const AttendArgs& a, int hd, int sms, cudaStream_t st);
+
+// ---- device side
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr long long kWaitClocks = 4000000000ll;                   // about two seconds
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mb_init(uint32_t mb, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mb_expect(uint32_t mb, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mb_arrive(uint32_t mb) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory");
+}
+__device__ __forceinline__ bool mb_try(uint32_t mb, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(mb), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Bounded; gives up early once another warp of the block has given up.
+__device__ __forceinline__ bool mb_wait_slow(uint32_t mb, uint32_t parity, volatile int* bad) {
+    const long long t0 = clock64();
+    while (!mb_try(mb, parity)) {
+        if (*bad) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            *bad = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+    return mb_try(mb, parity) || mb_wait_slow(mb, parity, bad);
+}
+// The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+    return __all_sync(0xffffffffu, mb_wait(mb, parity, bad));
+}
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int h, int r, int b, uint32_t mb) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(r), "r"(b), "r"(mb) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---- tensor maps
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeFn tensor_map_encoder() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (EncodeFn) nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
 
 }  // namespace sd

@@ -3,33 +3,44 @@
 //
 // A unit is (row b, kv head g, tile of up to 8 query rows of that head's group);
 // a row is (query i, head of the group).  Its positions are cut into tiles of
-// 64 or 128, and the tiles of all units, laid end to end, are dealt evenly to the
+// 128 or 256, and the tiles of all units, laid end to end, are dealt evenly to the
 // resident blocks: every block streams the same number of bytes whatever the
 // lengths are, and no host needs to know them.  A unit that ends up in several
 // blocks is joined by the last of them to arrive, in block order (results do not
 // depend on the order of arrival).
 //
-// The kernel is bound by the key and value bytes.  Each of a block's four warps
-// streams its own 16 or 32 positions of a tile through a ring of cp.async stages and
-// keeps its own running maximum and sum, so that the loop has no block-wide
-// barrier.  Scores are mma.sync products (m16n8k16): a decode step's 8 rows fill
-// half of the 16 rows of the instruction, and the other half holds the rows'
-// low-order parts, so q (fp32 as fp16 high + low) and the probabilities enter with
-// twice the bits at no further instruction.  (tcgen05 needs 64 or 128 rows, of
-// which 1 to 8 would hold work, while the tensor time here is a fraction of
-// the memory time.)
+// The kernel is bound by the key and value bytes.  Three warps walk the block's share
+// and load by TMA, in turn, a tile's keys and values (32 KB each) into a ring, running
+// ahead across the ends of units; a fourth prepares the units (where they lie, their queries).
+// Eight warps work on a tile, 16 or 32 positions each, with a running maximum and sum of
+// their own; four more merge and write a unit's result while the eight are at the next
+// one (merging in their place cost about 3 us a unit).  Positions behind a length or in a page
+// that is not there are masked; their values are set to 0 in shared memory, so that
+// what they hold does not matter.
+//
+// Scores are mma.sync products (m16n8k16): a decode step's 8 rows fill half of the
+// 16 rows of the instruction, and the other half holds the rows' low-order parts, so q
+// (fp32 as fp16 high + low) and the probabilities enter with twice the bits at no further
+// instruction.  (tcgen05 needs 64 or 128 rows, of which 1 to 8 would hold work, while
+// the tensor time here is a fraction of the memory time.)
 #include "attend_dev.cuh"
 
 namespace sd {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 8, kLoaders = 3, kMergers = kSplitRows / 2, kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32 * (kLoaders + 1 + kMergers);
+// Registers of a thread: 512 x 128 at launch = 256 x 176 + 256 x 80
+constexpr int kConsumerRegs = 176, kOtherRegs = 80;
+static_assert(kLoaders + 1 == 4 && kMergers == 4, "warpgroups");
+static_assert(kConsumers * kConsumerRegs + (kThreads - kConsumers) * kOtherRegs <= kThreads * 128, "the shares exceed what the block was launched with");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
+struct alignas(128) SplitArgs {
+    CUtensorMap k, v;
+    AttendArgs a;
+    int32_t box, groups;      // positions of a box (all of one page), boxes of a tile's keys or values and column part
+};
+
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t* r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -48,11 +59,6 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 // two e4m3 values (a 16-bit half of w) as fp16x2: exact
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t w) {
@@ -81,6 +87,17 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
+template <bool BF>
+__device__ __forceinline__ uint32_t round2(float x, float y) {
+    uint32_t hi, lo;
+    split2<BF>(x, y, hi, lo);
+    return hi;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 // high and low product; an infinite high product has no low one (0 * inf)
 __device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? hi + lo : hi; }
 
@@ -89,195 +106,472 @@ __device__ __forceinline__ float2 load2(const void* p, int64_t i, int dt) {
     if (dt == SD_F16) return __half22float2(*reinterpret_cast<const __half2*>(static_cast<const __half*>(p) + i));
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(p) + i));
 }
-__device__ __forceinline__ void store1(void* p, int64_t i, int dt, float v) {
-    if (dt == SD_F32) static_cast<float*>(p)[i] = v;
-    else if (dt == SD_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+// N (2 or 4) consecutive elements
+template <int N>
+__device__ __forceinline__ void storev(void* p, int64_t i, int dt, const float* v) {
+    if (dt == SD_F32) {
+#pragma unroll
+        for (int x = 0; x < N; x += 2) *reinterpret_cast<float2*>(static_cast<float*>(p) + i + x) = make_float2(v[x], v[x + 1]);
+    } else {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int x = 0; x < N; x += 2) w[x / 2] = dt == SD_F16 ? round2<false>(v[x], v[x + 1]) : round2<true>(v[x], v[x + 1]);
+        uint16_t* q = static_cast<uint16_t*>(p) + i;
+        if constexpr (N == 4) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(q) = w[0];
+    }
 }
+
+constexpr int kUnits = 4;                             // units prepared ahead
+constexpr int kMinTiles = 2;                          // of a part of a unit, where blocks are not short
 
 template <int HD, int KV>
 struct Shape {
     static constexpr bool kBf = KV == SD_BF16, kE4 = KV == SD_E4M3;
     static constexpr int kRow = HD * (kE4 ? 1 : 2);             // bytes of a position's row
     static constexpr int kCols = kRow / 16;                     // 16-byte columns
-    static constexpr int kChunk = kRow >= 256 ? 16 : 32;        // positions of a warp's step: independent products hide
-    static constexpr int kTile = kChunk * kWarps;               // each other's latency, registers allow 16 rows of 256 bytes
-    static constexpr int kStage = 2 * kChunk * kRow;            // K and V of a step
-    static constexpr int kStages = kStage >= 8192 ? 3 : 5;
-    // What beginning and ending a unit costs (about 4 us), in tiles: the share of a block counts it
-    static constexpr int kLead = 96 * 1024 / (kWarps * kStage);
-    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kPart = kRow < 128 ? kRow : 128;       // bytes of a row in a box
+    static constexpr int kParts = kRow / kPart;                 // 2 for 256-byte rows
+    static constexpr int kChunk = kRow >= 256 ? 16 : 32;        // positions of a warp
+    static constexpr int kTile = kChunk * kWarps;
+    static constexpr int kStage = kTile * kRow;                 // the keys, or the values, of a tile
     static constexpr int kMerge = kWarps * kSplitRows * (HD + 2) * 4;
-    static constexpr int kSmem = kRing + kMerge;
+    static constexpr int kQueries = kSplitRows * HD * 4;        // a unit's queries, in their own type
+    static constexpr int kStages = kStage >= 32768 ? 5 : 10;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kSmem = kRing + kMerge + kUnits * kQueries + 1024;
+    // What beginning and ending a unit costs, in tiles: the share of a block counts it
+    static constexpr int kLead = 1;
     // fp16 probabilities are kept as 2^15 p: the smallest ones stay above fp16's subnormal step
     static constexpr float kShift = kBf ? 0.f : 15.f;
-    // column of a row in shared memory: the 8 rows of a matrix fall into 8 different 16-byte bank groups
+    // byte of a 16-byte column of a row: the boxes' swizzle puts the 8 rows of a matrix into 8 different bank groups
     static __device__ __forceinline__ uint32_t at(int row, int col) {
-        return row * kRow + ((kCols >= 8 ? col ^ (row & 7) : col ^ ((row >> 1) & 3)) << 4);
+        if constexpr (kRow == 64) return row * 64 + ((col ^ ((row >> 1) & 3)) << 4);
+        return (col >> 3) * (kTile * 128) + row * 128 + (((col & 7) ^ (row & 7)) << 4);
     }
 };
 
+// What the warps on a unit need to know: m0 its first query row, steps its tiles in this block
+struct Unit {
+    int64_t m0;
+    int b, g, len, rows, i0, tiles, c_lo, c_hi, begins;
+};
+
 template <int HD, int KV>
-__global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_constant__ SplitArgs args) {
     using S = Shape<HD, KV>;
-    constexpr int kSteps = HD / 16, kOut = HD / 8, kSt = S::kStages, kChunk = S::kChunk, kTile = S::kTile;
-    pdl_trigger();
-    pdl_wait();
-    extern __shared__ __align__(128) unsigned char smem[];
-    float* s_o = reinterpret_cast<float*>(smem + S::kRing);              // [warp][row][HD]
-    float* s_m = s_o + kWarps * kSplitRows * HD;                          // [warp][row]
-    float* s_l = s_m + kWarps * kSplitRows;
-    __shared__ int64_t s_sum[kWarps];
+    constexpr int kSteps = HD / 16, kOut = HD / 8, kChunk = S::kChunk, kTile = S::kTile, kSt = S::kStages;
+    const AttendArgs& a = args.a;
+    extern __shared__ unsigned char smraw[];
+    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt];
+    __shared__ __align__(8) unsigned long long s_ufull[kUnits], s_uempty[kUnits], s_done, s_free;
+    __shared__ uint32_t s_live[kSt][kWarps];
+    __shared__ Unit s_unit[kUnits];
+    __shared__ int64_t s_sum[kThreads / 32];
     __shared__ int64_t s_base;
-    __shared__ int s_b, s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = lane >> 2, quad = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * kSt * S::kStage;
+    __shared__ int s_len[kThreads];
+    __shared__ int s_b, s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char* smem = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    const uint32_t ring = smem_u32(smem);
     const int G = a.H / a.Hkv;
     const int64_t M = (int64_t)a.Lq * G;                                  // query rows of a (b, kv head)
     const int64_t RT = (M + kSplitRows - 1) / kSplitRows;
     const int64_t U = RT * a.Hkv;                                         // units of a row b
+    volatile int* bad = &s_bad;
 
+    if (tid == kConsumers) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&args.k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&args.v)) : "memory");
+        for (int s = 0; s < kSt; ++s) {
+            mb_init(smem_u32(&s_full[s]), 1);
+            mb_init(smem_u32(&s_empty[s]), kWarps);
+        }
+        mb_init(smem_u32(&s_done), kWarps);
+        mb_init(smem_u32(&s_free), kMergers);
+        for (int s = 0; s < kUnits; ++s) {
+            mb_init(smem_u32(&s_ufull[s]), 1);
+            mb_init(smem_u32(&s_uempty[s]), kWarps + kMergers);
+        }
+        s_bad = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_trigger();
+    pdl_wait();
+
+    const bool few = a.B <= 32;                                           // a lane for each row, in every warp
     auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
-    // tiles of a unit, the first kLead of them empty
-    auto tiles = [&](int len) { return (len + kTile - 1) / kTile + S::kLead; };
+    auto tiles = [&](int len) { return (len + kTile - 1) / kTile; };
 
-    // ---- this block's share of all tiles
-    int64_t mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) mine += tiles(length(b));
-    // inclusive sums over the threads: of a row each where B <= kThreads
-    int64_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-    }
-    if (lane == 31) s_sum[warp] = sum;
-    __syncthreads();
-    int64_t T = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) sum += s_sum[w];
-        T += s_sum[w];
-    }
-    T *= U;
-    const int64_t per = max(quot(T + gridDim.x - 1, gridDim.x), (int64_t)1);
-    const int64_t t_begin = blockIdx.x * per, t_end = min(T, t_begin + per);
-    if (t_begin >= t_end) return;
-    // the row b that holds tile t_begin, and the first tile of that row
-    if (a.B <= kThreads) {
-        if ((sum - mine) * U <= t_begin && t_begin < sum * U) {
-            s_b = tid;
-            s_base = (sum - mine) * U;
+    // ---- this block's share.  Where every unit can have a block of its own, units are cut into parts of `per` tiles
+    // with a block each, per = (all tiles) / (blocks left over by whole units): no unit is cut without need, since
+    // joining costs about 3 us.  Otherwise all tiles, kLead empty ones before each unit, are dealt out evenly.
+    const int64_t grid = gridDim.x;
+    const int len0 = few && lane < a.B ? length(lane) : 0;
+    const bool whole = few && a.B * U <= grid;
+    const int lead = whole ? 0 : S::kLead;
+    int64_t per = 1;
+    // tiles of a unit with the empty ones before it, or behind it to a multiple of `per`
+    auto padded = [&](int n) -> int { return whole ? (int)(quot(max(n, 1) + per - 1, per) * per) : n + S::kLead; };
+    int64_t t, base, T;                                                   // next tile; first tile of row b_at
+    int b_at;
+    if (few) {
+        const int n = tiles(len0);
+        if (whole) {
+            const int64_t all = (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)n) * U, left = grid - a.B * U;
+            per = max(__reduce_max_sync(0xffffffffu, n), 1);
+            if (left > 0) per = min(per, max(quot(all + left - 1, left), (int64_t)kMinTiles));
         }
+        const int64_t mine = lane < a.B ? padded(n) : 0;
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        T = __shfl_sync(0xffffffffu, sum, 31) * U;
+        if (!whole) per = max(quot(T + grid - 1, grid), (int64_t)1);
+        t = blockIdx.x * per;
+        const uint32_t here = __ballot_sync(0xffffffffu, (sum - mine) * U <= t && t < sum * U);
+        b_at = __ffs(here) - 1;
+        base = __shfl_sync(0xffffffffu, (sum - mine) * U, b_at & 31);
     } else {
-        for (int64_t b0 = 0, before = 0; b0 < a.B; b0 += kThreads) {
-            const int64_t b = b0 + tid;
-            const int64_t n = b < a.B ? tiles(length((int)b)) * U : 0;
-            int64_t x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            __syncthreads();
-            if (lane == 31) s_sum[warp] = x;
-            __syncthreads();
-            int64_t base = before;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) base += s_sum[w];
-                before += s_sum[w];
-            }
-            if (n && base + x - n <= t_begin && t_begin < base + x) {
-                s_b = (int)b;
-                s_base = base + x - n;
-            }
-            if (before > t_begin) break;
+        // inclusive sums over the threads: of a row each where there are no more rows than threads
+        int64_t mine = 0;
+        for (int b = tid; b < a.B; b += kThreads) {
+            const int len = length(b);
+            if (b < kThreads) s_len[b] = len;
+            mine += padded(tiles(len));
         }
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) s_sum[warp] = sum;
+        __syncthreads();
+        T = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) sum += s_sum[w];
+            T += s_sum[w];
+        }
+        T *= U;
+        per = max(quot(T + grid - 1, grid), (int64_t)1);
+        t = blockIdx.x * per;
+        if (t >= T) return;
+        // the row that holds tile t, and its first tile
+        if (a.B <= kThreads) {
+            if ((sum - mine) * U <= t && t < sum * U) {
+                s_b = tid;
+                s_base = (sum - mine) * U;
+            }
+        } else {
+            for (int64_t b0 = 0, before = 0; b0 < a.B; b0 += kThreads) {
+                const int64_t b = b0 + tid;
+                const int64_t n = b < a.B ? padded(tiles(length((int)b))) * U : 0;
+                int64_t x = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                __syncthreads();
+                if (lane == 31) s_sum[warp] = x;
+                __syncthreads();
+                int64_t at = before;
+                for (int w = 0; w < kThreads / 32; ++w) {
+                    if (w < warp) at += s_sum[w];
+                    before += s_sum[w];
+                }
+                if (n && at + x - n <= t && t < at + x) {
+                    s_b = (int)b;
+                    s_base = at + x - n;
+                }
+                if (before > t) break;
+            }
+        }
+        __syncthreads();
+        b_at = s_b;
+        base = s_base;
     }
-    __syncthreads();
-    int b = s_b;
-    int64_t base = s_base;                                                // first tile of row b
+    if (t >= T) return;
+    const int64_t t_begin = t, t_end = min(T, t + per);
+    __syncthreads();                                                      // the barriers are initialised
 
-    for (int64_t t = t_begin; t < t_end;) {
-        const int len = length(b);
-        const int nt = tiles(len);
-        const int64_t in_b = t - base;
-        const int64_t u = quot(in_b, nt);
-        const int64_t u0 = base + u * nt;                                  // the unit's tiles [u0, u0 + nt)
+    // The units of this block in turn.
+    auto next_unit = [&](Unit& p) -> bool {
+        if (t >= t_end) return false;
+        p.b = b_at;
+        p.len = few ? __shfl_sync(0xffffffffu, len0, b_at) : b_at < kThreads ? s_len[b_at] : length(b_at);
+        const int real_tiles = tiles(p.len), nt = padded(real_tiles);
+        const int64_t u = quot(t - base, nt), u0 = base + u * nt;        // the unit's tiles [u0, u0 + nt)
         const int64_t next = min(u0 + nt, t_end);
         // blocks with a part of its tiles (an empty unit: the block with its last empty tile)
-        const int64_t real = min(u0 + S::kLead, u0 + nt - 1);
-        const int c_lo = (int)quot(real, per), c_hi = (int)quot(u0 + nt - 1, per);
-        if (next <= real) {                                                // only empty tiles here
-            t = next;
-            continue;
+        const int64_t real = min(u0 + lead, u0 + nt - 1);
+        if (next <= real) return false;                                   // only empty tiles left in this block
+        p.c_lo = (int)quot(real, per);
+        p.c_hi = (int)quot(u0 + nt - 1, per);
+        p.begins = real >= t_begin;
+        p.i0 = (int)max(t - u0 - lead, (int64_t)0);
+        p.tiles = min(real_tiles, (int)(next - u0) - lead) - p.i0;
+        p.g = (int)quot(u, RT);
+        p.m0 = (u - p.g * RT) * kSplitRows;
+        p.rows = (int)min((int64_t)kSplitRows, M - p.m0);
+        t = next;
+        if (next - base == nt * U) {
+            base = next;
+            ++b_at;
         }
-        const int i0 = (int)max(t - u0 - S::kLead, (int64_t)0);
-        const int i1 = (int)(next - u0) - S::kLead;
-        const int g = (int)quot(u, RT);
-        const int64_t m0 = (u - g * RT) * kSplitRows;
-        const int rows = (int)min((int64_t)kSplitRows, M - m0);
+        return true;
+    };
 
-        // ---- this warp's chunks: positions (i * 4 + warp) * kChunk ... for i in [i0, i1)
-        int n = 0;
-        {
-            const int first = i0 * kTile + warp * kChunk;
-            if (first < len) n = min(i1 - i0, (len - first + kTile - 1) / kTile);
-        }
-        const int64_t head = g * a.head_stride;
-        // element offset of position p, -1 without one
-        auto offset = [&](int p, int id) -> int64_t {
-            if (!a.table) return b * a.batch_stride + p * a.pos_stride + head;
-            const uint32_t page = a.by_ps.div((uint32_t)p);
-            return (uint32_t)id < (uint32_t)a.n_pages
-                       ? id * a.page_stride + (int64_t)((uint32_t)p - page * a.by_ps.d) * a.pos_stride + head : -1;
-        };
-        auto page_of = [&](int c) -> int {                                 // of this lane's position of chunk c
-            const int p = (i0 + c) * kTile + warp * kChunk + (lane & (kChunk - 1));
-            return a.table && c < n && p < len ? __ldcg(a.table + (int64_t)b * a.table_stride + a.by_ps.div((uint32_t)p)) : -1;
-        };
-        int ids[kSt];                                                     // page ids, a ring ahead of the copies
-#pragma unroll
-        for (int c = 0; c < kSt; ++c) ids[c] = page_of(c);
-        // ---- queries of this lane: a row, 4 elements of each 16
-        float2 x[kSteps][2];
-        {
-            const bool live = row < rows;
-            const int64_t m = m0 + (live ? row : 0), qi = quot(m, G);
-            const int64_t at = b * a.q_batch + qi * a.q_stride + ((int64_t)g * G + (m - qi * G)) * HD;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
+    float* s_o = reinterpret_cast<float*>(smem + S::kRing);              // [warp][row][HD]
+    float* s_m = s_o + kWarps * kSplitRows * HD;                          // [warp][row]
+    float* s_l = s_m + kWarps * kSplitRows;
+    unsigned char* s_q = smem + S::kRing + S::kMerge;                      // [unit][row][HD] of the queries' type
+    const int qbytes = a.dtype == SD_F32 ? 4 : 2;
+    if (warp >= kWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        bool ok = true;
+        if (warp > kWarps + kLoaders) {
+            // ============================================ mergers: two rows of every unit each, beside the next unit's tiles
+            const int mw = warp - kWarps - kLoaders - 1;
+            constexpr int kVec = HD / 32;                                 // columns of a lane
+            for (uint32_t nu = 0;; ++nu) {
+                if (!warp_wait(smem_u32(&s_ufull[nu % kUnits]), (nu / kUnits) & 1, bad)) break;
+                const Unit u = s_unit[nu % kUnits];
+                __syncwarp();
+                if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
+                if (!u.rows) break;
+                if (!warp_wait(smem_u32(&s_done), nu & 1, bad)) break;
+                float val[2][kVec], mm[2], ll[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int d = 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e);
-                    x[k][e] = live ? load2(a.q, at + d, a.dtype) : make_float2(0.f, 0.f);
+                    const int r = 2 * mw + e;
+                    float mw_[kWarps];
+                    mm[e] = -INFINITY;
+                    ll[e] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kVec; ++x) val[e][x] = 0.f;
+                    if (r >= u.rows) continue;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        mw_[w] = s_m[w * kSplitRows + r];
+                        mm[e] = fmaxf(mm[e], mw_[w]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        if (mw_[w] == -INFINITY) continue;
+                        const float f = ex2(mw_[w] - mm[e]);
+                        ll[e] = fmaf(f, s_l[w * kSplitRows + r], ll[e]);
+                        const float* so = s_o + (w * kSplitRows + r) * HD + lane * kVec;
+#pragma unroll
+                        for (int x = 0; x < kVec; ++x) val[e][x] = fmaf(f, so[x], val[e][x]);
+                    }
                 }
-        }
-        auto issue = [&](int c, int slot) {
-            const int p = (i0 + c) * kTile + warp * kChunk + (lane & (kChunk - 1));
-            const int64_t off = p < len ? offset(p, ids[slot]) : -1;
-            ids[slot] = page_of(c + kSt);
-            const uint32_t live = __ballot_sync(0xffffffffu, off >= 0);
-            const uint32_t dst = ring + slot * S::kStage;
+                __syncwarp();
+                if (lane == 0) mb_arrive(smem_u32(&s_free));
+                if (2 * mw >= u.rows) continue;
+                const int n_rows = min(2, u.rows - 2 * mw);
+                bool last = true;
+                if (u.c_lo != u.c_hi) {
+                    // ---- the last block of the unit to arrive joins the records in block order
+                    float* rec = a.part + (int64_t)(2 * blockIdx.x + u.begins) * kSplitRecord;
 #pragma unroll
-            for (int r0 = 0; r0 < kChunk; r0 += 32 / S::kCols) {
-                const int r = r0 + lane / S::kCols, col = lane % S::kCols;
-                const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-                const int64_t bytes = ro < 0 ? 0 : ro * (S::kE4 ? 1 : 2) + col * 16;
-                const uint32_t size = ro < 0 ? 0 : 16;
-                cp16(dst + S::at(r, col), static_cast<const char*>(a.k) + bytes, size);
-                cp16(dst + kChunk * S::kRow + S::at(r, col), static_cast<const char*>(a.v) + bytes, size);
+                    for (int e = 0; e < 2; ++e) {
+                        if (e >= n_rows) break;
+                        const int r = 2 * mw + e;
+#pragma unroll
+                        for (int x = 0; x < kVec; ++x) __stcg(rec + r * HD + lane * kVec + x, val[e][x]);
+                        if (lane == 0) __stcg(reinterpret_cast<float2*>(rec + kSplitRows * 128) + r, make_float2(mm[e], ll[e]));
+                    }
+                    __syncwarp();
+                    int before = 0;
+                    if (lane == 0) {
+                        __threadfence();
+                        before = atomicAdd(a.cnt + u.c_lo * kMergers + mw, 1);
+                        __threadfence();
+                    }
+                    last = __shfl_sync(0xffffffffu, before, 0) == u.c_hi - u.c_lo;
+                    if (last) {
+                        if (lane == 0) a.cnt[u.c_lo * kMergers + mw] = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (e >= n_rows) break;
+                            const int r = 2 * mw + e;
+                            mm[e] = -INFINITY;
+                            ll[e] = 0.f;
+#pragma unroll
+                            for (int x = 0; x < kVec; ++x) val[e][x] = 0.f;
+#pragma unroll 4
+                            for (int c = u.c_lo; c <= u.c_hi; ++c) {
+                                const float* p = a.part + (int64_t)(2 * c + (c == u.c_lo ? 1 : 0)) * kSplitRecord;
+                                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kSplitRows * 128) + r);
+                                float oc[kVec];
+#pragma unroll
+                                for (int x = 0; x < kVec; ++x) oc[x] = __ldcg(p + r * HD + lane * kVec + x);
+                                const bool have = ml.x != -INFINITY;
+                                const float mx = fmaxf(mm[e], ml.x);
+                                const float f0 = mm[e] == -INFINITY ? 0.f : ex2(mm[e] - mx), f1 = have ? ex2(ml.x - mx) : 0.f;
+                                ll[e] = ll[e] * f0 + ml.y * f1;
+#pragma unroll
+                                for (int x = 0; x < kVec; ++x) val[e][x] = val[e][x] * f0 + (have ? oc[x] * f1 : 0.f);
+                                mm[e] = mx;
+                            }
+                        }
+                    }
+                }
+                if (!last) continue;
+                const float vs = a.v_scale ? __ldcg(a.v_scale + u.g) : 1.f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= n_rows) break;
+                    const int64_t m = u.m0 + 2 * mw + e, qi = quot(m, G), h = (int64_t)u.g * G + (m - qi * G);
+                    const int64_t at = u.b * a.o_batch + qi * a.o_stride + h * HD + lane * kVec;
+                    const float inv = ll[e] == 0.f ? 0.f : vs / ll[e];
+#pragma unroll
+                    for (int x = 0; x < kVec; ++x) val[e][x] = ll[e] == 0.f ? 0.f : val[e][x] * inv;
+                    storev<kVec>(a.out, at, a.dtype, val[e]);
+                    if (lane == 0 && a.lse)
+                        a.lse[((int64_t)u.b * a.Lq + qi) * a.H + h] = ll[e] == 0.f ? -INFINITY : (mm[e] + log2f(ll[e]) - S::kShift) * kLn2;
+                }
             }
-            return live;
-        };
-        uint32_t live[kSt];                                               // live positions of the chunks in flight
-#pragma unroll
-        for (int s = 0; s < kSt; ++s) live[s] = 0;
-#pragma unroll
-        for (int c = 0; c < kSt - 1; ++c) {
-            if (c < n) live[c] = issue(c, c);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (lane == 0 && *bad) *a.err = SD_ERR_TIMEOUT;
+            return;
         }
+        Unit p;
+        if (warp == kWarps + kLoaders) {
+            // ============================================ units and their queries
+            uint32_t n = 0;
+            for (; ok && next_unit(p); ++n) {
+                const uint32_t slot = n % kUnits;
+                if (n >= kUnits) ok = warp_wait(smem_u32(&s_uempty[slot]), (n / kUnits - 1) & 1, bad);
+                if (!ok) break;
+                const int cols = HD * qbytes / 16;
+                for (int x = lane; x < kSplitRows * cols; x += 32) {
+                    const int r = x / cols, c = x - r * cols;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < p.rows) {
+                        const int64_t m = p.m0 + r, qi = quot(m, G);
+                        const int64_t at = p.b * a.q_batch + qi * a.q_stride + ((int64_t)p.g * G + (m - qi * G)) * HD;
+                        v = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at * qbytes + c * 16);
+                    }
+                    *reinterpret_cast<uint4*>(s_q + slot * S::kQueries + x * 16) = v;
+                }
+                if (lane == 0) s_unit[slot] = p;
+                __syncwarp();
+                if (lane == 0) mb_arrive(smem_u32(&s_ufull[slot]));
+            }
+            // behind the last unit: one without rows
+            const uint32_t slot = n % kUnits;
+            if (ok && n >= kUnits) ok = warp_wait(smem_u32(&s_uempty[slot]), (n / kUnits - 1) & 1, bad);
+            if (lane == 0) {
+                s_unit[slot].rows = 0;
+                mb_arrive(smem_u32(&s_ufull[slot]));
+            }
+            return;
+        }
+        // ================================================ loads: of a tile the keys (a stage) and the values (the next)
+        const uint32_t turn_of = warp - kWarps;
+        uint32_t n = 0, last = 0;                                         // tiles of all loaders so far; stages up to this one's last
+        const int groups = args.groups, box = args.box;
+        while (ok && next_unit(p)) {
+            // of a lane's box (k * 32 + lane) of tile i: its page, -1 without one
+            auto lookup = [&](int i, int k) -> int {
+                const int pos = (p.i0 + i) * kTile + (k * 32 + lane) * box;
+                if (i >= p.tiles || k * 32 + lane >= groups || pos >= p.len) return -1;
+                return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + a.by_ps.div((uint32_t)pos)) : p.b;
+            };
+            const int outer = a.table ? a.n_pages : a.B;
+            int i = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(i, 0);
+            for (; i < p.tiles && ok; i += kLoaders) {
+                const int first = (p.i0 + i) * kTile, rest = p.len - first;
+                int id[kTile / 32], in[kTile / 32], mine_boxes = 0;
+                id[0] = ahead;
+#pragma unroll
+                for (int k = 1; k < kTile / 32; ++k) id[k] = k * 32 < groups ? lookup(i, k) : -1;
+                ahead = lookup(i + kLoaders, 0);                          // a tile ahead: not waited for here
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k) {
+                    if ((uint32_t)id[k] >= (uint32_t)outer) id[k] = -1;
+                    in[k] = first + (k * 32 + lane) * box;
+                    if (a.table) in[k] -= (int)(a.by_ps.div((uint32_t)in[k]) * a.by_ps.d);
+                    mine_boxes += id[k] >= 0;
+                }
+                const int all = __reduce_add_sync(0xffffffffu, mine_boxes);
+#pragma unroll
+                for (int op = 0; op < 2; ++op) {
+                    const uint32_t st = 2 * (n + i) + op, slot = st % kSt, turn = st / kSt;
+                    if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
+                    if (!ok) break;
+                    last = st + 1;
+                    const uint32_t mb = smem_u32(&s_full[slot]), dst = ring + slot * S::kStage;
+                    if (op == 0) {
+                        // live positions of each chunk
+                        if (lane < kWarps) s_live[slot][lane] = 0;
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < kTile / 32; ++k) {
+                            if (id[k] < 0) continue;
+                            const int at = (k * 32 + lane) * box, end = min(at + box, rest);
+                            for (int r = at; r < end;) {
+                                const int c = r / kChunk, stop = min(end, (c + 1) * kChunk), count = stop - r;
+                                atomicOr(&s_live[slot][c], (0xffffffffu >> (32 - count)) << (r - c * kChunk));
+                                r = stop;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        if (all) mb_expect(mb, all * box * S::kRow);
+                        else mb_arrive(mb);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kTile / 32; ++k) {
+                        if (id[k] < 0) continue;
+                        const uint32_t to = dst + (k * 32 + lane) * box * S::kPart;
+#pragma unroll
+                        for (int part = 0; part < S::kParts; ++part)
+                            tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, in[k], p.g, id[k], mb);
+                    }
+                }
+            }
+            n += max(p.tiles, 0);
+        }
+        if (!ok)                                                          // bounded: this warp's own copies
+            for (uint32_t x = last > kSt ? last - kSt : 0; x < last; ++x) {
+                if ((x >> 1) % kLoaders != turn_of) continue;
+                const long long t0 = clock64();
+                while (!mb_try(smem_u32(&s_full[x % kSt]), (x / kSt) & 1) && clock64() - t0 < kWaitClocks) {}
+            }
+        return;
+    }
+
+    // ==================================================== scores and sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+    const int row = lane >> 2, quad = lane & 3, mi = lane >> 3, mr = lane & 7;
+    // Low-order parts: of q where the products' type does not hold it (a 16-bit q scaled into fp16 loses only what is
+    // 2^-24 of its row's largest element); of the probabilities for fp32 results and where bf16 is all they have
+    const bool q_low = a.dtype == SD_F32 || (S::kBf && a.dtype == SD_F16), p_low = a.dtype == SD_F32 || S::kBf;
+    uint32_t n = 0;                                                       // chunks of the units before (whole tiles)
+    for (uint32_t nu = 0;; ++nu) {
+        // a failed wait (flagged) ends the waiting, and with it the walk
+        bool ok = warp_wait(smem_u32(&s_ufull[nu % kUnits]), (nu / kUnits) & 1, bad);
+        const Unit pc = s_unit[nu % kUnits];
+        if (!ok || !pc.rows) break;
+        const int g = pc.g, rows = pc.rows;
+        // ---- queries of this lane: a row, 4 elements of each 16
+        float2 x[kSteps][2];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                x[k][e] = load2(s_q + nu % kUnits * S::kQueries, row * HD + 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e), a.dtype);
+        __syncwarp();
+        if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
         // ---- rows 0-7 of the A operand: the rounded rows; rows 8-15: what the rounding left
         uint32_t qa[kSteps][4];
         float row_scale = a.scale * kLog2e * (a.k_scale ? __ldcg(a.k_scale + g) : 1.f);
@@ -306,114 +600,135 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
         }
         float o[kOut][4];
 #pragma unroll
-        for (int n = 0; n < kOut; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        for (int y = 0; y < kOut; ++y) o[y][0] = o[y][1] = o[y][2] = o[y][3] = 0.f;
         float mrow = -INFINITY, lrow = 0.f;
 
-        for (int c0 = 0; c0 < n; c0 += kSt) {
+        // ---- this warp's chunks: every kWarps-th of the block's, eight to a tile
+        constexpr int kN = kChunk / 8, kH = kChunk / 16;                  // products of 8, halves of 16 positions
+        constexpr int kBlocks = kSteps * kH / (S::kE4 ? 2 : 1);           // of one ldmatrix each, as many for P V
+        static_assert(kBlocks == kH * kOut / (S::kE4 ? 4 : 2), "scores and results have as many blocks");
+        float sc[kN][4];
+        uint32_t pa[kH][4];
+        int r0 = 0;                                                       // first position of the chunk in its tile
+        auto score_block = [&](int u, uint32_t kb) {
+            uint32_t f[4];
+            if constexpr (!S::kE4) {
+                const int k = u / kH, h = u % kH;
+                ldm4(kb + S::at(r0 + 16 * h + (mi >> 1) * 8 + mr, 2 * k + (mi & 1)), f);
+                mma<S::kBf>(sc[2 * h], qa[k], f[0], f[1]);
+                mma<S::kBf>(sc[2 * h + 1], qa[k], f[2], f[3]);
+            } else {
+                const int k = 2 * (u / kH), h = u % kH;
+                ldm4(kb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, k + (mi >> 1)), f);
 #pragma unroll
-            for (int s = 0; s < kSt; ++s) {
-                const int c = c0 + s;
-                if (c >= n) break;
-                __syncwarp();
-                if (c + kSt - 1 < n) live[(s + kSt - 1) % kSt] = issue(c + kSt - 1, (s + kSt - 1) % kSt);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
-                __syncwarp();
-                const uint32_t kb = ring + s * S::kStage, vb = kb + kChunk * S::kRow;
-                const int mi = lane >> 3, mr = lane & 7;
-
-                constexpr int kN = kChunk / 8, kH = kChunk / 16;          // products of 8, halves of 16 positions
-                float sc[kN][4] = {};
-                if constexpr (!S::kE4) {
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                        for (int h = 0; h < kH; ++h) {
-                            uint32_t f[4];
-                            ldm4(kb + S::at(16 * h + (mi >> 1) * 8 + mr, 2 * k + (mi & 1)), f);
-                            mma<S::kBf>(sc[2 * h], qa[k], f[0], f[1]);
-                            mma<S::kBf>(sc[2 * h + 1], qa[k], f[2], f[3]);
-                        }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kSteps; k += 2)
-#pragma unroll
-                        for (int h = 0; h < kH; ++h) {
-                            uint32_t f[4];
-                            ldm4(kb + S::at(16 * h + (mi & 1) * 8 + mr, k + (mi >> 1)), f);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma<false>(sc[2 * h], qa[k + e], half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e] >> 16));
-                                mma<false>(sc[2 * h + 1], qa[k + e], half2_of_e4m3(f[2 * e + 1]),
-                                           half2_of_e4m3(f[2 * e + 1] >> 16));
-                            }
-                        }
-                }
-                // this lane's scores: row `row`, positions 8j + 2 quad and the next
-                float p[kN][2], mx = -INFINITY;
-                const uint32_t lv = live[s] >> (2 * quad);
-#pragma unroll
-                for (int j = 0; j < kN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = add_low(sc[j][e], sc[j][2 + e]) * row_scale;
-                        p[j][e] = (lv >> (8 * j + e)) & 1 ? x : -INFINITY;
-                        mx = fmaxf(mx, p[j][e] == p[j][e] ? p[j][e] : INFINITY);   // NaN reaches every result of its row
-                    }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(mrow, mx);
-                if (__any_sync(0xffffffffu, mn > mrow)) {
-                    const float keep = mrow == -INFINITY ? 0.f : ex2(mrow - mn);
-                    lrow *= keep;
-#pragma unroll
-                    for (int x = 0; x < kOut; ++x) {
-                        o[x][0] *= keep; o[x][1] *= keep;
-                        o[x][2] *= keep; o[x][3] *= keep;
-                    }
-                    mrow = mn;
-                }
-                const float ref = mrow == -INFINITY ? 0.f : mrow - S::kShift;
-                uint32_t pa[kH][4];
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    const float p0 = ex2(p[j][0] - ref), p1 = ex2(p[j][1] - ref);
-                    lrow += p0 + p1;
-                    split2<S::kBf>(p0, p1, pa[j / 2][2 * (j & 1)], pa[j / 2][2 * (j & 1) + 1]);
-                }
-                if constexpr (!S::kE4) {
-#pragma unroll
-                    for (int h = 0; h < kH; ++h)
-#pragma unroll
-                        for (int x = 0; x < kOut; x += 2) {
-                            uint32_t f[4];
-                            ldm4t(vb + S::at(16 * h + (mi & 1) * 8 + mr, x + (mi >> 1)), f);
-                            mma<S::kBf>(o[x], pa[h], f[0], f[1]);
-                            mma<S::kBf>(o[x + 1], pa[h], f[2], f[3]);
-                        }
-                } else {
-                    // a transposed matrix of byte pairs: even dimensions in the low bytes, odd ones in the high
-#pragma unroll
-                    for (int h = 0; h < kH; ++h)
-#pragma unroll
-                        for (int x = 0; x < kOut; x += 4) {
-                            uint32_t f[4];
-                            ldm4t(vb + S::at(16 * h + (mi & 1) * 8 + mr, x / 2 + (mi >> 1)), f);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma<false>(o[x + 2 * e], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)),
-                                           half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)));
-                                mma<false>(o[x + 2 * e + 1], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
-                                           half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431)));
-                            }
-                        }
+                for (int e = 0; e < 2; ++e) {
+                    mma<false>(sc[2 * h], qa[k + e], half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e] >> 16));
+                    mma<false>(sc[2 * h + 1], qa[k + e], half2_of_e4m3(f[2 * e + 1]), half2_of_e4m3(f[2 * e + 1] >> 16));
                 }
             }
+        };
+        auto result_block = [&](int u, uint32_t vb) {
+            uint32_t f[4];
+            if constexpr (!S::kE4) {
+                const int h = u / (kOut / 2), x = u % (kOut / 2) * 2;
+                ldm4t(vb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, x + (mi >> 1)), f);
+                mma<S::kBf>(o[x], pa[h], f[0], f[1]);
+                mma<S::kBf>(o[x + 1], pa[h], f[2], f[3]);
+            } else {
+                // a transposed matrix of byte pairs: even dimensions in the low bytes, odd ones in the high
+                const int h = u / (kOut / 4), x = u % (kOut / 4) * 4;
+                ldm4t(vb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, x / 2 + (mi >> 1)), f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma<false>(o[x + 2 * e], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)),
+                               half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)));
+                    mma<false>(o[x + 2 * e + 1], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
+                               half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431)));
+                }
+            }
+        };
+        auto release = [&](uint32_t slot) {
+            __syncwarp();
+            if (lane == 0) mb_arrive(smem_u32(&s_empty[slot]));
+        };
+        for (int c = (int)((warp + kWarps - n % kWarps) % kWarps); c < pc.tiles * kWarps; c += kWarps) {
+            const uint32_t st = 2 * ((n + c) / kWarps), sk = st % kSt, sv = (st + 1) % kSt;
+            const uint32_t kb = ring + sk * S::kStage, vb = ring + sv * S::kStage;
+            r0 = c % kWarps * kChunk;
+            warp_wait(smem_u32(&s_full[sk]), (st / kSt) & 1, bad);
+            const uint32_t live = s_live[sk][c % kWarps];
+            if (!live) {                                                  // nothing here
+                release(sk);
+                warp_wait(smem_u32(&s_full[sv]), ((st + 1) / kSt) & 1, bad);
+                release(sv);
+                continue;
+            }
+#pragma unroll
+            for (int y = 0; y < kN; ++y) sc[y][0] = sc[y][1] = sc[y][2] = sc[y][3] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kBlocks; ++u) score_block(u, kb);
+            release(sk);
+            // this lane's scores: row `row`, positions 8j + 2 quad and the next
+            float p[kN][2], mx = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < kN; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) p[y][e] = (q_low ? add_low(sc[y][e], sc[y][2 + e]) : sc[y][e]) * row_scale;
+            if (live != 0xffffffffu >> (32 - kChunk)) {
+                const uint32_t lv = live >> (2 * quad);
+#pragma unroll
+                for (int y = 0; y < kN; ++y)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!((lv >> (8 * y + e)) & 1)) p[y][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int y = 0; y < kN; ++y) mx = max_nan(mx, max_nan(p[y][0], p[y][1]));
+            if (mx != mx) mx = INFINITY;                                  // NaN reaches every result of its row
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(mrow, mx);
+            if (__any_sync(0xffffffffu, mn > mrow)) {
+                const float keep = mrow == -INFINITY ? 0.f : ex2(mrow - mn);
+                lrow *= keep;
+#pragma unroll
+                for (int x = 0; x < kOut; ++x) {
+                    o[x][0] *= keep; o[x][1] *= keep;
+                    o[x][2] *= keep; o[x][3] *= keep;
+                }
+                mrow = mn;
+            }
+            const float ref = mrow == -INFINITY ? 0.f : mrow - S::kShift;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                const float p0 = ex2(p[j][0] - ref), p1 = ex2(p[j][1] - ref);
+                lrow += p0 + p1;
+                if (p_low) {
+                    split2<S::kBf>(p0, p1, pa[j / 2][2 * (j & 1)], pa[j / 2][2 * (j & 1) + 1]);
+                } else {
+                    pa[j / 2][2 * (j & 1)] = round2<S::kBf>(p0, p1);
+                    pa[j / 2][2 * (j & 1) + 1] = 0;
+                }
+            }
+            warp_wait(smem_u32(&s_full[sv]), ((st + 1) / kSt) & 1, bad);
+            if (live != 0xffffffffu >> (32 - kChunk)) {
+                // values of positions that are not there: 0, whatever lies in memory
+                for (int y = lane; y < kChunk * S::kCols; y += 32) {
+                    const int r = y / S::kCols;
+                    if (!((live >> r) & 1))
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + S::at(r0 + r, y % S::kCols)), "r"(0) : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+#pragma unroll
+            for (int u = 0; u < kBlocks; ++u) result_block(u, vb);
+            release(sv);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
+        n += pc.tiles * kWarps;
 
-        // ---- the four warps' results
+        // ---- the warps' results
+        if (nu > 0) warp_wait(smem_u32(&s_free), (nu - 1) & 1, bad);
         lrow += __shfl_xor_sync(0xffffffffu, lrow, 1);
         lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
         if (quad == 0) {
@@ -421,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
             s_l[warp * kSplitRows + row] = lrow;
         }
         float* so = s_o + (warp * kSplitRows + row) * HD;
-        if (row < rows) {
+        if (row < rows && mrow != -INFINITY) {
 #pragma unroll
             for (int x = 0; x < kOut; ++x) {
                 const float v0 = add_low(o[x][0], o[x][2]), v1 = add_low(o[x][1], o[x][3]);
@@ -434,83 +749,52 @@ __global__ void __launch_bounds__(kThreads, kSplitBlocksPerSm) k_attend_split(co
                 }
             }
         }
-        __syncthreads();
-        const float vs = a.v_scale ? __ldcg(a.v_scale + g) : 1.f;
-        auto put = [&](int r, int d, float val, float mm, float ll) {
-            const int64_t m = m0 + r, qi = quot(m, G);
-            const int64_t h = (int64_t)g * G + (m - qi * G);
-            store1(a.out, b * a.o_batch + qi * a.o_stride + h * HD + d, a.dtype, ll == 0.f ? 0.f : val * vs / ll);
-            if (d == 0 && a.lse)
-                a.lse[((int64_t)b * a.Lq + qi) * a.H + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - S::kShift) * kLn2;
-        };
-        float* rec = a.part + (int64_t)(2 * blockIdx.x + (real >= t_begin ? 1 : 0)) * kSplitRecord;
-        for (int x = tid; x < rows * HD; x += kThreads) {
-            const int r = x / HD, d = x % HD;
-            float mm = -INFINITY, ll = 0.f, val = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * kSplitRows + r]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = s_m[w * kSplitRows + r], f = mw == -INFINITY ? 0.f : ex2(mw - mm);
-                ll = fmaf(f, s_l[w * kSplitRows + r], ll);
-                if (mw != -INFINITY) val = fmaf(f, s_o[(w * kSplitRows + r) * HD + d], val);
-            }
-            if (c_lo == c_hi) {
-                put(r, d, val, mm, ll);
-            } else {
-                __stcg(rec + r * HD + d, val);
-                if (d == 0) {
-                    __stcg(rec + kSplitRows * 128 + 2 * r, mm);
-                    __stcg(rec + kSplitRows * 128 + 2 * r + 1, ll);
-                }
-            }
-        }
-        if (c_lo != c_hi) {
-            // ---- the last block of the unit to arrive joins the records in block order
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                s_last = atomicAdd(a.cnt + c_lo, 1) == c_hi - c_lo;
-                __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                for (int x = tid; x < rows * HD; x += kThreads) {
-                    const int r = x / HD, d = x % HD;
-                    float mm = -INFINITY, ll = 0.f, val = 0.f;
-                    for (int c = c_lo; c <= c_hi; ++c) {
-                        const float* p = a.part + (int64_t)(2 * c + (c == c_lo ? 1 : 0)) * kSplitRecord;
-                        const float mc = __ldcg(p + kSplitRows * 128 + 2 * r), lc = __ldcg(p + kSplitRows * 128 + 2 * r + 1);
-                        const float oc = __ldcg(p + r * HD + d);
-                        if (mc == -INFINITY) continue;
-                        const float mx = fmaxf(mm, mc);
-                        const float f0 = mm == -INFINITY ? 0.f : ex2(mm - mx), f1 = ex2(mc - mx);
-                        ll = ll * f0 + lc * f1;
-                        val = val * f0 + oc * f1;
-                        mm = mx;
-                    }
-                    put(r, d, val, mm, ll);
-                }
-                if (tid == 0) a.cnt[c_lo] = 0;
-            }
-        }
-        __syncthreads();
-        t = next;
-        if (t - base == nt * U) {
-            base = t;
-            ++b;
-        }
+        // the mergers take it from here
+        __syncwarp();
+        if (lane == 0) mb_arrive(smem_u32(&s_done));
     }
+    if (tid == 0 && *bad) *a.err = SD_ERR_TIMEOUT;
+}
+
+// K or V by strides, as [outer][head][position][hd]: boxes of `box` positions of up to 128 bytes of a row
+bool map_kv(CUtensorMap* map, int dtype, const void* base, int hd, int positions, int heads, int outer, int64_t pos_stride,
+            int64_t head_stride, int64_t outer_stride, int box) {
+    EncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int bytes = dtype == SD_E4M3 ? 1 : 2, row = hd * bytes;
+    const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)positions, (cuuint64_t)heads, (cuuint64_t)outer};
+    // the stride of a dimension of one element is not used: any legal value
+    const cuuint64_t strides[3] = {(cuuint64_t)(positions > 1 ? pos_stride * bytes : row),
+                                   (cuuint64_t)(heads > 1 ? head_stride * bytes : row),
+                                   (cuuint64_t)(outer > 1 ? outer_stride * bytes : row)};
+    const cuuint32_t boxes[4] = {(cuuint32_t)(row < 128 ? hd : 128 / bytes), (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = dtype == SD_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == SD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(map, type, 4, const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, int KV>
 cudaError_t launch_one(const AttendArgs& a, int sms, cudaStream_t st) {
     using S = Shape<HD, KV>;
+    SplitArgs t;
+    int box = S::kTile;
+    if (a.table)
+        while (a.by_ps.d % box) box >>= 1;
+    t.box = box;
+    t.groups = S::kTile / box;
+    const int positions = a.table ? (int)a.by_ps.d : std::max(a.max_len, 1), outer = a.table ? a.n_pages : a.B;
+    const int64_t outer_stride = a.table ? a.page_stride : a.batch_stride;
+    if (!map_kv(&t.k, KV, a.k, HD, positions, a.Hkv, outer, a.pos_stride, a.head_stride, outer_stride, box) ||
+        !map_kv(&t.v, KV, a.v, HD, positions, a.Hkv, outer, a.pos_stride, a.head_stride, outer_stride, box))
+        return cudaErrorInvalidValue;
+    t.a = a;
     // no more blocks than tiles there can be
     const int64_t RT = ((int64_t)a.Lq * (a.H / a.Hkv) + kSplitRows - 1) / kSplitRows;
     const int64_t most = std::min<int64_t>((int64_t)1 << 30, (int64_t)a.B * RT * a.Hkv) * (a.max_len / S::kTile + 1);
-    const int grid = (int)std::min<int64_t>(kSplitBlocksPerSm * sms, most);
-    return launch_k(k_attend_split<HD, KV>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
+    const int grid = (int)std::min<int64_t>(sms, most);
+    return launch_k(k_attend_split<HD, KV>, dim3(grid), dim3(kThreads), S::kSmem, st, t);
 }
 
 template <int HD, int KV>

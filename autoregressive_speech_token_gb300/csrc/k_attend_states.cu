@@ -60,11 +60,11 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     if (!ws) return op_fail(SD_ERR_OOM, "sd_attn_ws_create: out of host memory");
     ws->device = device;
     cudaError_t e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, device);
-    const size_t blocks = (size_t)kSplitBlocksPerSm * ws->sms;
+    const size_t blocks = (size_t)ws->sms;
     if (e == cudaSuccess) e = cudaMalloc(&ws->part, 2 * blocks * kSplitRecord * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * sizeof(int));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * kSplitRows / 2 * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
-    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * kSplitRows / 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     if (e == cudaSuccess) e = cudaHostAlloc(&ws->err, sizeof(int), cudaHostAllocDefault);
     if (e == cudaSuccess) *ws->err = 0;
@@ -98,6 +98,8 @@ int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_
     if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
     if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
     if (int rc = check_q(who, dtype, c.dtype, q_dev, q_stride, out_dev, out_stride, n_head, c.n_kv_head, scale)) return rc;
+    if (c.dtype == SD_E4M3 && c.head_dim == 64 && c.page_size % 2)
+        return op_fail(SD_ERR_UNSUPPORTED, "%s: pages of an odd number of 64-byte rows", who);
     if (!ws) return op_fail(SD_ERR_INVALID_ARG, "%s: ws is NULL", who);
     if (R == 0) return SD_OK;
     AttendArgs a = {};
@@ -131,9 +133,9 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
         s.pos_stride = (int64_t)s.n_kv_head * s.head_dim;
         s.batch_stride = s.pos_stride * s.n_pos;
     }
-    if (s.batch_stride < 0 || s.head_stride < 0 || s.pos_stride < 0 || s.batch_stride % 8 || s.head_stride % 8 ||
-        s.pos_stride % 8)
-        return op_fail(SD_ERR_INVALID_ARG, "%s: the states' strides must be multiples of 16 bytes", who);
+    if (!tma_stride(s.batch_stride, 2, s.B) || !tma_stride(s.head_stride, 2, s.n_kv_head) ||
+        !tma_stride(s.pos_stride, 2, s.n_pos))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: the states' strides must be positive multiples of 16 bytes", who);
     if (int rc = check_q(who, dtype, s.dtype, q_dev, q_stride, out_dev, out_stride, n_head, s.n_kv_head, scale)) return rc;
     if (s.B > 1 && (!stride16(q_batch, dtype_bytes(dtype)) || !stride16(out_batch, dtype_bytes(dtype))))
         return op_fail(SD_ERR_INVALID_ARG, "%s: q_batch and out_batch must be multiples of 16 bytes", who);

@@ -22,8 +22,6 @@
 //
 // Every wait is bounded: on expiry the block records the error, lets its own copies
 // and products finish (bounded), frees its tensor memory and returns.
-#include <cuda.h>
-
 #include "attend_dev.cuh"
 
 namespace sd {
@@ -32,12 +30,10 @@ namespace {
 constexpr int kM = 128, kN = 128;                    // queries and positions of a tile
 constexpr int kSoftWarps = 8, kThreads = 32 * (kSoftWarps + 4);    // 2 softmax warpgroups; products, loads, 2 idle warps
 constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Registers of a thread: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72 (a softmax thread holds a row of 128 scores)
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
-constexpr long long kWaitClocks = 4000000000ll;      // about two seconds
 
 struct alignas(128) TcArgs {
     CUtensorMap q, k, v;
@@ -55,46 +51,6 @@ struct Cfg {
     static constexpr uint32_t kO = 256;                           // tensor memory: S0, S1, O0, O1
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mb_init(uint32_t mb, uint32_t n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(n) : "memory");
-}
-__device__ __forceinline__ void mb_expect(uint32_t mb, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mb_arrive(uint32_t mb) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory");
-}
-__device__ __forceinline__ bool mb_try(uint32_t mb, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(mb), "r"(parity) : "memory");
-    return ok != 0;
-}
-// Bounded; gives up early once another warp of the block has given up.
-__device__ __forceinline__ bool mb_wait_slow(uint32_t mb, uint32_t parity, volatile int* bad) {
-    const long long t0 = clock64();
-    while (!mb_try(mb, parity)) {
-        if (*bad) return false;
-        if (clock64() - t0 > kWaitClocks) {
-            *bad = 1;
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
-    return mb_try(mb, parity) || mb_wait_slow(mb, parity, bad);
-}
-// The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
-    return __all_sync(0xffffffffu, mb_wait(mb, parity, bad));
-}
-__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int h, int r, int b, uint32_t mb) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(r), "r"(b), "r"(mb) : "memory");
-}
 // Shared-memory descriptor of a 128-byte-swizzled operand: 8-row groups 1024 bytes apart; `lead` is the
 // distance of the next 64 columns for an operand read along its rows (V), unused otherwise.
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead) {
@@ -170,11 +126,6 @@ __device__ __forceinline__ void after_wait(float* v) {
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // two fp32 operations an instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -530,25 +481,10 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
     if (tid == 0 && s_bad) *a.err = SD_ERR_TIMEOUT;
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encoder() {
-    static EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return (EncodeFn) nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
 // [batch][row][head][hd] of 16-bit elements by strides: boxes of 128 rows of 64 elements of one head
 bool map4(CUtensorMap* map, bool bf, const void* base, int hd, int heads, int rows, int batch, int64_t head_stride,
           int64_t row_stride, int64_t batch_stride) {
-    EncodeFn enc = encoder();
+    EncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
     // the stride of a dimension of one element is not used: any legal value

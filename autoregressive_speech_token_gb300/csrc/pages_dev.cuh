@@ -28,6 +28,10 @@ inline int dtype_bytes(int dt) {
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool stride16(int64_t elements, int bytes) { return elements % (16 / bytes) == 0; }
+// A stride of a dimension of `count` elements that TMA can hold (not used where there is one element)
+inline bool tma_stride(int64_t elements, int bytes, int64_t count) {
+    return stride16(elements, bytes) && (count <= 1 || (elements > 0 && elements < ((int64_t)1 << 40) / bytes));
+}
 
 // Makes `device` current for one call and puts the caller's back.
 struct DeviceScope {
@@ -81,9 +85,9 @@ inline int check_pages(const char* who, const sd_pages* c, sd_pages* out) {
         out->head_stride = (int64_t)c->page_size * c->head_dim;
         out->page_stride = out->head_stride * c->n_kv_head;
     }
-    if (out->page_stride < 0 || out->head_stride < 0 || out->pos_stride < 0 || !stride16(out->page_stride, b) ||
-        !stride16(out->head_stride, b) || !stride16(out->pos_stride, b))
-        return op_fail(SD_ERR_INVALID_ARG, "%s: cache strides must be multiples of 16 bytes", who);
+    if (!tma_stride(out->page_stride, b, c->n_pages) || !tma_stride(out->head_stride, b, c->n_kv_head) ||
+        !tma_stride(out->pos_stride, b, c->page_size))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: cache strides must be positive multiples of 16 bytes", who);
     return SD_OK;
 }
 

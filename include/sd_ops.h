@@ -174,7 +174,8 @@ enum { SD_F32 = 1, SD_F16 = 2, SD_BF16 = 3, SD_E4M3 = 4 };
  * (elements, the same for k_dev and v_dev).  All three strides 0: the order
  * [page][kv_head][pos][dim], as in the contexts' cache; [page][pos][kv_head][dim]
  * and pages of all layers in one pool are given by their strides.  Pointers are
- * 16-byte aligned and strides multiples of 16 bytes.  dtype SD_F16, SD_BF16, or
+ * 16-byte aligned and strides positive multiples of 16 bytes (below 2^40; not used where
+ * there is one element).  dtype SD_F16, SD_BF16, or
  * SD_E4M3 (stored value times k_scale_dev[g] / v_scale_dev[g]; NULL: 1; the scale
  * pointers are NULL for the other types).  head_dim is 64 or 128, page_size 1 to
  * 65536, n_pages * page_size at most 2^31 - 1. */
@@ -273,15 +274,16 @@ void sd_attn_ws_destroy(sd_attn_ws* ws);
  * with rows q_stride elements apart, out_dev the same with out_stride; pointers
  * are 16-byte aligned, strides multiples of 16 bytes.  lse_dev [R][n_head] (may be
  * NULL): the natural logarithm of the softmax's denominator, -inf for len 0.
- * n_head is a multiple of n_kv_head.  q enters the products with at least 22
- * bits (all of them for 16-bit types), probabilities with 22 (16 for SD_BF16 caches);
- * sums and statistics are fp32. */
+ * n_head is a multiple of n_kv_head; an SD_E4M3 cache of head_dim 64 needs an even
+ * page_size.  q enters the products with at least 22
+ * bits (16-bit types with all of them), probabilities with 22 for SD_F32 results, 16 on
+ * SD_BF16 caches, 11 otherwise; sums and statistics are fp32. */
 int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
                     const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride,
                     int32_t n_head, float scale, void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
 
 /* Keys and values of an encoder's states, [B][n_pos][n_kv_head][head_dim] by
- * default (all three strides 0); other orders by their strides (elements,
+ * default (all three strides 0); other orders by their strides (elements, positive
  * multiples of 16 bytes; pointers 16-byte aligned).  len_dev[b] states of row b
  * are used (limited to [0, n_pos]; NULL: n_pos).  dtype SD_F16 or SD_BF16. */
 typedef struct sd_states {

@@ -152,6 +152,8 @@ def test_attend_pages_refuses_bad_caches(code, kw, words):
     (INVALID, dict(H=0), "n_head 0"), (INVALID, dict(scale=float("inf")), "scale"),
     (INVALID, dict(scale=float("nan")), "scale"), (INVALID, dict(), "ws is NULL"),
     (UNSUPPORTED, dict(dtype=1, cache=pages(dtype=3)), "SD_F32 queries"),
+    (UNSUPPORTED, dict(cache=pages(dtype=4, page_size=7)), "odd number"),
+    (INVALID, dict(cache=pages(page_stride=0, head_stride=1024, pos_stride=64)), "positive"),
 ])
 def test_attend_pages_refusals(code, kw, words):
     refused(code, words, pkg.sd_attend_pages, *_attend(**kw))
@@ -176,7 +178,7 @@ def _cross(st=None, **kw):
     (INVALID, dict(dtype=4), {}, "type 4"), (UNSUPPORTED, dict(head_dim=80), {}, "head_dim 80"),
     (INVALID, dict(B=-1), {}, "B -1"), (INVALID, dict(n_pos=-1), {}, "n_pos -1"), (INVALID, dict(n_kv_head=0), {}, "n_kv_head 0"),
     (INVALID, dict(batch_stride=1280, head_stride=64, pos_stride=132), {}, "strides"),
-    (INVALID, {}, dict(Lq=-1), "Lq -1"), (INVALID, {}, dict(q_batch=1001), "q_batch"),
+    (INVALID, dict(batch_stride=0, head_stride=64, pos_stride=128), {}, "positive"), (INVALID, {}, dict(Lq=-1), "Lq -1"), (INVALID, {}, dict(q_batch=1001), "q_batch"),
     (INVALID, {}, dict(out_batch=1001), "out_batch"), (INVALID, {}, dict(q_stride=100), "16 bytes"),
     (INVALID, {}, dict(H=5), "n_head 5"), (INVALID, {}, {}, "ws is NULL"),
     (UNSUPPORTED, dict(dtype=3), dict(dtype=1), "SD_F32 queries"),
