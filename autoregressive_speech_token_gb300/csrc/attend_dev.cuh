@@ -51,6 +51,9 @@ __device__ __forceinline__ void mb_init(uint32_t mb, uint32_t n) {
 __device__ __forceinline__ void mb_expect(uint32_t mb, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void mb_expect_more(uint32_t mb, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mb_arrive(uint32_t mb) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory");
 }
@@ -60,10 +63,19 @@ __device__ __forceinline__ bool mb_try(uint32_t mb, uint32_t parity) {
                  : "=r"(ok) : "r"(mb), "r"(parity) : "memory");
     return ok != 0;
 }
+// The same, asleep until the phase completes or about 20 us have passed: a polling warp takes issue slots from the
+// others of its scheduler
+__device__ __forceinline__ bool mb_sleep(uint32_t mb, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(mb), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
 // Bounded; gives up early once another warp of the block has given up.
-__device__ __forceinline__ bool mb_wait_slow(uint32_t mb, uint32_t parity, volatile int* bad) {
+__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+    if (mb_sleep(mb, parity)) return true;
     const long long t0 = clock64();
-    while (!mb_try(mb, parity)) {
+    while (!mb_sleep(mb, parity)) {
         if (*bad) return false;
         if (clock64() - t0 > kWaitClocks) {
             *bad = 1;
@@ -71,9 +83,6 @@ __device__ __forceinline__ bool mb_wait_slow(uint32_t mb, uint32_t parity, volat
         }
     }
     return true;
-}
-__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
-    return mb_try(mb, parity) || mb_wait_slow(mb, parity, bad);
 }
 // The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {

@@ -18,11 +18,12 @@
 // that is not there are masked; their values are set to 0 in shared memory, so that
 // what they hold does not matter.
 //
-// Scores are mma.sync products (m16n8k16): a decode step's 8 rows fill half of the
-// 16 rows of the instruction, and the other half holds the rows' low-order parts, so q
-// (fp32 as fp16 high + low) and the probabilities enter with twice the bits at no further
-// instruction.  (tcgen05 needs 64 or 128 rows, of which 1 to 8 would hold work, while
-// the tensor time here is a fraction of the memory time.)
+// Scores and results are mma.sync products (m16n8k16) in transposed form, S^T = K q^T and
+// O^T = V^T P^T: positions and dimensions fill the 16 rows and the 8 query rows the 8
+// columns, so that no part of an instruction is empty and a warp's results take 32 to 64
+// registers.  Where fp16 or bf16 does not hold q (fp32) or the probabilities (fp32 results, bf16
+// caches), a second product adds what the rounding left.  (tcgen05 needs 64 or 128 query
+// rows, of which 1 to 8 would hold work.)
 #include "attend_dev.cuh"
 
 namespace sd {
@@ -32,7 +33,7 @@ constexpr int kWarps = 8, kLoaders = 3, kMergers = kSplitRows / 2, kConsumers = 
 constexpr int kThreads = kConsumers + 32 * (kLoaders + 1 + kMergers);
 // Registers of a thread: 512 x 128 at launch = 256 x 176 + 256 x 80
 constexpr int kConsumerRegs = 176, kOtherRegs = 80;
-static_assert(kLoaders + 1 == 4 && kMergers == 4, "warpgroups");
+static_assert(kLoaders + 1 == 4 && kMergers == 4 && kWarps % 4 == 0, "warpgroups");
 static_assert(kConsumers * kConsumerRegs + (kThreads - kConsumers) * kOtherRegs <= kThreads * 128, "the shares exceed what the block was launched with");
 
 struct alignas(128) SplitArgs {
@@ -101,10 +102,20 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // high and low product; an infinite high product has no low one (0 * inf)
 __device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? hi + lo : hi; }
 
-__device__ __forceinline__ float2 load2(const void* p, int64_t i, int dt) {
-    if (dt == SD_F32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
-    if (dt == SD_F16) return __half22float2(*reinterpret_cast<const __half2*>(static_cast<const __half*>(p) + i));
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(p) + i));
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t at) {
+    uint32_t x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ float2 lds2(uint32_t at) {
+    float2 x;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
+    return x;
 }
 // N (2 or 4) consecutive elements
 template <int N>
@@ -135,9 +146,13 @@ struct Shape {
     static constexpr int kChunk = kRow >= 256 ? 16 : 32;        // positions of a warp
     static constexpr int kTile = kChunk * kWarps;
     static constexpr int kStage = kTile * kRow;                 // the keys, or the values, of a tile
-    static constexpr int kMerge = kWarps * kSplitRows * (HD + 2) * 4;
+    static constexpr int kPitch = HD + 4;                       // floats of a row of results: no bank conflicts between heads
+    static constexpr int kMerge = kWarps * kSplitRows * (kPitch + 2) * 4;
     static constexpr int kQueries = kSplitRows * HD * 4;        // a unit's queries, in their own type
     static constexpr int kStages = kStage >= 32768 ? 5 : 10;
+    // A loader waits for the stage `kStages` before its own by parity, so the one 2 kStages before must be known to be
+    // free: it is, as every warp takes every tile in order and the loader has waited for a later one, 2 kLoaders - 1 before.
+    static_assert(kStages >= 2 * kLoaders - 1, "a loader could mistake the phase of a stage");
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kRing + kMerge + kUnits * kQueries + 1024;
     // What beginning and ending a unit costs, in tiles: the share of a block counts it
@@ -160,7 +175,7 @@ struct Unit {
 template <int HD, int KV>
 __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_constant__ SplitArgs args) {
     using S = Shape<HD, KV>;
-    constexpr int kSteps = HD / 16, kOut = HD / 8, kChunk = S::kChunk, kTile = S::kTile, kSt = S::kStages;
+    constexpr int kSteps = HD / 16, kOut = HD / 16, kChunk = S::kChunk, kTile = S::kTile, kSt = S::kStages;
     const AttendArgs& a = args.a;
     extern __shared__ unsigned char smraw[];
     __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt];
@@ -328,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     };
 
     float* s_o = reinterpret_cast<float*>(smem + S::kRing);              // [warp][row][HD]
-    float* s_m = s_o + kWarps * kSplitRows * HD;                          // [warp][row]
+    float* s_m = s_o + kWarps * kSplitRows * S::kPitch;                         // [warp][row]
     float* s_l = s_m + kWarps * kSplitRows;
     unsigned char* s_q = smem + S::kRing + S::kMerge;                      // [unit][row][HD] of the queries' type
     const int qbytes = a.dtype == SD_F32 ? 4 : 2;
@@ -366,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                         if (mw_[w] == -INFINITY) continue;
                         const float f = ex2(mw_[w] - mm[e]);
                         ll[e] = fmaf(f, s_l[w * kSplitRows + r], ll[e]);
-                        const float* so = s_o + (w * kSplitRows + r) * HD + lane * kVec;
+                        const float* so = s_o + (w * kSplitRows + r) * S::kPitch + lane * kVec;
 #pragma unroll
                         for (int x = 0; x < kVec; ++x) val[e][x] = fmaf(f, so[x], val[e][x]);
                     }
@@ -428,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (e >= n_rows) break;
-                    const int64_t m = u.m0 + 2 * mw + e, qi = quot(m, G), h = (int64_t)u.g * G + (m - qi * G);
+                    const int64_t m = u.m0 + 2 * mw + e, qi = a.Lq == 1 ? 0 : quot(m, G), h = (int64_t)u.g * G + (m - qi * G);
                     const int64_t at = u.b * a.o_batch + qi * a.o_stride + h * HD + lane * kVec;
                     const float inv = ll[e] == 0.f ? 0.f : vs / ll[e];
 #pragma unroll
@@ -449,16 +464,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 const uint32_t slot = n % kUnits;
                 if (n >= kUnits) ok = warp_wait(smem_u32(&s_uempty[slot]), (n / kUnits - 1) & 1, bad);
                 if (!ok) break;
+                // rows of cols 16-byte pieces; four loads of a lane in flight together
                 const int cols = HD * qbytes / 16;
-                for (int x = lane; x < kSplitRows * cols; x += 32) {
-                    const int r = x / cols, c = x - r * cols;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < p.rows) {
-                        const int64_t m = p.m0 + r, qi = quot(m, G);
-                        const int64_t at = p.b * a.q_batch + qi * a.q_stride + ((int64_t)p.g * G + (m - qi * G)) * HD;
-                        v = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at * qbytes + c * 16);
+                for (int x0 = lane; x0 < kSplitRows * cols; x0 += 128) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int x = x0 + y * 32, r = x / cols, c = x - r * cols;
+                        v[y] = make_uint4(0, 0, 0, 0);
+                        if (r < p.rows) {
+                            const int64_t m = p.m0 + r, qi = a.Lq == 1 ? 0 : quot(m, G);
+                            const int64_t at = p.b * a.q_batch + qi * a.q_stride + ((int64_t)p.g * G + (m - qi * G)) * HD;
+                            v[y] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + at * qbytes + c * 16);
+                        }
                     }
-                    *reinterpret_cast<uint4*>(s_q + slot * S::kQueries + x * 16) = v;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int x = x0 + y * 32;
+                        if (x < kSplitRows * cols) *reinterpret_cast<uint4*>(s_q + slot * S::kQueries + x * 16) = v[y];
+                    }
                 }
                 if (lane == 0) s_unit[slot] = p;
                 __syncwarp();
@@ -488,33 +512,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             int i = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(i, 0);
             for (; i < p.tiles && ok; i += kLoaders) {
                 const int first = (p.i0 + i) * kTile, rest = p.len - first;
-                int id[kTile / 32], in[kTile / 32], mine_boxes = 0;
-                id[0] = ahead;
-#pragma unroll
-                for (int k = 1; k < kTile / 32; ++k) id[k] = k * 32 < groups ? lookup(i, k) : -1;
+                // of a box: its position within its page (or row)
+                auto inside = [&](int k) -> int {
+                    const int pos = first + (k * 32 + lane) * box;
+                    return a.table ? pos - (int)(a.by_ps.div((uint32_t)pos) * a.by_ps.d) : pos;
+                };
+                const int id0 = (uint32_t)ahead < (uint32_t)outer ? ahead : -1, in0 = inside(0);
                 ahead = lookup(i + kLoaders, 0);                          // a tile ahead: not waited for here
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k) {
-                    if ((uint32_t)id[k] >= (uint32_t)outer) id[k] = -1;
-                    in[k] = first + (k * 32 + lane) * box;
-                    if (a.table) in[k] -= (int)(a.by_ps.div((uint32_t)in[k]) * a.by_ps.d);
-                    mine_boxes += id[k] >= 0;
-                }
-                const int all = __reduce_add_sync(0xffffffffu, mine_boxes);
-#pragma unroll
+#pragma unroll 1
                 for (int op = 0; op < 2; ++op) {
                     const uint32_t st = 2 * (n + i) + op, slot = st % kSt, turn = st / kSt;
                     if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
                     if (!ok) break;
                     last = st + 1;
                     const uint32_t mb = smem_u32(&s_full[slot]), dst = ring + slot * S::kStage;
-                    if (op == 0) {
-                        // live positions of each chunk
-                        if (lane < kWarps) s_live[slot][lane] = 0;
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < kTile / 32; ++k) {
-                            if (id[k] < 0) continue;
+                    if (op == 0 && lane < kWarps) s_live[slot][lane] = 0;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int k = 0; k * 32 < groups; ++k) {
+                        int id = id0, in = in0;
+                        if (k > 0) {
+                            id = lookup(i, k);
+                            if ((uint32_t)id >= (uint32_t)outer) id = -1;
+                            in = inside(k);
+                        }
+                        if (op == 0 && id >= 0) {
+                            // live positions of each warp's part of the tile
                             const int at = (k * 32 + lane) * box, end = min(at + box, rest);
                             for (int r = at; r < end;) {
                                 const int c = r / kChunk, stop = min(end, (c + 1) * kChunk), count = stop - r;
@@ -522,21 +545,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                                 r = stop;
                             }
                         }
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        if (all) mb_expect(mb, all * box * S::kRow);
-                        else mb_arrive(mb);
+                        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+                        if (lane == 0 && have) mb_expect_more(mb, __popc(have) * box * S::kRow);
+                        // box by box from one lane: loads by several lanes of a warp at once took 250 cycles each
+                        for (int y = 0; y < min(32, groups - k * 32); ++y) {
+                            const int page = __shfl_sync(0xffffffffu, id, y), pos = __shfl_sync(0xffffffffu, in, y);
+                            if (lane == 0 && page >= 0) {
+                                const uint32_t to = dst + (k * 32 + y) * box * S::kPart;
+#pragma unroll
+                                for (int part = 0; part < S::kParts; ++part)
+                                    tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, pos, p.g, page, mb);
+                            }
+                        }
                     }
                     __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < kTile / 32; ++k) {
-                        if (id[k] < 0) continue;
-                        const uint32_t to = dst + (k * 32 + lane) * box * S::kPart;
-#pragma unroll
-                        for (int part = 0; part < S::kParts; ++part)
-                            tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, in[k], p.g, id[k], mb);
-                    }
+                    if (lane == 0) mb_arrive(mb);
                 }
             }
             n += max(p.tiles, 0);
@@ -556,27 +579,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     // Low-order parts: of q where the products' type does not hold it (a 16-bit q scaled into fp16 loses only what is
     // 2^-24 of its row's largest element); of the probabilities for fp32 results and where bf16 is all they have
     const bool q_low = a.dtype == SD_F32 || (S::kBf && a.dtype == SD_F16), p_low = a.dtype == SD_F32 || S::kBf;
-    uint32_t n = 0;                                                       // chunks of the units before (whole tiles)
+    uint32_t n = 0;                                                       // tiles of the units before
     for (uint32_t nu = 0;; ++nu) {
         // a failed wait (flagged) ends the waiting, and with it the walk
         bool ok = warp_wait(smem_u32(&s_ufull[nu % kUnits]), (nu / kUnits) & 1, bad);
         const Unit pc = s_unit[nu % kUnits];
         if (!ok || !pc.rows) break;
         const int g = pc.g, rows = pc.rows;
-        // ---- queries of this lane: a row, 4 elements of each 16
-        float2 x[kSteps][2];
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                x[k][e] = load2(s_q + nu % kUnits * S::kQueries, row * HD + 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e), a.dtype);
-        __syncwarp();
-        if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
-        // ---- rows 0-7 of the A operand: the rounded rows; rows 8-15: what the rounding left
-        uint32_t qa[kSteps][4];
-        float row_scale = a.scale * kLog2e * (a.k_scale ? __ldcg(a.k_scale + g) : 1.f);
+        // ---- the B operand: head `row` of the unit, 4 elements of each 16 a lane
+        uint32_t qh[kSteps][2], ql[kSteps][2];
+        float scale[2];                                                   // of this lane's two columns of the scores
         {
-            float down = 1.f;
+            float2 x[kSteps][2];
+            const uint32_t at = smem_u32(s_q) + nu % kUnits * S::kQueries;
+            if (a.dtype == SD_F32) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) x[k][e] = lds2(at + 4 * (row * HD + 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e)));
+            } else {
+                uint32_t w[kSteps][2];
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) w[k][e] = lds1(at + 2 * (row * HD + 16 * k + (S::kE4 ? 4 * quad + 2 * e : 2 * quad + 8 * e)));
+                const bool bf = a.dtype == SD_BF16;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[k][e] = bf ? make_float2(__uint_as_float(w[k][e] << 16), __uint_as_float(w[k][e] & 0xffff0000u))
+                                     : __half22float2(*reinterpret_cast<const __half2*>(&w[k][e]));
+            }
+            __syncwarp();
+            if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
+            float down = 1.f, row_scale = a.scale * kLog2e * (a.k_scale ? __ldcg(a.k_scale + g) : 1.f);
             if (!S::kBf && a.dtype != SD_F16) {
                 // wider exponents than fp16's: the row by a power of two to a largest element in [1, 2)
                 float mx = 0.f;
@@ -595,121 +632,124 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qa[k][2 * e], qa[k][2 * e + 1]);
+                for (int e = 0; e < 2; ++e) split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qh[k][e], ql[k][e]);
+            scale[0] = __shfl_sync(0xffffffffu, row_scale, 8 * quad);
+            scale[1] = __shfl_sync(0xffffffffu, row_scale, 8 * quad + 4);
         }
+        // this lane's results: heads 2 quad and 2 quad + 1, dimensions `row` and `row` + 8 of each 16 (e4m3: 2 row, 2 row + 1)
         float o[kOut][4];
 #pragma unroll
         for (int y = 0; y < kOut; ++y) o[y][0] = o[y][1] = o[y][2] = o[y][3] = 0.f;
-        float mrow = -INFINITY, lrow = 0.f;
-
-        // ---- this warp's chunks: every kWarps-th of the block's, eight to a tile
-        constexpr int kN = kChunk / 8, kH = kChunk / 16;                  // products of 8, halves of 16 positions
-        constexpr int kBlocks = kSteps * kH / (S::kE4 ? 2 : 1);           // of one ldmatrix each, as many for P V
-        static_assert(kBlocks == kH * kOut / (S::kE4 ? 4 : 2), "scores and results have as many blocks");
-        float sc[kN][4];
-        uint32_t pa[kH][4];
-        int r0 = 0;                                                       // first position of the chunk in its tile
-        auto score_block = [&](int u, uint32_t kb) {
-            uint32_t f[4];
-            if constexpr (!S::kE4) {
-                const int k = u / kH, h = u % kH;
-                ldm4(kb + S::at(r0 + 16 * h + (mi >> 1) * 8 + mr, 2 * k + (mi & 1)), f);
-                mma<S::kBf>(sc[2 * h], qa[k], f[0], f[1]);
-                mma<S::kBf>(sc[2 * h + 1], qa[k], f[2], f[3]);
-            } else {
-                const int k = 2 * (u / kH), h = u % kH;
-                ldm4(kb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, k + (mi >> 1)), f);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mma<false>(sc[2 * h], qa[k + e], half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e] >> 16));
-                    mma<false>(sc[2 * h + 1], qa[k + e], half2_of_e4m3(f[2 * e + 1]), half2_of_e4m3(f[2 * e + 1] >> 16));
-                }
-            }
-        };
-        auto result_block = [&](int u, uint32_t vb) {
-            uint32_t f[4];
-            if constexpr (!S::kE4) {
-                const int h = u / (kOut / 2), x = u % (kOut / 2) * 2;
-                ldm4t(vb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, x + (mi >> 1)), f);
-                mma<S::kBf>(o[x], pa[h], f[0], f[1]);
-                mma<S::kBf>(o[x + 1], pa[h], f[2], f[3]);
-            } else {
-                // a transposed matrix of byte pairs: even dimensions in the low bytes, odd ones in the high
-                const int h = u / (kOut / 4), x = u % (kOut / 4) * 4;
-                ldm4t(vb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, x / 2 + (mi >> 1)), f);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mma<false>(o[x + 2 * e], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)),
-                               half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)));
-                    mma<false>(o[x + 2 * e + 1], pa[h], half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
-                               half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431)));
-                }
-            }
-        };
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         auto release = [&](uint32_t slot) {
             __syncwarp();
             if (lane == 0) mb_arrive(smem_u32(&s_empty[slot]));
         };
-        for (int c = (int)((warp + kWarps - n % kWarps) % kWarps); c < pc.tiles * kWarps; c += kWarps) {
-            const uint32_t st = 2 * ((n + c) / kWarps), sk = st % kSt, sv = (st + 1) % kSt;
+
+        // ---- this warp's eighth of every tile
+        constexpr int kH = kChunk / 16;
+        const int r0 = warp * kChunk;                                     // its first position in a tile
+        for (int i = 0; i < pc.tiles; ++i) {
+            const uint32_t st = 2 * (n + i), sk = st % kSt, sv = (st + 1) % kSt;
             const uint32_t kb = ring + sk * S::kStage, vb = ring + sv * S::kStage;
-            r0 = c % kWarps * kChunk;
             warp_wait(smem_u32(&s_full[sk]), (st / kSt) & 1, bad);
-            const uint32_t live = s_live[sk][c % kWarps];
+            const uint32_t live = s_live[sk][warp];
             if (!live) {                                                  // nothing here
                 release(sk);
                 warp_wait(smem_u32(&s_full[sv]), ((st + 1) / kSt) & 1, bad);
                 release(sv);
                 continue;
             }
+            // S^T = K q^T: rows are positions 16 h + row and + 8, columns this lane's heads
+            float s[kH][4];
+            auto scores = [&](const uint32_t (&q)[kSteps][2], float (&d)[kH][4]) {
 #pragma unroll
-            for (int y = 0; y < kN; ++y) sc[y][0] = sc[y][1] = sc[y][2] = sc[y][3] = 0.f;
+                for (int h = 0; h < kH; ++h) d[h][0] = d[h][1] = d[h][2] = d[h][3] = 0.f;
+                if constexpr (!S::kE4) {
 #pragma unroll
-            for (int u = 0; u < kBlocks; ++u) score_block(u, kb);
-            release(sk);
-            // this lane's scores: row `row`, positions 8j + 2 quad and the next
-            float p[kN][2], mx = -INFINITY;
+                    for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-            for (int y = 0; y < kN; ++y)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) p[y][e] = (q_low ? add_low(sc[y][e], sc[y][2 + e]) : sc[y][e]) * row_scale;
-            if (live != 0xffffffffu >> (32 - kChunk)) {
-                const uint32_t lv = live >> (2 * quad);
-#pragma unroll
-                for (int y = 0; y < kN; ++y)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (!((lv >> (8 * y + e)) & 1)) p[y][e] = -INFINITY;
-            }
-#pragma unroll
-            for (int y = 0; y < kN; ++y) mx = max_nan(mx, max_nan(p[y][0], p[y][1]));
-            if (mx != mx) mx = INFINITY;                                  // NaN reaches every result of its row
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(mrow, mx);
-            if (__any_sync(0xffffffffu, mn > mrow)) {
-                const float keep = mrow == -INFINITY ? 0.f : ex2(mrow - mn);
-                lrow *= keep;
-#pragma unroll
-                for (int x = 0; x < kOut; ++x) {
-                    o[x][0] *= keep; o[x][1] *= keep;
-                    o[x][2] *= keep; o[x][3] *= keep;
-                }
-                mrow = mn;
-            }
-            const float ref = mrow == -INFINITY ? 0.f : mrow - S::kShift;
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                const float p0 = ex2(p[j][0] - ref), p1 = ex2(p[j][1] - ref);
-                lrow += p0 + p1;
-                if (p_low) {
-                    split2<S::kBf>(p0, p1, pa[j / 2][2 * (j & 1)], pa[j / 2][2 * (j & 1) + 1]);
+                        for (int h = 0; h < kH; ++h) {
+                            uint32_t f[4];
+                            ldm4(kb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, 2 * k + (mi >> 1)), f);
+                            mma<S::kBf>(d[h], f, q[k][0], q[k][1]);
+                        }
                 } else {
-                    pa[j / 2][2 * (j & 1)] = round2<S::kBf>(p0, p1);
-                    pa[j / 2][2 * (j & 1) + 1] = 0;
+#pragma unroll
+                    for (int k = 0; k < kSteps; k += 2)
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) {
+                            uint32_t f[4];
+                            ldm4(kb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, k + (mi >> 1)), f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t x[4] = {half2_of_e4m3(f[2 * e]), half2_of_e4m3(f[2 * e + 1]),
+                                                       half2_of_e4m3(f[2 * e] >> 16), half2_of_e4m3(f[2 * e + 1] >> 16)};
+                                mma<false>(d[h], x, q[k + e][0], q[k + e][1]);
+                            }
+                        }
                 }
+            };
+            scores(qh, s);
+            if (q_low) {
+                float d[kH][4];
+                scores(ql, d);
+#pragma unroll
+                for (int h = 0; h < kH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[h][e] = add_low(s[h][e], d[h][e]);
             }
+            release(sk);
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[h][e] *= scale[e & 1];
+            if (live != 0xffffffffu >> (32 - kChunk)) {
+#pragma unroll
+                for (int h = 0; h < kH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((live >> (16 * h + 8 * (e >> 1) + row)) & 1)) s[h][e] = -INFINITY;
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mx[e] = max_nan(mx[e], max_nan(s[h][e], s[h][2 + e]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mx[e] = max_nan(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mx[e] = mx[e] == mx[e] ? fmaxf(mx[e], m[e]) : INFINITY;   // NaN reaches every result of its row
+            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    keep[e] = m[e] == -INFINITY ? 0.f : ex2(m[e] - mx[e]);
+                    l[e] *= keep[e];
+                    m[e] = mx[e];
+                }
+#pragma unroll
+                for (int x = 0; x < kOut; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[x][e] *= keep[e & 1];
+            }
+            float ref[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e] - S::kShift;
+            // P^T as the B operand: each 8 positions x 8 heads transposed
+            uint32_t ph[kH][2], pl[kH][2];
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float p0 = ex2(s[h][2 * y] - ref[0]), p1 = ex2(s[h][2 * y + 1] - ref[1]);
+                    l[0] += p0;
+                    l[1] += p1;
+                    split2<S::kBf>(p0, p1, ph[h][y], pl[h][y]);
+                    ph[h][y] = transpose8(ph[h][y]);
+                }
             warp_wait(smem_u32(&s_full[sv]), ((st + 1) / kSt) & 1, bad);
             if (live != 0xffffffffu >> (32 - kChunk)) {
                 // values of positions that are not there: 0, whatever lies in memory
@@ -721,31 +761,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
+            // O^T += V^T P^T
+            auto results = [&](const uint32_t (&p)[kH][2]) {
+                if constexpr (!S::kE4) {
 #pragma unroll
-            for (int u = 0; u < kBlocks; ++u) result_block(u, vb);
+                    for (int h = 0; h < kH; ++h)
+#pragma unroll
+                        for (int x = 0; x < kOut; ++x) {
+                            uint32_t f[4];
+                            ldm4t(vb + S::at(r0 + 16 * h + (mi >> 1) * 8 + mr, 2 * x + (mi & 1)), f);
+                            mma<S::kBf>(o[x], f, p[h][0], p[h][1]);
+                        }
+                } else {
+                    // a transposed matrix of byte pairs: even dimensions in the low bytes, odd ones in the high
+#pragma unroll
+                    for (int h = 0; h < kH; ++h)
+#pragma unroll
+                        for (int x = 0; x < kOut; x += 2) {
+                            uint32_t f[4];
+                            ldm4t(vb + S::at(r0 + 16 * h + (mi & 1) * 8 + mr, x + (mi >> 1)), f);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t y[4] = {half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4420)), half2_of_e4m3(__byte_perm(f[2 * e], 0, 0x4431)),
+                                                       half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4420)), half2_of_e4m3(__byte_perm(f[2 * e + 1], 0, 0x4431))};
+                                mma<false>(o[x + e], y, p[h][0], p[h][1]);
+                            }
+                        }
+                }
+            };
+            results(ph);
+            if (p_low) {
+#pragma unroll
+                for (int h = 0; h < kH; ++h)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) pl[h][y] = transpose8(pl[h][y]);
+                results(pl);
+            }
             release(sv);
         }
-        n += pc.tiles * kWarps;
+        n += max(pc.tiles, 0);
 
         // ---- the warps' results
         if (nu > 0) warp_wait(smem_u32(&s_free), (nu - 1) & 1, bad);
-        lrow += __shfl_xor_sync(0xffffffffu, lrow, 1);
-        lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
-        if (quad == 0) {
-            s_m[warp * kSplitRows + row] = mrow;
-            s_l[warp * kSplitRows + row] = lrow;
-        }
-        float* so = s_o + (warp * kSplitRows + row) * HD;
-        if (row < rows && mrow != -INFINITY) {
 #pragma unroll
-            for (int x = 0; x < kOut; ++x) {
-                const float v0 = add_low(o[x][0], o[x][2]), v1 = add_low(o[x][1], o[x][3]);
-                if constexpr (S::kE4) {
-                    const int d = 16 * (x / 2) + 4 * quad + (x & 1);
-                    so[d] = v0;
-                    so[d + 2] = v1;
-                } else {
-                    *reinterpret_cast<float2*>(so + 8 * x + 2 * quad) = make_float2(v0, v1);
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+            const int head = 2 * quad + e;
+            if (row == 0) {
+                s_m[warp * kSplitRows + head] = m[e];
+                s_l[warp * kSplitRows + head] = l[e];
+            }
+            float* so = s_o + (warp * kSplitRows + head) * S::kPitch;
+            if (head < rows && m[e] != -INFINITY) {
+#pragma unroll
+                for (int x = 0; x < kOut; ++x) {
+                    so[16 * x + (S::kE4 ? 2 * row : row)] = o[x][e];
+                    so[16 * x + (S::kE4 ? 2 * row + 1 : row + 8)] = o[x][2 + e];
                 }
             }
         }
