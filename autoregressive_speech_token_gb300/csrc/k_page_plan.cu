@@ -19,7 +19,7 @@
 namespace sd {
 namespace {
 
-constexpr int kThreads = 512, kTok = 1024, kWords = kTok / 32;
+constexpr int kThreads = 512, kTok = 512, kWords = kTok / 32;
 enum { BIT_ROWS = 1, BIT_FREE = 2, BIT_WIDE = 4, BIT_NEG = 8 };
 
 struct PlanArgs {
@@ -55,6 +55,7 @@ __device__ __forceinline__ Request request(const PlanArgs& a, int r) {
 
 __device__ __forceinline__ int32_t clip(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int32_t)v; }
 
+template <int kOwn>
 __global__ void __launch_bounds__(kThreads) k_page_plan(const PlanArgs a) {
     pdl_trigger();
     pdl_wait();
@@ -71,11 +72,23 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(const PlanArgs a) {
 
     int64_t tok0 = 0, page0 = 0;   // tokens and pages of the requests before this round's
     int32_t flags = 0, longest = 0;
-    for (int r0 = 0, round = 0; r0 < a.R; r0 += kThreads, ++round) {
-        const int r = r0 + tid;
-        Request q = {};
-        if (r < a.R) q = request(a, r);
-        int64_t t = q.fresh, p = q.take;
+    int round = 0;
+    for (int64_t r0 = 0; r0 < a.R; r0 += kThreads * kOwn, ++round) {
+        // kOwn consecutive requests a thread: one exchange between the threads for all of them
+        const int64_t first_r = r0 + tid * kOwn;
+        Request q[kOwn] = {};
+        int64_t t = 0, p = 0;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (first_r + k < a.R) q[k] = request(a, (int)(first_r + k));
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            t += q[k].fresh;
+            p += q[k].take;
+            flags |= q[k].flags;
+            longest = max(longest, clip(q[k].total));
+        }
+        const int64_t own_t = t, own_p = p;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t tt = __shfl_up_sync(0xffffffffu, t, o), pp = __shfl_up_sync(0xffffffffu, p, o);
@@ -89,35 +102,35 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(const PlanArgs a) {
             s_page[warp] = p;
         }
         __syncthreads();
-        int64_t bt = tok0, bp = page0, allt = 0, allp = 0;
+        int64_t start = tok0 + t - own_t, first = page0 + p - own_p;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             const int64_t x = s_tok[w], y = s_page[w];
             if (w < warp) {
-                bt += x;
-                bp += y;
+                start += x;
+                first += y;
             }
-            allt += x;
-            allp += y;
+            tok0 += x;
+            page0 += y;
         }
-        const int64_t start = bt + t - q.fresh, first = bp + p - q.take;
-        tok0 += allt;
-        page0 += allp;
-        flags |= q.flags;
-        longest = max(longest, clip(q.total));
-        if (r < a.R) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const int64_t r = first_r + k;
+            if (r >= a.R) break;
             if (round % gridDim.x == blockIdx.x) {
-                a.total[r] = clip(q.total);
+                a.total[r] = clip(q[k].total);
                 a.start[r] = clip(start);
             }
-            if (q.fresh > 0 && start < hi && start + q.fresh > lo) {
+            if (q[k].fresh > 0 && start < hi && start + q[k].fresh > lo) {
                 const int at = start > lo ? (int)(start - lo) : 0;
                 atomicOr(&s_mark[at >> 5], 1u << (at & 31));
-                s_req[at] = r;
-                s_len[at] = q.len;
+                s_req[at] = (int32_t)r;
+                s_len[at] = q[k].len;
                 s_off[at] = (int32_t)(lo + at - start);          // tokens of the request before this one
                 s_first[at] = clip(first);
             }
+            start += q[k].fresh;
+            first += q[k].take;
         }
         __syncthreads();
     }
@@ -127,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(const PlanArgs a) {
     }
     // the last mark before each group of 32 tokens
     if (warp == 0) {
-        const uint32_t m = s_mark[lane];
+        const uint32_t m = lane < kWords ? s_mark[lane] : 0;
         int32_t last = m ? lane * 32 + 31 - __clz(m) : -1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -135,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(const PlanArgs a) {
             if (lane >= o) last = max(last, x);
         }
         const int32_t before = __shfl_up_sync(0xffffffffu, last, 1);
-        s_prev[lane] = lane ? before : -1;
+        if (lane < kWords) s_prev[lane] = lane ? before : -1;
     }
     __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
@@ -205,7 +218,11 @@ extern "C" int sd_page_plan(const int32_t* len_dev, const int32_t* new_dev, int3
     a.R = R; a.n_free = n_free; a.width = table_stride; a.rows = rows; a.ps = (uint32_t)page_size;
     a.by_ps = FastDiv((uint32_t)page_size);
     const int grid = rows > kTok ? (int)(((int64_t)rows + kTok - 1) / kTok) : 1;
-    cudaError_t e = launch_k(k_page_plan, dim3(grid), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+    // Requests of a thread: one where the threads suffice (16 requests: 3.1 us, 4.0 us with four), else four, which
+    // saves exchanges between the threads (2000 requests, 61k tokens: 5.0 us, 8.0 us with one and 1024 tokens a block).
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = R <= kThreads ? launch_k(k_page_plan<1>, dim3(grid), dim3(kThreads), 0, st, a)
+                                        : launch_k(k_page_plan<4>, dim3(grid), dim3(kThreads), 0, st, a);
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return SD_OK;
 }

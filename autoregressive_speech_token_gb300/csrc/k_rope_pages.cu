@@ -8,10 +8,11 @@
 // to the nearest quarter turn, leave |r| <= 1/8 turn, which fp32 holds to 2^-28
 // of a turn, and sincospif of it gives cos and sin to about their last bit.
 //
-// The call moves its data once and is bound by memory.  A block takes a few tokens:
-// their sines and cosines are formed once, in shared memory, for all heads,
-// while the block's first loads are in flight; then each thread rotates 8 pairs
-// of one head per step with 16-byte loads and stores.
+// The call moves its data once and is bound by memory.  A block takes one or two tokens:
+// their sines and cosines are formed once, in shared memory, for all heads, while the
+// block's first loads are in flight; then each thread rotates 8 pairs of one head per
+// step with 16-byte loads and stores.  30011 tokens (483 MB) take 81 us, 0.88 of the copy rate,
+// into single positions of random pages.
 #include <cmath>
 
 #include "pages_dev.cuh"
@@ -19,7 +20,6 @@
 namespace sd {
 namespace {
 
-constexpr int kThreads = 256;
 
 struct RopeArgs {
     sd_rope rope;
@@ -85,7 +85,7 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
     }
 }
 
-template <typename T, typename TC, int HD>
+template <typename T, typename TC, int HD, int kThreads>
 __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__ RopeArgs a, int tokens) {
     constexpr int kHalf = HD / 2, kChunks = kHalf / 8;   // 8-pair chunks of a head
     pdl_trigger();
@@ -94,6 +94,28 @@ __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * tokens;
     const int nt = min(tokens, a.n - t0);
+    const int heads = a.H + 2 * a.c.n_kv_head, per = heads * kChunks;   // work items of a token: q, k and v heads
+    const int items = nt * per;
+    float x[8], y[8];
+    int32_t slot = -1;
+    auto place = [&](int i, int& t, int& head, int& d) {
+        t = i / per;
+        const int j = i - t * per;
+        head = j / kChunks;
+        d = (j - head * kChunks) * 8;
+    };
+    auto load = [&](int i) {
+        int t, head, d;
+        place(i, t, head, d);
+        const int64_t tok = t0 + t;
+        slot = a.slot[tok];
+        const T* src = head < a.H ? static_cast<const T*>(a.q) + tok * a.q_stride + head * HD
+                       : head < a.H + a.c.n_kv_head ? static_cast<const T*>(a.k) + tok * a.kv_stride + (head - a.H) * HD
+                                                    : static_cast<const T*>(a.v) + tok * a.kv_stride + (head - a.H - a.c.n_kv_head) * HD;
+        load8(src + d, x);
+        load8(src + d + kHalf, y);
+    };
+    if (tid < items) load(tid);
     if (a.rotate) {
         for (int i = tid; i < nt * kHalf; i += kThreads) {
             const int t = i / kHalf, p = i - t * kHalf;
@@ -109,21 +131,12 @@ __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__
         }
         __syncthreads();
     }
-    const int per = (a.H + 2 * a.c.n_kv_head) * kChunks;  // work items of a token: q, k and v heads
-    for (int i = tid; i < nt * per; i += kThreads) {
-        const int t = i / per, j = i - t * per;
-        const int head = j / kChunks, d = (j - head * kChunks) * 8;
-        const int64_t tok = t0 + t;
-        const int32_t slot = a.slot[tok];
+    for (int i = tid; i < items; i += kThreads) {
+        if (i != tid) load(i);
         if (slot < 0 || slot >= a.slots) continue;
-        float x[8], y[8];
+        int t, head, d;
+        place(i, t, head, d);
         const bool is_q = head < a.H, is_k = !is_q && head < a.H + a.c.n_kv_head;
-        const int g = is_q ? head : is_k ? head - a.H : head - a.H - a.c.n_kv_head;
-        const T* src = is_q ? static_cast<const T*>(a.q) + tok * a.q_stride
-                            : static_cast<const T*>(is_k ? a.k : a.v) + tok * a.kv_stride;
-        src += g * HD + d;
-        load8(src, x);
-        load8(src + kHalf, y);
         if (a.rotate && (is_q || is_k)) {
             const float* cs = s_cs + t * HD + d;
 #pragma unroll
@@ -135,13 +148,13 @@ __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__
             }
         }
         if (is_q) {
-            T* dst = static_cast<T*>(a.q_out) + tok * a.qo_stride + g * HD + d;
+            T* dst = static_cast<T*>(a.q_out) + (int64_t)(t0 + t) * a.qo_stride + head * HD + d;
             store8(dst, x);
             store8(dst + kHalf, y);
         } else {
+            const int g = is_k ? head - a.H : head - a.H - a.c.n_kv_head;
             const uint32_t page = a.by_ps.div((uint32_t)slot);
-            const int64_t off = page * a.c.page_stride + (slot - page * a.by_ps.d) * a.c.pos_stride +
-                                g * a.c.head_stride + d;
+            const int64_t off = page * a.c.page_stride + (slot - page * a.by_ps.d) * a.c.pos_stride + g * a.c.head_stride + d;
             if constexpr (sizeof(TC) == 1) {
                 const float* sp = is_k ? a.c.k_scale_dev : a.c.v_scale_dev;
                 const float sc = sp ? sp[g] : 1.0f;
@@ -160,12 +173,18 @@ __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__
 
 template <typename T, typename TC>
 cudaError_t launch_hd(const RopeArgs& a, cudaStream_t st) {
-    // Two tokens a block; one where that leaves SMs without a block.
-    const int tokens = a.n > 512 ? 2 : 1;
+    // Many tokens: two to a block of 128 threads, so that an SM holds many blocks at different points (30011 tokens of
+    // 16 + 8 + 8 heads of 128, bf16: 81 us; 84 us with 256 threads and four tokens, 104 us with one token, 110 us with
+    // 512 threads).  Few tokens: one each and more threads, so that no thread takes a third piece.
+    const bool many = a.n > 512;
+    const int tokens = many ? 2 : 1;
     const dim3 grid((a.n + tokens - 1) / tokens);
     const size_t smem = sizeof(float) * tokens * a.c.head_dim;
-    return a.c.head_dim == 64 ? launch_k(k_rope_pages<T, TC, 64>, grid, dim3(kThreads), smem, st, a, tokens)
-                              : launch_k(k_rope_pages<T, TC, 128>, grid, dim3(kThreads), smem, st, a, tokens);
+    if (a.c.head_dim == 64)
+        return many ? launch_k(k_rope_pages<T, TC, 64, 128>, grid, dim3(128), smem, st, a, tokens)
+                    : launch_k(k_rope_pages<T, TC, 64, 256>, grid, dim3(256), smem, st, a, tokens);
+    return many ? launch_k(k_rope_pages<T, TC, 128, 128>, grid, dim3(128), smem, st, a, tokens)
+                : launch_k(k_rope_pages<T, TC, 128, 256>, grid, dim3(256), smem, st, a, tokens);
 }
 template <typename T>
 cudaError_t launch_cache(const RopeArgs& a, cudaStream_t st) {
