@@ -4,7 +4,7 @@
 
 #include "pages_dev.cuh"
 
-// Partial results of the split kernel: two records a block, one arrival counter.
+// Partial results: two records a block, arrival counters of 8 warps (either kernel's; calls do not overlap).
 // The counters are zero between calls (the last arriver of a unit clears its own).
 struct sd_attn_ws {
     int device = 0, sms = 0;
@@ -31,6 +31,7 @@ struct AttendArgs {
 
 constexpr int kSplitRows = 8;                                     // query rows of a unit
 constexpr int kSplitRecord = kSplitRows * (128 + 2);              // floats of a partial record
+constexpr int kTcRecord = 2 * 128 * (128 + 2);                    // of the tensor-core kernel: two tiles of 128 queries
 
 constexpr int kMaxPositions = INT32_MAX - 1023;                   // of a row: tile arithmetic stays within int32
 
@@ -87,6 +88,13 @@ __device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile i
 // The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
     return __all_sync(0xffffffffu, mb_wait(mb, parity, bad));
+}
+// One lane of a converged warp.  (The compiler keeps what such a branch computes in uniform registers, which a
+// comparison of lane numbers does not give.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int h, int r, int b, uint32_t mb) {
     asm volatile(

@@ -2,8 +2,10 @@
 // tcgen05 products with scores, probabilities and results in tensor memory.
 //
 // A work item is a pair of query tiles (128 queries of one head each) of one (row b,
-// kv head g), against all of that row's positions in tiles of 128.  One block per
-// SM walks the items; per position tile j and query tile i
+// kv head g), against all of that row's positions in tiles of 128.  One block per SM
+// takes whole items, or, where that would leave SMs idle for long, an even share of
+// the tiles of all items, and the parts of an item are joined by the last block to
+// arrive, in block order.  Per position tile j and query tile i
 //   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
 //   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
 //   O_i += P_i V_j (fp32, head_dim columns)
@@ -33,13 +35,14 @@ constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 // Registers of a thread: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72 (a softmax thread holds a row of 128 scores)
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
+constexpr int kLead = 1;                              // what beginning and ending an item costs, in tiles
+constexpr int kJoin = 6;                              // what joining the parts of items costs, in tiles
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
 
 struct alignas(128) TcArgs {
     CUtensorMap q, k, v;
     AttendArgs a;
     int32_t nq, pairs;                                // query tiles of a head, pairs of a (b, g)
-    int64_t items;
 };
 
 template <int HD>
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
     extern __shared__ unsigned char smraw[];
     __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_tail;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_row[32], s_len[32];
     const AttendArgs& a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sm = (smem_u32(smraw) + 1023u) & ~1023u;
@@ -207,19 +210,110 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
 
     const int G = a.H / a.Hkv;
     const int per_g = G * t.nq;                                    // query tiles of a (b, g)
+    // ---- this block's share, found by every warp for itself: whole items, or an even part of all tiles
+    auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
+    auto padded = [&](int len) { return (len + kN - 1) / kN + kLead; };
+    const int64_t per_b = (int64_t)a.Hkv * t.pairs, items = a.B * per_b;    // items of a row, of all
+    const int64_t grid = gridDim.x, rounds = (items + grid - 1) / grid;
+    int64_t all = 0;
+    int most = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int n = padded(length(b));
+        all += n;
+        most = max(most, n);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    all *= per_b;
+    // Whole items are taken in rounds, there and back over the blocks, the longest rows first where a warp can sort
+    // them.  A round takes as long as its longest item.
+    int64_t whole_cost = rounds * most;
+    const bool sorted = a.B <= 32;
+    if (sorted) {
+        const int mine = lane < a.B ? length(lane) : -1;
+        int rank = 0;
+        for (int x = 0; x < a.B; ++x) {
+            const int other = __shfl_sync(0xffffffffu, mine, x);
+            rank += other > mine || (other == mine && x < lane);
+        }
+        if (warp == 0 && lane < a.B) {
+            s_row[rank] = lane;
+            s_len[lane] = mine;
+        }
+        __syncthreads();
+        if (rounds <= 32) {
+            int64_t first = lane < rounds ? padded(s_len[s_row[(int)(lane * grid / per_b)]]) : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+            whole_cost = first;
+        }
+    }
+    const int64_t per = (all + grid - 1) / grid;
+    // Parts of items are even, but joining them costs as much as about kJoin tiles (777 queries over up to 1500 states
+    // of 8 rows and 16 heads of 64: 64 us cut evenly, 53 us whole; 8192 over 8190: 822 and 815 us).
+    const bool whole = whole_cost <= per + per / 16 + kJoin;
+    const int64_t t_begin = blockIdx.x * per, t_end = min(all, t_begin + per);
+    int64_t at = whole ? 0 : t_begin, base = 0;                    // whole: the next round; else: the next tile, row b_at's first
+    int b_at = a.B;
+    for (int b0 = 0; b0 < a.B && !whole; b0 += 32) {
+        const int64_t mine = b0 + lane < a.B ? padded(length(b0 + lane)) * per_b : 0;
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, base + sum - mine <= at && at < base + sum);
+        if (here) {
+            b_at = b0 + __ffs(here) - 1;
+            base += __shfl_sync(0xffffffffu, sum - mine, __ffs(here) - 1);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    // A piece: tiles [i0, i0 + tiles) of an item; c_lo .. c_hi the blocks with a part of its tiles.
     struct Item {
-        int b, g, len, tiles, first, two;
+        int b, g, len, i0, tiles, first, two, c_lo, c_hi, begins;
     };
-    auto item = [&](int64_t w) {
-        Item it;
-        const int64_t bg = w / t.pairs;
-        it.b = (int)(bg / a.Hkv);
-        it.g = (int)(bg - (int64_t)it.b * a.Hkv);
-        it.first = (int)(w - bg * t.pairs) * 2;
-        it.two = it.first + 1 < per_g;
-        it.len = min(max(a.len ? __ldcg(a.len + it.b) : a.max_len, 0), a.max_len);
-        it.tiles = (it.len + kN - 1) / kN;
-        return it;
+    auto next_item = [&](Item& p) -> bool {
+        int64_t u;                                                 // item of its row
+        if (whole) {
+            const int64_t w = at * grid + ((at & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+            if (w >= items) return false;
+            const int r = (int)(w / per_b);
+            u = w - r * per_b;
+            p.b = sorted ? s_row[r] : r;
+            p.len = sorted ? s_len[p.b] : length(p.b);
+            p.c_lo = p.c_hi = p.i0 = p.begins = 0;
+            p.tiles = padded(p.len) - kLead;
+            ++at;
+        } else {
+            if (at >= t_end) return false;
+            p.b = b_at;
+            p.len = sorted ? s_len[b_at] : length(b_at);
+            const int nt = padded(p.len);
+            u = (at - base) / nt;
+            const int64_t u0 = base + u * nt, next = min(u0 + nt, t_end);
+            const int64_t real = min(u0 + kLead, u0 + nt - 1);     // first tile (an empty row: its last empty one)
+            if (next <= real) return false;
+            p.c_lo = (int)(real / per);
+            p.c_hi = (int)((u0 + nt - 1) / per);
+            p.begins = real >= t_begin;
+            p.i0 = (int)max(at - u0 - kLead, (int64_t)0);
+            p.tiles = (int)(next - u0) - kLead - p.i0;
+            at = next;
+            if (next - base == nt * per_b) {
+                base = next;
+                ++b_at;
+            }
+        }
+        p.g = (int)(u / t.pairs);
+        p.first = (int)(u - (int64_t)p.g * t.pairs) * 2;
+        p.two = p.first + 1 < per_g;
+        return true;
     };
 
     if (warp >= kSoftWarps) {
@@ -229,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
         uint32_t n = 0, nq = 0, tail_n = 0;                        // tiles loaded, items; the last zeroed tile's number
         bool tails = false;
         bool ok = true;
-        for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
-            const Item it = item(w);
+        Item it;
+        while (ok && next_item(it)) {
             if (!it.tiles) continue;
             if (nq > 0) ok = warp_wait(smem_u32(&s_qempty), (nq - 1) & 1, bad);
             if (!ok) break;
@@ -251,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                 if (lane == 0) {
                     mb_expect(mb, C::kTileBytes);
                     for (int p = 0; p < HD / 64; ++p)
-                        tma4(dst + p * C::kPanel, (j & 1) ? &t.v : &t.k, p * 64, it.g, (j >> 1) * kN, it.b, mb);
+                        tma4(dst + p * C::kPanel, (j & 1) ? &t.v : &t.k, p * 64, it.g, (it.i0 + (j >> 1)) * kN, it.b, mb);
                 }
-                const int rest = it.len - (it.tiles - 1) * kN;
+                const int rest = it.len - (it.i0 + it.tiles - 1) * kN;
                 if (j == 2 * it.tiles - 1 && rest < kN) {
                     // values behind the row's last position: 0 x anything must be 0
                     ok = warp_wait(mb, turn & 1, bad);
@@ -285,14 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
             }
         }
       } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             // -------------------------------------------- products
             // descriptors: a tile or a K step further is an addition (addresses / 16 stay within their 14 bits)
             const uint64_t qdesc = sdesc(sm, 16), kdesc = sdesc(ring, 16), vdesc = sdesc(ring, C::kPanel);
             uint32_t n = 0, nq = 0, ntail = 0, np[2] = {0, 0}, no[2] = {0, 0};
             bool ok = true, any = false;
-            for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
-                const Item it = item(w);
+            Item it;
+            while (ok && next_item(it)) {
                 if (!it.tiles) continue;
                 ok = mb_wait(smem_u32(&s_qfull), nq & 1, bad) && mb_wait(smem_u32(&s_full[n % kSt]), (n / kSt) & 1, bad);
                 if (!ok) break;
@@ -308,7 +402,7 @@ score_steps<HD, C::kPanel>(tmem + i * kN, q, kd, kIdescS);
                 commit(smem_u32(&s_empty[n % kSt]));
                 if (it.tiles == 1) commit(smem_u32(&s_qempty));
                 ++n;
-                const bool tail = it.len % kN != 0;
+                const bool tail = it.len - (it.i0 + it.tiles - 1) * kN < kN;
                 for (int j = 0; j < it.tiles && ok; ++j) {
                     const uint32_t sv = n % kSt, pv = (n / kSt) & 1, sk = (n + 1) % kSt, pk = ((n + 1) / kSt) & 1;
                     const bool more = j + 1 < it.tiles;
@@ -364,10 +458,9 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
         const float sl = a.scale * kLog2e;
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        for (int64_t w = blockIdx.x; w < t.items && ok; w += gridDim.x) {
-            const Item it = item(w);
+        Item it;
+        while (ok && next_item(it)) {
             if (i && !it.two) continue;
-            const int x = it.first + i, h = it.g * G + x / t.nq, qi = (x % t.nq) * kM + r;
             float m = -INFINITY, ref = 0.f, l = 0.f;
             for (int j = 0; j < it.tiles; ++j) {
                 ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
@@ -380,7 +473,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 tm_wait_ld();
 #pragma unroll
                 for (int c = 0; c < kN; c += 16) after_wait(s + c);
-                const int rest = it.len - j * kN;
+                const int rest = it.len - (it.i0 + j) * kN;
                 if (rest < kN) {
 #pragma unroll
                     for (int c = 0; c < kN; ++c) s[c] = c < rest ? s[c] : -INFINITY;
@@ -441,15 +534,27 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
             }
             if (!ok) break;
             // ---- the result
-            float inv = 0.f;
+            const int x = it.first + i, h = it.g * G + x / t.nq, qi = (x % t.nq) * kM + r;
             if (it.tiles) {
                 ok = warp_wait(smem_u32(&s_ofull[i]), no & 1, bad);
                 if (!ok) break;
                 ++no;
                 tm_after();
-                inv = 1.f / l;
             }
             uint16_t* out = static_cast<uint16_t*>(a.out) + it.b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD;
+            auto put = [&](int c, const float* o, float inv) {         // 16 columns
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        u[y] = l == 0.f ? 0u : pack2<BF>(o[e + 2 * y] * inv, o[e + 2 * y + 1] * inv);
+                    *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            };
+            // a part of an item: its record of 4-column pieces [piece][query], then (maximum, sum) of each query
+            float* rec = a.part + (int64_t)(2 * blockIdx.x + it.begins) * kTcRecord;
+            const int at4 = i * (HD / 4) * kM + r, at_ml = 2 * kM * HD + 2 * (i * kM + r);
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
                 float o[16];
@@ -458,18 +563,56 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                     tm_wait_ld();
                     after_wait(o);
                 }
-                if (qi < a.Lq) {
+                if (it.c_lo == it.c_hi) {
+                    if (qi < a.Lq) put(c, o, 1.f / l);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            u[y] = l == 0.f ? 0u : pack2<BF>(o[e + 2 * y] * inv, o[e + 2 * y + 1] * inv);
-                        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        __stcg(reinterpret_cast<float4*>(rec) + at4 + (c / 4 + y) * kM, make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
                 }
             }
             tm_before();
+            if (it.c_lo != it.c_hi) {
+                // ---- the last block of the item to arrive joins the records in block order, each warp its 32 queries
+                __stcg(reinterpret_cast<float2*>(rec + at_ml), make_float2(m, l));
+                __syncwarp();
+                int before = 0;
+                if (lane == 0) {
+                    __threadfence();
+                    before = atomicAdd(a.cnt + it.c_lo * kSoftWarps + warp, 1);
+                    __threadfence();
+                }
+                if (__shfl_sync(0xffffffffu, before, 0) != it.c_hi - it.c_lo) continue;
+                if (lane == 0) a.cnt[it.c_lo * kSoftWarps + warp] = 0;
+                auto record = [&](int c) { return a.part + (int64_t)(2 * c + (c == it.c_lo ? 1 : 0)) * kTcRecord; };
+                m = -INFINITY;
+                for (int c = it.c_lo; c <= it.c_hi; ++c) m = fmaxf(m, __ldcg(record(c) + at_ml));
+                l = 0.f;
+                for (int c = it.c_lo; c <= it.c_hi; ++c) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(c) + at_ml));
+                    if (ml.y != 0.f) l += ml.y * (ml.x == -INFINITY ? 1.f : ex2(ml.x - m));
+                }
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                    float o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                    for (int p = it.c_lo; p <= it.c_hi; ++p) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(p) + at_ml));
+                        const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(record(p)) + at4 + (c / 4 + y) * kM);
+                            if (f == 0.f) continue;
+                            o[4 * y] = fmaf(v.x, f, o[4 * y]);
+                            o[4 * y + 1] = fmaf(v.y, f, o[4 * y + 1]);
+                            o[4 * y + 2] = fmaf(v.z, f, o[4 * y + 2]);
+                            o[4 * y + 3] = fmaf(v.w, f, o[4 * y + 3]);
+                        }
+                    }
+                    if (qi < a.Lq) put(c, o, 1.f / l);
+                }
+            }
             if (a.lse && qi < a.Lq)
                 a.lse[((int64_t)it.b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
         }
@@ -528,8 +671,9 @@ cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t 
     t.nq = (a.Lq + kM - 1) / kM;
     const int64_t pairs = ((int64_t)(a.H / a.Hkv) * t.nq + 1) / 2;
     t.pairs = (int32_t)pairs;
-    t.items = (int64_t)a.B * a.Hkv * pairs;
-    const int grid = (int)std::min<int64_t>(sms, t.items);
+    // no more blocks than tiles there can be
+    const int64_t most = std::min<int64_t>((int64_t)1 << 30, (int64_t)a.B * a.Hkv * pairs) * ((a.max_len + kN - 1) / kN);
+    const int grid = (int)std::min<int64_t>(sms, most);
     if (hd == 64) return bf ? launch_tc<64, true>(t, grid, st) : launch_tc<64, false>(t, grid, st);
     return bf ? launch_tc<128, true>(t, grid, st) : launch_tc<128, false>(t, grid, st);
 }

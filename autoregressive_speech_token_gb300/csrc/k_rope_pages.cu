@@ -8,10 +8,10 @@
 // to the nearest quarter turn, leave |r| <= 1/8 turn, which fp32 holds to 2^-28
 // of a turn, and sincospif of it gives cos and sin to about their last bit.
 //
-// The call moves its data once and is bound by memory.  A block takes one or two tokens:
+// The call moves its data once and is bound by memory.  A block takes one token or four:
 // their sines and cosines are formed once, in shared memory, for all heads, while the
 // block's first loads are in flight; then each thread rotates 8 pairs of one head per
-// step with 16-byte loads and stores.  30011 tokens (483 MB) take 81 us, 0.88 of the copy rate,
+// step with 16-byte loads and stores.  30011 tokens (483 MB) take 84 us, 0.85 of the copy rate,
 // into single positions of random pages.
 #include <cmath>
 
@@ -173,11 +173,11 @@ __global__ void __launch_bounds__(kThreads) k_rope_pages(const __grid_constant__
 
 template <typename T, typename TC>
 cudaError_t launch_hd(const RopeArgs& a, cudaStream_t st) {
-    // Many tokens: two to a block of 128 threads, so that an SM holds many blocks at different points (30011 tokens of
-    // 16 + 8 + 8 heads of 128, bf16: 81 us; 84 us with 256 threads and four tokens, 104 us with one token, 110 us with
-    // 512 threads).  Few tokens: one each and more threads, so that no thread takes a third piece.
+    // Many tokens: four to a block of 128 threads, so that an SM holds many blocks at different points (30011 tokens of
+    // 16 + 8 + 8 heads of 128, bf16: 84 us; 87 us with two tokens, 86 with eight, 110 with 512 threads).  Few tokens: one
+    // each and more threads, so that no thread takes a third piece.
     const bool many = a.n > 512;
-    const int tokens = many ? 2 : 1;
+    const int tokens = many ? 4 : 1;
     const dim3 grid((a.n + tokens - 1) / tokens);
     const size_t smem = sizeof(float) * tokens * a.c.head_dim;
     if (a.c.head_dim == 64)

@@ -256,7 +256,7 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
                         int64_t kv_stride, const sd_pages* cache, void* stream);
 
 /* Workspace of the attention entries below: the partial results of split
- * lengths, a fixed few MB, allocated here on `device` (-1: the current one).
+ * lengths, fixed at about 40 MB, allocated here on `device` (-1: the current one).
  * Calls with one workspace, replays of graphs that captured one among them, must
  * not overlap: one workspace for each stream. */
 typedef struct sd_attn_ws sd_attn_ws;
