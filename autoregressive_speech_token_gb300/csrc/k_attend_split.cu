@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     __shared__ __align__(8) unsigned long long s_ufull[kUnits], s_uempty[kUnits], s_done, s_free;
     __shared__ uint32_t s_live[kSt][kWarps];
     __shared__ Unit s_unit[kUnits];
+    __shared__ int2 s_box[kLoaders][32];
     __shared__ int64_t s_sum[kThreads / 32];
     __shared__ int64_t s_base;
     __shared__ int s_len[kThreads];
@@ -546,15 +547,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                             }
                         }
                         const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-                        if (lane == 0 && have) mb_expect_more(mb, __popc(have) * box * S::kRow);
-                        // box by box from one lane: loads by several lanes of a warp at once took 250 cycles each
-                        for (int y = 0; y < min(32, groups - k * 32); ++y) {
-                            const int page = __shfl_sync(0xffffffffu, id, y), pos = __shfl_sync(0xffffffffu, in, y);
-                            if (lane == 0 && page >= 0) {
-                                const uint32_t to = dst + (k * 32 + y) * box * S::kPart;
+                        if (k > 0) __syncwarp();
+                        s_box[turn_of][lane] = make_int2(id, in);
+                        __syncwarp();
+                        // box by box from the elected lane (by several lanes of a warp at once: 250 cycles each)
+                        if (elect_one()) {
+                            if (have) mb_expect_more(mb, __popc(have) * box * S::kRow);
+                            const int boxes = min(32, groups - k * 32);
+                            uint32_t to = dst + k * 32 * box * S::kPart;
+                            for (int y = 0; y < boxes; ++y, to += box * S::kPart) {
+                                const int2 v = s_box[turn_of][y];
+                                if (v.x < 0) continue;
 #pragma unroll
                                 for (int part = 0; part < S::kParts; ++part)
-                                    tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, pos, p.g, page, mb);
+                                    tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, v.y, p.g, v.x, mb);
                             }
                         }
                     }
