@@ -4,7 +4,7 @@
 
 #include "pages_dev.cuh"
 
-// Partial results: two records a block, arrival counters of 8 warps (either kernel's; calls do not overlap).
+// Partial results: two records a block, and the split kernel's arrival counters.
 // The counters are zero between calls (the last arriver of a unit clears its own).
 struct sd_attn_ws {
     int device = 0, sms = 0;

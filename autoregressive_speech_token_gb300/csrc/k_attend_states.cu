@@ -62,9 +62,9 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     cudaError_t e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, device);
     const size_t blocks = (size_t)ws->sms;
     if (e == cudaSuccess) e = cudaMalloc(&ws->part, 2 * blocks * kTcRecord * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * 8 * sizeof(int));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * kSplitRows / 2 * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
-    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * 8 * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * kSplitRows / 2 * sizeof(int));
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     if (e == cudaSuccess) e = cudaHostAlloc(&ws->err, sizeof(int), cudaHostAllocDefault);
     if (e == cudaSuccess) *ws->err = 0;

@@ -4,8 +4,8 @@
 // A work item is a pair of query tiles (128 queries of one head each) of one (row b,
 // kv head g), against all of that row's positions in tiles of 128.  One block per SM
 // takes whole items, or, where that would leave SMs idle for long, an even share of
-// the tiles of all items, and the parts of an item are joined by the last block to
-// arrive, in block order.  Per position tile j and query tile i
+// the tiles of all items; a second kernel then joins the parts of the items that were
+// cut, in block order.  Per position tile j and query tile i
 //   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
 //   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
 //   O_i += P_i V_j (fp32, head_dim columns)
@@ -36,13 +36,14 @@ constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
 constexpr int kLead = 1;                              // what beginning and ending an item costs, in tiles
-constexpr int kJoin = 6;                              // what joining the parts of items costs, in tiles
+constexpr int kJoin = 4;                              // what joining the parts of items costs, in tiles
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
 
 struct alignas(128) TcArgs {
     CUtensorMap q, k, v;
     AttendArgs a;
     int32_t nq, pairs;                                // query tiles of a head, pairs of a (b, g)
+    int32_t parts, blocks, join_blocks;               // items may be cut; blocks of the grid, and of the joining one
 };
 
 template <int HD>
@@ -161,6 +162,65 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     }
 }
 
+__device__ __forceinline__ int tc_length(const AttendArgs& a, int b) {
+    return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len);
+}
+// Tiles of an item, with what beginning and ending it costs
+__device__ __forceinline__ int tc_padded(int len) { return (len + kN - 1) / kN + kLead; }
+
+// How the items are shared out among `grid` blocks, found by every warp for itself; s_row (rows by falling length) and
+// s_len are filled where there are at most 32 rows.  Called by all threads of a block.
+struct Share {
+    bool whole, sorted;
+    int64_t per, all, per_b;                                       // tiles of a block, of all; items of a row
+};
+__device__ __forceinline__ Share tc_share(const TcArgs& t, int64_t grid, int* s_row, int* s_len) {
+    const AttendArgs& a = t.a;
+    const int lane = threadIdx.x & 31;
+    Share s;
+    s.per_b = (int64_t)a.Hkv * t.pairs;
+    const int64_t rounds = (a.B * s.per_b + grid - 1) / grid;
+    int64_t all = 0;
+    int most = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int n = tc_padded(tc_length(a, b));
+        all += n;
+        most = max(most, n);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    s.all = all * s.per_b;
+    s.per = (s.all + grid - 1) / grid;
+    s.sorted = a.B <= 32;
+    // Whole items are taken in rounds, there and back over the blocks, the longest rows first where a warp can sort
+    // them.  A round takes as long as its longest item.
+    int64_t cost = rounds * most;
+    if (s.sorted) {
+        const int mine = lane < a.B ? tc_length(a, lane) : -1;
+        int rank = 0;
+        for (int x = 0; x < a.B; ++x) {
+            const int other = __shfl_sync(0xffffffffu, mine, x);
+            rank += other > mine || (other == mine && x < lane);
+        }
+        if (threadIdx.x < a.B) {
+            s_row[rank] = lane;
+            s_len[lane] = mine;
+        }
+        __syncthreads();
+        if (rounds <= 32) {
+            cost = lane < rounds ? tc_padded(s_len[s_row[(int)(lane * grid / s.per_b)]]) : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+        }
+    }
+    // Parts are even, but cost their records and a second kernel, as much as about kJoin tiles.
+    s.whole = !t.parts || cost <= s.per + s.per / 16 + kJoin;
+    return s;
+}
+
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant__ TcArgs t) {
     using C = Cfg<HD>;
@@ -210,56 +270,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
 
     const int G = a.H / a.Hkv;
     const int per_g = G * t.nq;                                    // query tiles of a (b, g)
-    // ---- this block's share, found by every warp for itself: whole items, or an even part of all tiles
-    auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
-    auto padded = [&](int len) { return (len + kN - 1) / kN + kLead; };
-    const int64_t per_b = (int64_t)a.Hkv * t.pairs, items = a.B * per_b;    // items of a row, of all
-    const int64_t grid = gridDim.x, rounds = (items + grid - 1) / grid;
-    int64_t all = 0;
-    int most = 0;
-    for (int b = lane; b < a.B; b += 32) {
-        const int n = padded(length(b));
-        all += n;
-        most = max(most, n);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    all *= per_b;
-    // Whole items are taken in rounds, there and back over the blocks, the longest rows first where a warp can sort
-    // them.  A round takes as long as its longest item.
-    int64_t whole_cost = rounds * most;
-    const bool sorted = a.B <= 32;
-    if (sorted) {
-        const int mine = lane < a.B ? length(lane) : -1;
-        int rank = 0;
-        for (int x = 0; x < a.B; ++x) {
-            const int other = __shfl_sync(0xffffffffu, mine, x);
-            rank += other > mine || (other == mine && x < lane);
-        }
-        if (warp == 0 && lane < a.B) {
-            s_row[rank] = lane;
-            s_len[lane] = mine;
-        }
-        __syncthreads();
-        if (rounds <= 32) {
-            int64_t first = lane < rounds ? padded(s_len[s_row[(int)(lane * grid / per_b)]]) : 0;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-            whole_cost = first;
-        }
-    }
-    const int64_t per = (all + grid - 1) / grid;
-    // Parts of items are even, but joining them costs as much as about kJoin tiles (777 queries over up to 1500 states
-    // of 8 rows and 16 heads of 64: 64 us cut evenly, 53 us whole; 8192 over 8190: 822 and 815 us).
-    const bool whole = whole_cost <= per + per / 16 + kJoin;
+    // ---- this block's share: whole items, or an even part of all tiles
+    auto length = [&](int b) { return tc_length(a, b); };
+    const Share share = tc_share(t, gridDim.x, s_row, s_len);
+    const bool whole = share.whole, sorted = share.sorted;
+    const int64_t per = share.per, all = share.all, per_b = share.per_b, grid = gridDim.x, items = share.per_b * a.B;
     const int64_t t_begin = blockIdx.x * per, t_end = min(all, t_begin + per);
     int64_t at = whole ? 0 : t_begin, base = 0;                    // whole: the next round; else: the next tile, row b_at's first
     int b_at = a.B;
     for (int b0 = 0; b0 < a.B && !whole; b0 += 32) {
-        const int64_t mine = b0 + lane < a.B ? padded(length(b0 + lane)) * per_b : 0;
+        const int64_t mine = b0 + lane < a.B ? tc_padded(length(b0 + lane)) * per_b : 0;
         int64_t sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -288,13 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
             p.b = sorted ? s_row[r] : r;
             p.len = sorted ? s_len[p.b] : length(p.b);
             p.c_lo = p.c_hi = p.i0 = p.begins = 0;
-            p.tiles = padded(p.len) - kLead;
+            p.tiles = tc_padded(p.len) - kLead;
             ++at;
         } else {
             if (at >= t_end) return false;
             p.b = b_at;
             p.len = sorted ? s_len[b_at] : length(b_at);
-            const int nt = padded(p.len);
+            const int nt = tc_padded(p.len);
             u = (at - base) / nt;
             const int64_t u0 = base + u * nt, next = min(u0 + nt, t_end);
             const int64_t real = min(u0 + kLead, u0 + nt - 1);     // first tile (an empty row: its last empty one)
@@ -565,7 +585,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 }
                 if (it.c_lo == it.c_hi) {
                     if (qi < a.Lq) put(c, o, 1.f / l);
-                } else {
+                } else if (qi < a.Lq) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         __stcg(reinterpret_cast<float4*>(rec) + at4 + (c / 4 + y) * kM, make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]));
@@ -573,45 +593,8 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
             }
             tm_before();
             if (it.c_lo != it.c_hi) {
-                // ---- the last block of the item to arrive joins the records in block order, each warp its 32 queries
-                __stcg(reinterpret_cast<float2*>(rec + at_ml), make_float2(m, l));
-                __syncwarp();
-                int before = 0;
-                if (lane == 0) {
-                    __threadfence();
-                    before = atomicAdd(a.cnt + it.c_lo * kSoftWarps + warp, 1);
-                    __threadfence();
-                }
-                if (__shfl_sync(0xffffffffu, before, 0) != it.c_hi - it.c_lo) continue;
-                if (lane == 0) a.cnt[it.c_lo * kSoftWarps + warp] = 0;
-                auto record = [&](int c) { return a.part + (int64_t)(2 * c + (c == it.c_lo ? 1 : 0)) * kTcRecord; };
-                m = -INFINITY;
-                for (int c = it.c_lo; c <= it.c_hi; ++c) m = fmaxf(m, __ldcg(record(c) + at_ml));
-                l = 0.f;
-                for (int c = it.c_lo; c <= it.c_hi; ++c) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(c) + at_ml));
-                    if (ml.y != 0.f) l += ml.y * (ml.x == -INFINITY ? 1.f : ex2(ml.x - m));
-                }
-#pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
-                    float o[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
-                    for (int p = it.c_lo; p <= it.c_hi; ++p) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(record(p) + at_ml));
-                        const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(record(p)) + at4 + (c / 4 + y) * kM);
-                            if (f == 0.f) continue;
-                            o[4 * y] = fmaf(v.x, f, o[4 * y]);
-                            o[4 * y + 1] = fmaf(v.y, f, o[4 * y + 1]);
-                            o[4 * y + 2] = fmaf(v.z, f, o[4 * y + 2]);
-                            o[4 * y + 3] = fmaf(v.w, f, o[4 * y + 3]);
-                        }
-                    }
-                    if (qi < a.Lq) put(c, o, 1.f / l);
-                }
+                if (qi < a.Lq) __stcg(reinterpret_cast<float2*>(rec + at_ml), make_float2(m, l));
+                continue;
             }
             if (a.lse && qi < a.Lq)
                 a.lse[((int64_t)it.b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
@@ -622,6 +605,82 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
     tm_after();
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     if (tid == 0 && s_bad) *a.err = SD_ERR_TIMEOUT;
+}
+
+// Joins the parts of the items that were cut: a block for each query tile of an item, the records in block order.
+constexpr int kJoinThreads = 256;
+template <int HD, bool BF>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ TcArgs t) {
+    constexpr float kShift = BF ? 0.f : 7.f;
+    __shared__ int s_row[32], s_len[32];
+    pdl_trigger();
+    pdl_wait();
+    const AttendArgs& a = t.a;
+    const Share s = tc_share(t, t.blocks, s_row, s_len);
+    if (s.whole) return;
+    const int lane = threadIdx.x & 31, G = a.H / a.Hkv;
+    constexpr int kCols = HD / 8 / (kJoinThreads / kM);            // blocks across a row's columns
+    for (int64_t piece = blockIdx.x; piece < 2 * kCols * s.per_b * a.B; piece += gridDim.x) {
+    const int64_t w = piece / (2 * kCols), u = w % s.per_b;
+    const int i = (int)(piece / kCols & 1), b = (int)(w / s.per_b);
+    // the row's first tile
+    int64_t base = 0;
+    for (int x = lane; x < b; x += 32) base += tc_padded(tc_length(a, x));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+    const int nt = tc_padded(tc_length(a, b));
+    const int64_t u0 = base * s.per_b + u * nt;
+    const int c_lo = (int)(min(u0 + kLead, u0 + nt - 1) / s.per), c_hi = (int)((u0 + nt - 1) / s.per);
+    const int g = (int)(u / t.pairs), x = (int)(u - (int64_t)g * t.pairs) * 2 + i;
+    if (c_lo == c_hi || x >= G * t.nq) continue;
+    // a query of the tile, 8 of its columns; the records in batches whose loads are in flight together
+    const int r = threadIdx.x % kM, c8 = (int)(piece % kCols) * (kJoinThreads / kM) + threadIdx.x / kM;
+    const int h = g * G + x / t.nq, qi = (x % t.nq) * kM + r;
+    if (qi < a.Lq) {
+    const int at4 = (i * (HD / 4) + 2 * c8) * kM + r, at_ml = 2 * kM * HD + 2 * (i * kM + r);
+    auto record = [&](int c) { return a.part + (int64_t)(2 * c + (c == c_lo ? 1 : 0)) * kTcRecord; };
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    constexpr int kBatch = 6;
+    for (int c = c_lo; c <= c_hi; c += kBatch) {
+        float2 ml[kBatch];
+        float4 v[kBatch][2];
+        float mx = m;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+            const float* p = record(min(c + y, c_hi));
+            ml[y] = __ldcg(reinterpret_cast<const float2*>(p + at_ml));
+            v[y][0] = __ldcg(reinterpret_cast<const float4*>(p) + at4);
+            v[y][1] = __ldcg(reinterpret_cast<const float4*>(p) + at4 + kM);
+        }
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+            if (c + y > c_hi) ml[y] = make_float2(-INFINITY, 0.f);
+            mx = fmaxf(mx, ml[y].x);
+        }
+        const float keep = m == -INFINITY ? 1.f : ex2(m - mx);
+        m = mx;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= keep;
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+            if (ml[y].y == 0.f) continue;                          // nothing in this part
+            const float f = ml[y].x == -INFINITY ? 1.f : ex2(ml[y].x - m);
+            l = fmaf(f, ml[y].y, l);
+            o[0] = fmaf(v[y][0].x, f, o[0]); o[1] = fmaf(v[y][0].y, f, o[1]); o[2] = fmaf(v[y][0].z, f, o[2]); o[3] = fmaf(v[y][0].w, f, o[3]);
+            o[4] = fmaf(v[y][1].x, f, o[4]); o[5] = fmaf(v[y][1].y, f, o[5]); o[6] = fmaf(v[y][1].z, f, o[6]); o[7] = fmaf(v[y][1].w, f, o[7]);
+        }
+    }
+    const float inv = 1.f / l;
+    uint32_t y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0u : pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD + c8 * 8) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+    if (a.lse && c8 == 0)
+        a.lse[((int64_t)b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+    }
+    }
 }
 
 // [batch][row][head][hd] of 16-bit elements by strides: boxes of 128 rows of 64 elements of one head
@@ -641,8 +700,9 @@ bool map4(CUtensorMap* map, bool bf, const void* base, int hd, int heads, int ro
 }
 
 template <int HD, bool BF>
-cudaError_t launch_tc(const TcArgs& t, int grid, cudaStream_t st) {
-    return launch_k(k_attend_tc<HD, BF>, dim3(grid), dim3(kThreads), Cfg<HD>::kSmem, st, t);
+cudaError_t launch_tc(const TcArgs& t, cudaStream_t st) {
+    const cudaError_t e = launch_k(k_attend_tc<HD, BF>, dim3(t.blocks), dim3(kThreads), Cfg<HD>::kSmem, st, t);
+    return e != cudaSuccess || !t.parts ? e : launch_k(k_attend_join<HD, BF>, dim3(t.join_blocks), dim3(kJoinThreads), 0, st, t);
 }
 template <int HD, bool BF>
 cudaError_t prepare_tc() {
@@ -671,11 +731,15 @@ cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t 
     t.nq = (a.Lq + kM - 1) / kM;
     const int64_t pairs = ((int64_t)(a.H / a.Hkv) * t.nq + 1) / 2;
     t.pairs = (int32_t)pairs;
-    // no more blocks than tiles there can be
-    const int64_t most = std::min<int64_t>((int64_t)1 << 30, (int64_t)a.B * a.Hkv * pairs) * ((a.max_len + kN - 1) / kN);
-    const int grid = (int)std::min<int64_t>(sms, most);
-    if (hd == 64) return bf ? launch_tc<64, true>(t, grid, st) : launch_tc<64, false>(t, grid, st);
-    return bf ? launch_tc<128, true>(t, grid, st) : launch_tc<128, false>(t, grid, st);
+    // Items may be cut where there are fewer than the SMs could take in two rounds; the more there are, the longer they
+    // have to be for what that can save to outweigh the second launch (about 3 us; 64 queries over 1500 states, 16 heads
+    // of 64: 15 us cut, 20 us whole; 128 over 32768, 16 heads of 128 in 8 groups: 46 and 350 us).
+    const int64_t items = (int64_t)a.B * a.Hkv * pairs, tiles = (a.max_len + kN - 1) / kN;
+    t.parts = items <= sms / 2 ? tiles > 8 : items < 2 * (int64_t)sms && tiles >= 24;
+    t.blocks = (int)std::min<int64_t>(sms, t.parts ? items * tiles : items);
+    t.join_blocks = (int)std::min<int64_t>(3 * (int64_t)sms, 2 * items * (hd / 8 / (kJoinThreads / kM)));
+    if (hd == 64) return bf ? launch_tc<64, true>(t, st) : launch_tc<64, false>(t, st);
+    return bf ? launch_tc<128, true>(t, st) : launch_tc<128, false>(t, st);
 }
 
 }  // namespace sd
