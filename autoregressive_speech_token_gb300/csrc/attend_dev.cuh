@@ -4,7 +4,7 @@
 
 #include "pages_dev.cuh"
 
-// Partial results: two records a block, and the split kernel's arrival counters.
+// Partial results: a record a block of the tensor-core kernel, or two of the split kernel with its arrival counters.
 // The counters are zero between calls (the last arriver of a unit clears its own).
 struct sd_attn_ws {
     int device = 0, sms = 0;

@@ -6,8 +6,6 @@
 namespace sd {
 namespace {
 
-constexpr int kTcQueries = 48;
-
 int check_q(const char* who, int dtype, int kv_dtype, const void* q, int64_t q_stride, const void* out,
             int64_t out_stride, int n_head, int n_kv, float scale) {
     const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
@@ -32,9 +30,11 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream)
     a.err = ws->err;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    // Tensor-core tiles of 128 queries of a head: queries, keys and values of one 16-bit type, and enough queries
+    // Tensor-core tiles of 128 queries of a head: queries, keys and values of one 16-bit type, and more query rows to a
+    // kv head than two units of the split kernel (16 rows of 1500 states, 16 heads of 64: 24 queries 32 us, 39 us
+    // split, 16 queries 32 and 29; 16 heads of 128 in 8 groups: 8 queries 25 and 30 us, 4 queries 24 and 19).
     bool taken = false;
-    if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && a.Lq >= kTcQueries)
+    if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && (int64_t)a.Lq * (a.H / a.Hkv) > 2 * kSplitRows)
         e = launch_attend_tc(a, hd, ws->sms, st, &taken);
     if (!taken) e = launch_attend_split(a, hd, ws->sms, st);
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
@@ -61,7 +61,7 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     ws->device = device;
     cudaError_t e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, device);
     const size_t blocks = (size_t)ws->sms;
-    if (e == cudaSuccess) e = cudaMalloc(&ws->part, 2 * blocks * kTcRecord * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->part, blocks * kTcRecord * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * kSplitRows / 2 * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
     if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * kSplitRows / 2 * sizeof(int));
@@ -95,13 +95,13 @@ int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_
     static const char* who = "sd_attend_pages";
     sd_pages c;
     if (int rc = check_pages(who, cache, &c)) return rc;
-    if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
     if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
+    if (R == 0) return SD_OK;
+    if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
     if (int rc = check_q(who, dtype, c.dtype, q_dev, q_stride, out_dev, out_stride, n_head, c.n_kv_head, scale)) return rc;
     if (c.dtype == SD_E4M3 && c.head_dim == 64 && c.page_size % 2)
         return op_fail(SD_ERR_UNSUPPORTED, "%s: pages of an odd number of 64-byte rows", who);
     if (!ws) return op_fail(SD_ERR_INVALID_ARG, "%s: ws is NULL", who);
-    if (R == 0) return SD_OK;
     AttendArgs a = {};
     a.q = q_dev; a.k = c.k_dev; a.v = c.v_dev; a.out = out_dev; a.lse = lse_dev; a.table = table_dev; a.len = len_dev;
     a.k_scale = c.k_scale_dev; a.v_scale = c.v_scale_dev; a.by_ps = FastDiv((uint32_t)c.page_size);
@@ -126,6 +126,11 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
         return op_fail(SD_ERR_UNSUPPORTED, "%s: head_dim %d is not 64 or 128", who, s.head_dim);
     if (s.B < 0 || s.n_pos < 0 || s.n_kv_head < 1 || Lq < 0)
         return op_fail(SD_ERR_INVALID_ARG, "%s: B %d, n_pos %d, n_kv_head %d, Lq %d", who, s.B, s.n_pos, s.n_kv_head, Lq);
+    if (s.B == 0 || Lq == 0) return SD_OK;
+    if (s.n_pos == 0) {                                            // nothing is read: any legal address and strides
+        s.k_dev = s.v_dev = q_dev;
+        s.head_stride = s.pos_stride = s.batch_stride = s.head_dim;
+    }
     if (!s.k_dev || !s.v_dev || !aligned16(s.k_dev) || !aligned16(s.v_dev))
         return op_fail(SD_ERR_INVALID_ARG, "%s: k_dev or v_dev is NULL or not 16-byte aligned", who);
     if (!s.batch_stride && !s.head_stride && !s.pos_stride) {
@@ -140,7 +145,6 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
     if (s.B > 1 && (!stride16(q_batch, dtype_bytes(dtype)) || !stride16(out_batch, dtype_bytes(dtype))))
         return op_fail(SD_ERR_INVALID_ARG, "%s: q_batch and out_batch must be multiples of 16 bytes", who);
     if (!ws) return op_fail(SD_ERR_INVALID_ARG, "%s: ws is NULL", who);
-    if (s.B == 0 || Lq == 0) return SD_OK;
     AttendArgs a = {};
     a.q = q_dev; a.k = s.k_dev; a.v = s.v_dev; a.out = out_dev; a.lse = lse_dev; a.len = s.len_dev;
     a.batch_stride = s.batch_stride; a.head_stride = s.head_stride; a.pos_stride = s.pos_stride;

@@ -3,9 +3,10 @@
 //
 // A work item is a pair of query tiles (128 queries of one head each) of one (row b,
 // kv head g), against all of that row's positions in tiles of 128.  One block per SM
-// takes whole items, or, where that would leave SMs idle for long, an even share of
-// the tiles of all items; a second kernel then joins the parts of the items that were
-// cut, in block order.  Per position tile j and query tile i
+// takes whole items; where there are fewer items than SMs, they are cut into parts with a
+// block each, and a second kernel joins the parts in order (64 queries over 1500 states, 16
+// heads of 64: 12 us cut, 17 us whole; 128 over 32768, 16 heads of 128 in 8 groups: 39 and 324
+// us).  Per position tile j and query tile i
 //   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
 //   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
 //   O_i += P_i V_j (fp32, head_dim columns)
@@ -35,8 +36,7 @@ constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 // Registers of a thread: 384 x 168 at launch = 2 x 128 x 216 + 128 x 72 (a softmax thread holds a row of 128 scores)
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
-constexpr int kLead = 1;                              // what beginning and ending an item costs, in tiles
-constexpr int kJoin = 4;                              // what joining the parts of items costs, in tiles
+constexpr int kJoin = 4;                              // what cutting and joining items costs, in tiles
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
 
 struct alignas(128) TcArgs {
@@ -165,39 +165,22 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ int tc_length(const AttendArgs& a, int b) {
     return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len);
 }
-// Tiles of an item, with what beginning and ending it costs
-__device__ __forceinline__ int tc_padded(int len) { return (len + kN - 1) / kN + kLead; }
+__device__ __forceinline__ int tc_tiles(int len) { return (len + kN - 1) / kN; }
 
 // How the items are shared out among `grid` blocks, found by every warp for itself; s_row (rows by falling length) and
 // s_len are filled where there are at most 32 rows.  Called by all threads of a block.
 struct Share {
     bool whole, sorted;
-    int64_t per, all, per_b;                                       // tiles of a block, of all; items of a row
+    int per;                                                       // tiles of a part at most
+    int64_t per_b;                                                 // items of a row
+    __device__ __forceinline__ int parts(int len) const { return max((tc_tiles(len) + per - 1) / per, 1); }
 };
 __device__ __forceinline__ Share tc_share(const TcArgs& t, int64_t grid, int* s_row, int* s_len) {
     const AttendArgs& a = t.a;
     const int lane = threadIdx.x & 31;
     Share s;
     s.per_b = (int64_t)a.Hkv * t.pairs;
-    const int64_t rounds = (a.B * s.per_b + grid - 1) / grid;
-    int64_t all = 0;
-    int most = 0;
-    for (int b = lane; b < a.B; b += 32) {
-        const int n = tc_padded(tc_length(a, b));
-        all += n;
-        most = max(most, n);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    s.all = all * s.per_b;
-    s.per = (s.all + grid - 1) / grid;
     s.sorted = a.B <= 32;
-    // Whole items are taken in rounds, there and back over the blocks, the longest rows first where a warp can sort
-    // them.  A round takes as long as its longest item.
-    int64_t cost = rounds * most;
     if (s.sorted) {
         const int mine = lane < a.B ? tc_length(a, lane) : -1;
         int rank = 0;
@@ -210,14 +193,29 @@ __device__ __forceinline__ Share tc_share(const TcArgs& t, int64_t grid, int* s_
             s_len[lane] = mine;
         }
         __syncthreads();
-        if (rounds <= 32) {
-            cost = lane < rounds ? tc_padded(s_len[s_row[(int)(lane * grid / s.per_b)]]) : 0;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-        }
     }
-    // Parts are even, but cost their records and a second kernel, as much as about kJoin tiles.
-    s.whole = !t.parts || cost <= s.per + s.per / 16 + kJoin;
+    // Each part has a block of its own: with `left` blocks more than items, parts of (all tiles) / left are short enough.
+    // They cost their records and a second kernel, as much as about kJoin tiles.
+    const int64_t left = grid - a.B * s.per_b;
+    s.whole = true;
+    s.per = 1;
+    if (t.parts && left > 0) {
+        int64_t all = 0;
+        int most = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            const int n = tc_tiles(s.sorted ? s_len[b] : tc_length(a, b));
+            all += n;
+            most = max(most, n);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, o);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        }
+        const int64_t per = max((all * s.per_b + left - 1) / left, (int64_t)2);
+        s.whole = per + kJoin >= most;
+        s.per = s.whole ? max(most, 1) : (int)per;
+    }
     return s;
 }
 
@@ -270,66 +268,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
 
     const int G = a.H / a.Hkv;
     const int per_g = G * t.nq;                                    // query tiles of a (b, g)
-    // ---- this block's share: whole items, or an even part of all tiles
-    auto length = [&](int b) { return tc_length(a, b); };
+    // ---- this block's share.  Whole items are taken in rounds, there and back over the blocks, the longest rows first
+    // where a warp can sort them; or the block has one part of an item.
     const Share share = tc_share(t, gridDim.x, s_row, s_len);
-    const bool whole = share.whole, sorted = share.sorted;
-    const int64_t per = share.per, all = share.all, per_b = share.per_b, grid = gridDim.x, items = share.per_b * a.B;
-    const int64_t t_begin = blockIdx.x * per, t_end = min(all, t_begin + per);
-    int64_t at = whole ? 0 : t_begin, base = 0;                    // whole: the next round; else: the next tile, row b_at's first
-    int b_at = a.B;
-    for (int b0 = 0; b0 < a.B && !whole; b0 += 32) {
-        const int64_t mine = b0 + lane < a.B ? tc_padded(length(b0 + lane)) * per_b : 0;
-        int64_t sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const uint32_t here = __ballot_sync(0xffffffffu, base + sum - mine <= at && at < base + sum);
-        if (here) {
-            b_at = b0 + __ffs(here) - 1;
-            base += __shfl_sync(0xffffffffu, sum - mine, __ffs(here) - 1);
-            break;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    // A piece: tiles [i0, i0 + tiles) of an item; c_lo .. c_hi the blocks with a part of its tiles.
+    const int64_t per_b = share.per_b, items = per_b * a.B;
+    int64_t round = 0;
+    // A piece: tiles [i0, i0 + tiles) of an item; its parts are in blocks c_lo .. c_hi.
     struct Item {
-        int b, g, len, i0, tiles, first, two, c_lo, c_hi, begins;
+        int b, g, len, i0, tiles, first, two, c_lo, c_hi;
     };
     auto next_item = [&](Item& p) -> bool {
         int64_t u;                                                 // item of its row
-        if (whole) {
-            const int64_t w = at * grid + ((at & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+        if (share.whole) {
+            const int64_t w = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (w >= items) return false;
             const int r = (int)(w / per_b);
             u = w - r * per_b;
-            p.b = sorted ? s_row[r] : r;
-            p.len = sorted ? s_len[p.b] : length(p.b);
-            p.c_lo = p.c_hi = p.i0 = p.begins = 0;
-            p.tiles = tc_padded(p.len) - kLead;
-            ++at;
+            p.b = share.sorted ? s_row[r] : r;
+            p.len = share.sorted ? s_len[p.b] : tc_length(a, p.b);
+            p.c_lo = p.c_hi = p.i0 = 0;
+            p.tiles = tc_tiles(p.len);
         } else {
-            if (at >= t_end) return false;
-            p.b = b_at;
-            p.len = sorted ? s_len[b_at] : length(b_at);
-            const int nt = tc_padded(p.len);
-            u = (at - base) / nt;
-            const int64_t u0 = base + u * nt, next = min(u0 + nt, t_end);
-            const int64_t real = min(u0 + kLead, u0 + nt - 1);     // first tile (an empty row: its last empty one)
-            if (next <= real) return false;
-            p.c_lo = (int)(real / per);
-            p.c_hi = (int)((u0 + nt - 1) / per);
-            p.begins = real >= t_begin;
-            p.i0 = (int)max(at - u0 - kLead, (int64_t)0);
-            p.tiles = (int)(next - u0) - kLead - p.i0;
-            at = next;
-            if (next - base == nt * per_b) {
-                base = next;
-                ++b_at;
+            if (round) return false;
+            int64_t base = 0;                                      // blocks of the rows before (few rows: fewer items than SMs)
+            int parts = 1;
+            for (p.b = 0; p.b < a.B; ++p.b) {
+                p.len = share.sorted ? s_len[p.b] : tc_length(a, p.b);
+                parts = share.parts(p.len);
+                if (blockIdx.x < base + parts * per_b) break;
+                base += parts * per_b;
             }
+            if (p.b == a.B) return false;
+            u = (blockIdx.x - base) / parts;
+            p.c_lo = (int)(base + u * parts);
+            p.c_hi = p.c_lo + parts - 1;
+            const int n = tc_tiles(p.len), each = (n + parts - 1) / parts;   // equal parts, none empty
+            p.i0 = ((int)blockIdx.x - p.c_lo) * each;
+            p.tiles = min(n - p.i0, each);
         }
+        ++round;
         p.g = (int)(u / t.pairs);
         p.first = (int)(u - (int64_t)p.g * t.pairs) * 2;
         p.two = p.first + 1 < per_g;
@@ -573,7 +550,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 }
             };
             // a part of an item: its record of 4-column pieces [piece][query], then (maximum, sum) of each query
-            float* rec = a.part + (int64_t)(2 * blockIdx.x + it.begins) * kTcRecord;
+            float* rec = a.part + (int64_t)blockIdx.x * kTcRecord;
             const int at4 = i * (HD / 4) * kM + r, at_ml = 2 * kM * HD + 2 * (i * kM + r);
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
@@ -618,68 +595,63 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     const AttendArgs& a = t.a;
     const Share s = tc_share(t, t.blocks, s_row, s_len);
     if (s.whole) return;
-    const int lane = threadIdx.x & 31, G = a.H / a.Hkv;
+    const int G = a.H / a.Hkv;
     constexpr int kCols = HD / 8 / (kJoinThreads / kM);            // blocks across a row's columns
     for (int64_t piece = blockIdx.x; piece < 2 * kCols * s.per_b * a.B; piece += gridDim.x) {
-    const int64_t w = piece / (2 * kCols), u = w % s.per_b;
-    const int i = (int)(piece / kCols & 1), b = (int)(w / s.per_b);
-    // the row's first tile
-    int64_t base = 0;
-    for (int x = lane; x < b; x += 32) base += tc_padded(tc_length(a, x));
+        const int64_t w = piece / (2 * kCols), u = w % s.per_b;
+        const int i = (int)(piece / kCols & 1), b = (int)(w / s.per_b);
+        // the blocks of the rows before
+        int64_t base = 0;
+        for (int x = 0; x < b; ++x) base += s.parts(tc_length(a, x)) * s.per_b;
+        const int parts = s.parts(tc_length(a, b)), c_lo = (int)(base + u * parts), c_hi = c_lo + parts - 1;
+        const int g = (int)(u / t.pairs), x = (int)(u - (int64_t)g * t.pairs) * 2 + i;
+        if (c_lo == c_hi || x >= G * t.nq) continue;
+        // a query of the tile, 8 of its columns; the records in batches whose loads are in flight together
+        const int r = threadIdx.x % kM, c8 = (int)(piece % kCols) * (kJoinThreads / kM) + threadIdx.x / kM;
+        const int h = g * G + x / t.nq, qi = (x % t.nq) * kM + r;
+        if (qi >= a.Lq) continue;
+        const int at4 = (i * (HD / 4) + 2 * c8) * kM + r, at_ml = 2 * kM * HD + 2 * (i * kM + r);
+        auto record = [&](int c) { return a.part + (int64_t)c * kTcRecord; };
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        constexpr int kBatch = 6;
+        for (int c = c_lo; c <= c_hi; c += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch][2];
+            float mx = m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
-    const int nt = tc_padded(tc_length(a, b));
-    const int64_t u0 = base * s.per_b + u * nt;
-    const int c_lo = (int)(min(u0 + kLead, u0 + nt - 1) / s.per), c_hi = (int)((u0 + nt - 1) / s.per);
-    const int g = (int)(u / t.pairs), x = (int)(u - (int64_t)g * t.pairs) * 2 + i;
-    if (c_lo == c_hi || x >= G * t.nq) continue;
-    // a query of the tile, 8 of its columns; the records in batches whose loads are in flight together
-    const int r = threadIdx.x % kM, c8 = (int)(piece % kCols) * (kJoinThreads / kM) + threadIdx.x / kM;
-    const int h = g * G + x / t.nq, qi = (x % t.nq) * kM + r;
-    if (qi < a.Lq) {
-    const int at4 = (i * (HD / 4) + 2 * c8) * kM + r, at_ml = 2 * kM * HD + 2 * (i * kM + r);
-    auto record = [&](int c) { return a.part + (int64_t)(2 * c + (c == c_lo ? 1 : 0)) * kTcRecord; };
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    constexpr int kBatch = 6;
-    for (int c = c_lo; c <= c_hi; c += kBatch) {
-        float2 ml[kBatch];
-        float4 v[kBatch][2];
-        float mx = m;
+            for (int y = 0; y < kBatch; ++y) {
+                const float* p = record(min(c + y, c_hi));
+                ml[y] = __ldcg(reinterpret_cast<const float2*>(p + at_ml));
+                v[y][0] = __ldcg(reinterpret_cast<const float4*>(p) + at4);
+                v[y][1] = __ldcg(reinterpret_cast<const float4*>(p) + at4 + kM);
+            }
 #pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-            const float* p = record(min(c + y, c_hi));
-            ml[y] = __ldcg(reinterpret_cast<const float2*>(p + at_ml));
-            v[y][0] = __ldcg(reinterpret_cast<const float4*>(p) + at4);
-            v[y][1] = __ldcg(reinterpret_cast<const float4*>(p) + at4 + kM);
+            for (int y = 0; y < kBatch; ++y) {
+                if (c + y > c_hi) ml[y] = make_float2(-INFINITY, 0.f);
+                mx = fmaxf(mx, ml[y].x);
+            }
+            const float keep = m == -INFINITY ? 1.f : ex2(m - mx);
+            m = mx;
+            l *= keep;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= keep;
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                if (ml[y].y == 0.f) continue;                          // nothing in this part
+                const float f = ml[y].x == -INFINITY ? 1.f : ex2(ml[y].x - m);
+                l = fmaf(f, ml[y].y, l);
+                o[0] = fmaf(v[y][0].x, f, o[0]); o[1] = fmaf(v[y][0].y, f, o[1]); o[2] = fmaf(v[y][0].z, f, o[2]); o[3] = fmaf(v[y][0].w, f, o[3]);
+                o[4] = fmaf(v[y][1].x, f, o[4]); o[5] = fmaf(v[y][1].y, f, o[5]); o[6] = fmaf(v[y][1].z, f, o[6]); o[7] = fmaf(v[y][1].w, f, o[7]);
+            }
         }
+        const float inv = 1.f / l;
+        uint32_t y[4];
 #pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-            if (c + y > c_hi) ml[y] = make_float2(-INFINITY, 0.f);
-            mx = fmaxf(mx, ml[y].x);
-        }
-        const float keep = m == -INFINITY ? 1.f : ex2(m - mx);
-        m = mx;
-        l *= keep;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= keep;
-#pragma unroll
-        for (int y = 0; y < kBatch; ++y) {
-            if (ml[y].y == 0.f) continue;                          // nothing in this part
-            const float f = ml[y].x == -INFINITY ? 1.f : ex2(ml[y].x - m);
-            l = fmaf(f, ml[y].y, l);
-            o[0] = fmaf(v[y][0].x, f, o[0]); o[1] = fmaf(v[y][0].y, f, o[1]); o[2] = fmaf(v[y][0].z, f, o[2]); o[3] = fmaf(v[y][0].w, f, o[3]);
-            o[4] = fmaf(v[y][1].x, f, o[4]); o[5] = fmaf(v[y][1].y, f, o[5]); o[6] = fmaf(v[y][1].z, f, o[6]); o[7] = fmaf(v[y][1].w, f, o[7]);
-        }
-    }
-    const float inv = 1.f / l;
-    uint32_t y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0u : pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD + c8 * 8) =
-        make_uint4(y[0], y[1], y[2], y[3]);
-    if (a.lse && c8 == 0)
-        a.lse[((int64_t)b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
-    }
+        for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0u : pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD + c8 * 8) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+        if (a.lse && c8 == 0)
+            a.lse[((int64_t)b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
     }
 }
 
@@ -731,11 +703,9 @@ cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t 
     t.nq = (a.Lq + kM - 1) / kM;
     const int64_t pairs = ((int64_t)(a.H / a.Hkv) * t.nq + 1) / 2;
     t.pairs = (int32_t)pairs;
-    // Items may be cut where there are fewer than the SMs could take in two rounds; the more there are, the longer they
-    // have to be for what that can save to outweigh the second launch (about 3 us; 64 queries over 1500 states, 16 heads
-    // of 64: 15 us cut, 20 us whole; 128 over 32768, 16 heads of 128 in 8 groups: 46 and 350 us).
+    // Items may be cut where there are fewer than SMs, and the longest is worth more than the second launch
     const int64_t items = (int64_t)a.B * a.Hkv * pairs, tiles = (a.max_len + kN - 1) / kN;
-    t.parts = items <= sms / 2 ? tiles > 8 : items < 2 * (int64_t)sms && tiles >= 24;
+    t.parts = items < sms && tiles > 2 + kJoin;
     t.blocks = (int)std::min<int64_t>(sms, t.parts ? items * tiles : items);
     t.join_blocks = (int)std::min<int64_t>(3 * (int64_t)sms, 2 * items * (hd / 8 / (kJoinThreads / kM)));
     if (hd == 64) return bf ? launch_tc<64, true>(t, st) : launch_tc<64, false>(t, st);

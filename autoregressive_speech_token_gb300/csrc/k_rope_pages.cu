@@ -243,6 +243,7 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
     const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
     if (!b) return op_fail(SD_ERR_INVALID_ARG, "%s: type %d is not SD_F32, SD_F16 or SD_BF16", who, dtype);
     if (n < 0 || n_head < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: n %d, n_head %d", who, n, n_head);
+    if (n == 0) return SD_OK;
     if (!slot_dev || !k_dev || !v_dev || (rope && !pos_dev))
         return op_fail(SD_ERR_INVALID_ARG, "%s: NULL argument", who);
     if ((n_head > 0) != (q_dev != nullptr) || (n_head > 0) != (q_out_dev != nullptr))
@@ -260,7 +261,6 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
             if (rope->axis[i] >= rope->n_axes) return op_fail(SD_ERR_INVALID_ARG, "%s: rope is not initialised", who);
         a.rope = *rope;
     }
-    if (n == 0) return SD_OK;
     a.pos = pos_dev; a.slot = slot_dev; a.q = q_dev; a.k = k_dev; a.v = v_dev; a.q_out = q_out_dev;
     a.pos_stride = pos_stride; a.q_stride = q_stride; a.qo_stride = q_out_stride; a.kv_stride = kv_stride;
     a.slots = (int64_t)a.c.n_pages * a.c.page_size; a.n = n; a.H = n_head; a.rotate = rope != nullptr;

@@ -30,7 +30,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool stride16(int64_t elements, int bytes) { return elements % (16 / bytes) == 0; }
 // A stride of a dimension of `count` elements that TMA can hold (not used where there is one element)
 inline bool tma_stride(int64_t elements, int bytes, int64_t count) {
-    return stride16(elements, bytes) && (count <= 1 || (elements > 0 && elements < ((int64_t)1 << 40) / bytes));
+    return count <= 1 || (stride16(elements, bytes) && elements > 0 && elements < ((int64_t)1 << 40) / bytes);
 }
 
 // Makes `device` current for one call and puts the caller's back.

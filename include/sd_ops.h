@@ -164,7 +164,8 @@ int sd_attend_rows_static(const float* q_dev, const uint16_t* k_dev, const uint1
  * `stream` and return; nothing is allocated, copied or waited for, so they may be
  * captured into a graph.  They run on the calling thread's current device (the
  * attention entries: on their workspace's device); the stream and every pointer
- * belong to that device.  Return values report arguments and launches. */
+ * belong to that device.  Return values report arguments and launches.  A call with
+ * no rows (n, R, B or Lq 0) returns SD_OK and does nothing, whatever its pointers. */
 
 /* Element types.  E4M3 is a cache type only. */
 enum { SD_F32 = 1, SD_F16 = 2, SD_BF16 = 3, SD_E4M3 = 4 };
@@ -256,10 +257,13 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
                         int64_t kv_stride, const sd_pages* cache, void* stream);
 
 /* Workspace of the attention entries below: the partial results of split
- * lengths, fixed at about 40 MB, allocated here on `device` (-1: the current one).
+ * lengths, fixed at about 20 MB, allocated here on `device` (-1: the current one).
  * Calls with one workspace, replays of graphs that captured one among them, must
- * not overlap: one workspace for each stream. */
+ * not overlap: one workspace for each stream.  A kernel whose bounded waits (about
+ * two seconds each) expire leaves its results unfinished, and the next call with the
+ * workspace returns SD_ERR_TIMEOUT, as does every later one. */
 typedef struct sd_attn_ws sd_attn_ws;
+/* Not while a stream is being captured. */
 int sd_attn_ws_create(int32_t device, sd_attn_ws** out);
 void sd_attn_ws_destroy(sd_attn_ws* ws);
 

@@ -344,6 +344,11 @@ PAGED = [
     ([640, 200, 31], 8, 2, 64, "f16", "f16", 16, "hnd", 0.4),
     ([100, 320], 4, 4, 128, "bf16", "bf16", 5, "hnd", 0.3),
     ([33000], 8, 8, 64, "f32", "f16", 64, "hnd", 0),
+    ([1, 2000, 0, 7] * 25, 8, 2, 128, "f16", "f16", 32, "nhd", 0),
+    ([3000, 12], 4, 2, 128, "bf16", "e4m3", 512, "hnd", 0),
+    ([900] * 3, 2, 1, 64, "bf16", "e4m3", 2, "hnd", 0.2),
+    ([256, 512, 128, 384], 16, 16, 64, "f16", "f16", 1024, "hnd", 0),
+    ([1300, 70], 9, 1, 128, "f32", "f16", 3, "pool", 0.1),
 ]
 
 
@@ -478,6 +483,12 @@ CROSS = [
     ([400, 77], 64, 400, 2, 2, 128, "f16", "bf16", "blhd"),
     ([400, 77], 200, 400, 4, 2, 64, "bf16", "f16", "blhd"),
     ([2049, 1], 300, 2049, 4, 4, 128, "f16", "f16", "blhd"),
+    ([9001], 130, 9001, 2, 1, 128, "bf16", "bf16", "blhd"),
+    ([4000, 0, 130, 1], 33, 4000, 4, 2, 64, "f16", "f16", "bhld"),
+    ([300, 7, 0, 129, 1000] * 8, 20, 1000, 2, 2, 64, "bf16", "bf16", "blhd"),
+    ([60, 0, 200] * 14, 3, 200, 12, 1, 128, "f16", "f16", "blhd"),
+    ([900, 3], 17, 900, 1, 1, 64, "bf16", "bf16", "blhd"),
+    ([1500, 1499], 16, 1500, 2, 2, 64, "f16", "f16", "blhd"),
 ]
 
 
@@ -683,3 +694,69 @@ def test_two_graphs_share_a_workspace_in_turn(sd):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+
+
+def test_captured_calls_follow_their_lengths(sd, ws):
+    """One capture of each attention call; the lengths change between the replays, and with them the shares."""
+    g = gen(43)
+    lens = [[3000, 5, 0, 700], [1, 2900, 64, 0], [0, 0, 0, 1], [1500, 1500, 1500, 1500]]
+    full = [3000] * 4
+    kc, vc, table, rows = build_cache(g, np.random.default_rng(9), full, 2, 128, 16, "f16", "hnd")
+    q = randn(g, 4, 8, 128, dt="f16")
+    k, v = (randn(g, 4, 3000, 2, 128, dt="f16") for _ in range(2))
+    cq = randn(g, 4, 40, 8, 128, dt="f16")
+    ld, cache = i32(full), sd.Pages.of(kc, vc)
+    states = sd.States.of(k, v, ld)
+    out, cout = torch.zeros_like(q), torch.zeros_like(cq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = torch.cuda.current_stream().cuda_stream
+        sd.sd_attend_pages(ws, cache, table, table.shape[1], ld, 4, sd.DTYPES["f16"], q, 1024, 8, 0.1, out, 1024, None, s)
+        sd.sd_attend_cross(ws, states, sd.DTYPES["f16"], cq, 40 * 1024, 1024, 40, 8, 0.1, cout, 40 * 1024, 1024, None, s)
+    for n in lens:
+        ld.copy_(i32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        a, _ = run_paged(sd, ws, q, kc, vc, table, n, 0.1)
+        b, _ = run_cross(sd, ws, cq, k, v, n, 0.1)
+        assert torch.equal(out, a) and torch.equal(cout, b)
+        for r in range(4):
+            kk, vv = rows[r][0][:n[r], 0].double(), rows[r][1][:n[r], 0].double()
+            ref, mag, size, _ = attend_ref(q[r, :4].double(), kk, vv, 0.1)
+            tol, _ = bounds(ref, mag, size, n[r], "f16", "f16", 128)
+            assert torch.all((out[r, :4].double() - ref).abs() <= tol)
+
+
+def test_one_page_pools_and_single_elements(sd, ws):
+    """Dimensions of one element, whose strides mean nothing."""
+    g = gen(44)
+    kc, vc = randn(g, 1, 1, 1, 64, dt="f16"), randn(g, 1, 1, 1, 64, dt="f16")
+    q = randn(g, 3, 1, 64, dt="f16")
+    cache = sd.Pages.of(kc, vc)
+    cache.page_stride = cache.head_stride = cache.pos_stride = 3
+    out, ld = torch.zeros_like(q), i32([1, 0, 1])
+    sd.sd_attend_pages(ws, cache, i32([[0], [0], [0]]), 1, ld, 3, sd.DTYPES["f16"], q, 64, 1, 0.1, out, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], vc[0, 0]) and torch.equal(out[2], vc[0, 0]) and torch.all(out[1] == 0)
+
+
+def test_workspace_of_the_device_and_calls_without_rows(sd, ws):
+    kc, vc = pool("hnd", 2, 1, 16, 64, "f16", 0.0)
+    cache = sd.Pages.of(kc, vc)
+    q = torch.zeros(1, 1, 64, device="cuda", dtype=torch.float16)
+    sd.sd_attend_pages(ws, cache, i32([[0]]), 1, i32([1]), 0, sd.DTYPES["f16"], q, 64, 1, 0.1, q, 64)
+    st = sd.States.of(kc[:0].transpose(1, 2), vc[:0].transpose(1, 2))
+    sd.sd_attend_cross(ws, st, sd.DTYPES["f16"], q, 64, 64, 1, 1, 0.1, q, 64, 64)
+    # states without positions: zeros
+    none = torch.zeros(2, 0, 1, 64, device="cuda", dtype=torch.float16)
+    for Lq in (1, 40):
+        cq = torch.ones(2, Lq, 2, 64, device="cuda", dtype=torch.float16)
+        out = torch.full_like(cq, 5.0)
+        sd.sd_attend_cross(ws, sd.States.of(none, none), sd.DTYPES["f16"], cq, Lq * 128, 128, Lq, 2, 0.1, out, Lq * 128, 128)
+        torch.cuda.synchronize()
+        assert torch.all(out == 0)
+    with pytest.raises(sd.SdError):
+        sd.AttnWorkspace(torch.cuda.device_count() + 7)
+    w = sd.AttnWorkspace(0)
+    w.close()
+    w.close()

@@ -99,8 +99,11 @@ def test_write_refuses_another_heads_rope():
     refused(INVALID, "head_dim 128", pkg.sd_rope_write_pages, *_write(rope=pkg.sd_rope_init(128, 1e4)))
 
 
-def test_calls_without_tokens_do_nothing():
-    pkg.sd_rope_write_pages(*_write(n=0))
+def test_calls_without_rows_do_nothing():
+    pkg.sd_rope_write_pages(*_write(n=0, slot=None, pos=None, k=None, v=None))
+    pkg.sd_attend_pages(*_attend(R=0, table=None, len=None, q=None, out=None))
+    pkg.sd_attend_cross(*_cross(Lq=0, q=None, out=None))
+    pkg.sd_attend_cross(*_cross(st=states(B=0, k_dev=None, v_dev=None), q=None, out=None))
 
 
 @pytest.mark.parametrize("args,code,words", [
