@@ -84,10 +84,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
         lo = *reinterpret_cast<const uint32_t*>(&l);
     }
 }
-// a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division costs a few hundred cycles)
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
 template <bool BF>
 __device__ __forceinline__ uint32_t round2(float x, float y) {
     uint32_t hi, lo;

@@ -40,18 +40,22 @@ constexpr int kJoin = 4;                              // what cutting and joinin
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
 
 struct alignas(128) TcArgs {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
     AttendArgs a;
     int32_t nq, pairs;                                // query tiles of a head, pairs of a (b, g)
     int32_t parts, blocks, join_blocks;               // items may be cut; blocks of the grid, and of the joining one
+    int32_t staged;                                   // o is a map of the output
 };
 
 template <int HD>
 struct Cfg {
     static constexpr int kPanel = kN * 128;                       // 128 rows of 64 elements, 128-byte swizzle
     static constexpr int kTileBytes = kPanel * (HD / 64);         // a Q, K or V tile
-    static constexpr int kStages = HD == 128 ? 5 : 11;            // K and V tiles in flight
-    static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+    static constexpr int kStages = HD == 128 ? 5 : 9;             // K and V tiles in flight
+    // Heads of 64 leave room to hand results to TMA: 32 queries of a warp, swizzled.  (Stored row by row from the
+    // registers they hold up the next item's first scores by about 2 us.)
+    static constexpr bool kStaged = HD == 64;
+    static constexpr int kSmem = (2 + kStages) * kTileBytes + (kStaged ? 8 * 32 * 128 : 0) + 1024;
     static constexpr uint32_t kO = 256;                           // tensor memory: S0, S1, O0, O1
 };
 
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
         if (share.whole) {
             const int64_t w = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (w >= items) return false;
-            const int r = (int)(w / per_b);
+            const int r = (int)quot(w, per_b);
             u = w - r * per_b;
             p.b = share.sorted ? s_row[r] : r;
             p.len = share.sorted ? s_len[p.b] : tc_length(a, p.b);
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                 base += parts * per_b;
             }
             if (p.b == a.B) return false;
-            u = (blockIdx.x - base) / parts;
+            u = quot(blockIdx.x - base, parts);
             p.c_lo = (int)(base + u * parts);
             p.c_hi = p.c_lo + parts - 1;
             const int n = tc_tiles(p.len), each = (n + parts - 1) / parts;   // equal parts, none empty
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
             p.tiles = min(n - p.i0, each);
         }
         ++round;
-        p.g = (int)(u / t.pairs);
+        p.g = (int)quot(u, t.pairs);
         p.first = (int)(u - (int64_t)p.g * t.pairs) * 2;
         p.two = p.first + 1 < per_g;
         return true;
@@ -538,6 +542,13 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 ++no;
                 tm_after();
             }
+            const bool staged = C::kStaged && t.staged && it.c_lo == it.c_hi;
+            const uint32_t stage = ring + kSt * C::kTileBytes + warp * 4096 + lane * 128;
+            if (staged) {
+                // the store of the item before has read this warp's part
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+            }
             uint16_t* out = static_cast<uint16_t*>(a.out) + it.b * a.o_batch + (int64_t)qi * a.o_stride + (int64_t)h * HD;
             auto put = [&](int c, const float* o, float inv) {         // 16 columns
 #pragma unroll
@@ -546,7 +557,11 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         u[y] = l == 0.f ? 0u : pack2<BF>(o[e + 2 * y] * inv, o[e + 2 * y + 1] * inv);
-                    *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                    if (staged)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + ((((c + e) >> 3) ^ (lane & 7)) << 4)),
+                                     "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+                    else
+                        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
             };
             // a part of an item: its record of 4-column pieces [piece][query], then (maximum, sum) of each query
@@ -561,7 +576,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                     after_wait(o);
                 }
                 if (it.c_lo == it.c_hi) {
-                    if (qi < a.Lq) put(c, o, 1.f / l);
+                    if (staged || qi < a.Lq) put(c, o, 1.f / l);
                 } else if (qi < a.Lq) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
@@ -569,6 +584,16 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 }
             }
             tm_before();
+            if (staged) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                // queries behind the last are outside the map's range and are not written
+                if (lane == 0 && qi < a.Lq) {
+                    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];"
+                                 ::"l"(reinterpret_cast<uint64_t>(&t.o)), "r"(0), "r"(h), "r"(qi), "r"(it.b), "r"(stage) : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
             if (it.c_lo != it.c_hi) {
                 if (qi < a.Lq) __stcg(reinterpret_cast<float2*>(rec + at_ml), make_float2(m, l));
                 continue;
@@ -577,6 +602,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 a.lse[((int64_t)it.b * a.Lq + qi) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
         }
     }
+    if (C::kStaged && warp < kSoftWarps && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     tm_before();
     __syncthreads();
     tm_after();
@@ -655,9 +681,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     }
 }
 
-// [batch][row][head][hd] of 16-bit elements by strides: boxes of 128 rows of 64 elements of one head
+// [batch][row][head][hd] of 16-bit elements by strides: boxes of rows of 64 elements of one head
 bool map4(CUtensorMap* map, bool bf, const void* base, int hd, int heads, int rows, int batch, int64_t head_stride,
-          int64_t row_stride, int64_t batch_stride) {
+          int64_t row_stride, int64_t batch_stride, int box_rows = 128) {
     EncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
@@ -665,7 +691,7 @@ bool map4(CUtensorMap* map, bool bf, const void* base, int hd, int heads, int ro
     const cuuint64_t strides[3] = {heads > 1 ? (cuuint64_t)head_stride * 2 : (cuuint64_t)hd * 2,
                                    rows > 1 ? (cuuint64_t)row_stride * 2 : (cuuint64_t)hd * 2,
                                    batch > 1 ? (cuuint64_t)batch_stride * 2 : (cuuint64_t)hd * 2};
-    const cuuint32_t box[4] = {64, 1, 128, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1}, one[4] = {1, 1, 1, 1};
     return enc(map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims,
                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -699,6 +725,7 @@ cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t 
              map4(&t.k, bf, a.k, hd, a.Hkv, a.max_len, a.B, a.head_stride, a.pos_stride, a.batch_stride) &&
              map4(&t.v, bf, a.v, hd, a.Hkv, a.max_len, a.B, a.head_stride, a.pos_stride, a.batch_stride);
     if (!*taken) return cudaSuccess;
+    t.staged = hd == 64 && map4(&t.o, bf, a.out, hd, a.H, a.Lq, a.B, hd, a.o_stride, a.o_batch, 32);
     t.a = a;
     t.nq = (a.Lq + kM - 1) / kM;
     const int64_t pairs = ((int64_t)(a.H / a.Hkv) * t.nq + 1) / 2;
