@@ -273,7 +273,9 @@ void sd_attn_ws_destroy(sd_attn_ws* ws);
  * position j in page table_dev[r * table_stride + j / page_size].  len 0 (or
  * negative) gives zeros; a len beyond table_stride * page_size (or 2^31 - 1024) is limited to it; the
  * positions of a page id outside [0, n_pages) are left out, as if masked.
- * Nothing behind len is used, whatever it holds.  dtype (q and out): SD_F32
+ * Nothing behind len is used, whatever it holds.  (An infinite or NaN element of V at
+ * a used position makes its output element infinite or NaN.)  out_dev overlaps no other
+ * argument.  dtype (q and out): SD_F32
  * (with an SD_F16 or SD_E4M3 cache), SD_F16 or SD_BF16.  q_dev [R][n_head][head_dim]
  * with rows q_stride elements apart, out_dev the same with out_stride; pointers
  * are 16-byte aligned, strides multiples of 16 bytes.  lse_dev [R][n_head] (may be
@@ -299,7 +301,8 @@ typedef struct sd_states {
 } sd_states;
 
 /* Cross attention: every query i < Lq of row b attends to all len[b] states of its
- * row, whatever Lq is,
+ * row, whatever Lq is (masks, values that are not finite and overlap as in
+ * sd_attend_pages),
  *   out[b][i][h] = sum_{j < len} softmax_j(scale * q[b][i][h] . K[b][g][j]) V[b][g][j].
  * q_dev [B][Lq][n_head][head_dim]: batch rows q_batch elements apart (unused for B
  * 1), queries q_stride apart; out_dev the same with out_batch, out_stride.  A row
