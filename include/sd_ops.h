@@ -267,23 +267,22 @@ typedef struct sd_attn_ws sd_attn_ws;
 int sd_attn_ws_create(int32_t device, sd_attn_ws** out);
 void sd_attn_ws_destroy(sd_attn_ws* ws);
 
-/* Attention of one new token per request over the paged cache: with g = h /
- * (n_head / n_kv_head) and len = len_dev[r],
+/* Attention of one new token per request over the paged cache: with g = h / (n_head /
+ * n_kv_head) and len = len_dev[r],
  *   out[r][h] = sum_{j < len} softmax_j(scale * q[r][h] . K[g][j]) V[g][j],
- * position j in page table_dev[r * table_stride + j / page_size].  len 0 (or
- * negative) gives zeros; a len beyond table_stride * page_size (or 2^31 - 1024) is limited to it; the
- * positions of a page id outside [0, n_pages) are left out, as if masked.
- * Nothing behind len is used, whatever it holds.  (An infinite or NaN element of V at
- * a used position makes its output element infinite or NaN.)  out_dev overlaps no other
- * argument.  dtype (q and out): SD_F32
- * (with an SD_F16 or SD_E4M3 cache), SD_F16 or SD_BF16.  q_dev [R][n_head][head_dim]
- * with rows q_stride elements apart, out_dev the same with out_stride; pointers
- * are 16-byte aligned, strides multiples of 16 bytes.  lse_dev [R][n_head] (may be
- * NULL): the natural logarithm of the softmax's denominator, -inf for len 0.
- * n_head is a multiple of n_kv_head; an SD_E4M3 cache of head_dim 64 needs an even
- * page_size.  q enters the products with at least 22
- * bits (16-bit types with all of them), probabilities with 22 for SD_F32 results, 16 on
- * SD_BF16 caches, 11 otherwise; sums and statistics are fp32. */
+ * position j in page table_dev[r * table_stride + j / page_size]. len 0 (or negative)
+ * gives zeros; a len beyond table_stride * page_size (or 2^31 - 1024) is limited to it;
+ * the positions of a page id outside [0, n_pages) are left out, as if masked. Nothing
+ * behind len is used, whatever it holds. (An infinite or NaN element of V at a used
+ * position makes its output element infinite or NaN.) out_dev overlaps no other
+ * argument. dtype (q and out): SD_F32 (with an SD_F16 or SD_E4M3 cache), SD_F16 or
+ * SD_BF16. q_dev [R][n_head][head_dim] with rows q_stride elements apart, out_dev the
+ * same with out_stride; pointers are 16-byte aligned, strides multiples of 16 bytes.
+ * lse_dev [R][n_head] (may be NULL): the natural logarithm of the softmax's denominator,
+ * -inf for len 0. n_head is a multiple of n_kv_head; an SD_E4M3 cache of head_dim 64
+ * needs an even page_size. q enters the products with at least 22 bits (16-bit types
+ * with all of them, down to 2^-24 of a row's largest element), probabilities with 22 for
+ * SD_F32 results, 16 on SD_BF16 caches, 11 otherwise; sums and statistics are fp32. */
 int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
                     const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride,
                     int32_t n_head, float scale, void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
@@ -300,15 +299,16 @@ typedef struct sd_states {
     int32_t dtype, B, n_pos, n_kv_head, head_dim, reserved;
 } sd_states;
 
-/* Cross attention: every query i < Lq of row b attends to all len[b] states of its
- * row, whatever Lq is (masks, values that are not finite and overlap as in
- * sd_attend_pages),
+/* Cross attention: every query i < Lq of row b attends to all len[b] states of its row,
+ * whatever Lq is (masks, values that are not finite and overlap as in sd_attend_pages),
  *   out[b][i][h] = sum_{j < len} softmax_j(scale * q[b][i][h] . K[b][g][j]) V[b][g][j].
- * q_dev [B][Lq][n_head][head_dim]: batch rows q_batch elements apart (unused for B
- * 1), queries q_stride apart; out_dev the same with out_batch, out_stride.  A row
- * without states gives zeros.  States behind len are not used, whatever they hold.
- * dtype (q and out): SD_F32 (with SD_F16 states), SD_F16 or SD_BF16.  lse_dev
- * [B][Lq][n_head] (may be NULL) as in sd_attend_pages. */
+ * q_dev [B][Lq][n_head][head_dim]: batch rows q_batch elements apart (unused for B 1),
+ * queries q_stride apart; out_dev the same with out_batch, out_stride. A row without
+ * states gives zeros. States behind len are not used, whatever they hold. dtype (q and
+ * out): SD_F32 (with SD_F16 states), SD_F16 or SD_BF16. lse_dev [B][Lq][n_head] (may be
+ * NULL) as in sd_attend_pages. Precision as there; with more than 16 query rows to a kv
+ * head (Lq * n_head / n_kv_head) and one 16-bit type throughout, probabilities enter
+ * with that type's bits (SD_BF16: 8). */
 int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, const void* q_dev, int64_t q_batch,
                     int64_t q_stride, int32_t Lq, int32_t n_head, float scale, void* out_dev, int64_t out_batch,
                     int64_t out_stride, float* lse_dev, void* stream);
