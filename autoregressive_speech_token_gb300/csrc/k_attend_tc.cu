@@ -10,7 +10,11 @@
 //   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
 //   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
 //   O_i += P_i V_j (fp32, head_dim columns)
-// One thread issues all products, one all loads.  Two warpgroups each own one query
+// 8192 queries over 8000 and 8190 states, 16 heads of 128 in 8 groups, bf16: 610 us, 1.78 PFLOP/s,
+// bound by the tensor cores; heads of 64 by the exponentials (4 x 2048 over 2048: 80 us).
+//
+// One elected thread issues all products (from a lane compared by number it took 813 us
+// for that first case), one warp all loads.  Two warpgroups each own one query
 // tile, a thread per query: running maximum and sum need no exchange between
 // threads, and while one warpgroup forms P of its tile the tensor cores work on the
 // other's.  The reference m_i of the exponentials moves only when the maximum has
