@@ -12,7 +12,7 @@
 // The kernel is bound by the key and value bytes: 48 requests of up to 32768 positions, 8 kv
 // heads of 128, bf16, 651 MB take 104 us, 6.3 TB/s, 0.92 of the copy rate (e4m3, 64 requests of
 // 2000 to 4100, 64 heads to 8: 73 us, 0.81).  Three warps walk the block's share
-// and load by TMA, in turn, a tile's keys and values (32 KB each) into a ring, running
+// and load by TMA, in turn, a tile's keys or its values (32 KB) into a ring, running
 // ahead across the ends of units; a fourth prepares the units (where they lie, their queries).
 // Eight warps work on a tile, 16 or 32 positions each, with a running maximum and sum of
 // their own; four more merge and write a unit's result while the eight are at the next
@@ -149,8 +149,8 @@ struct Shape {
     static constexpr int kQueries = kSplitRows * HD * 4;        // a unit's queries, in their own type
     static constexpr int kStages = kStage >= 32768 ? 5 : 10;
     // A loader waits for the stage `kStages` before its own by parity, so the one 2 kStages before must be known to be
-    // free: it is, as every warp takes every tile in order and the loader has waited for a later one, 2 kLoaders - 1 before.
-    static_assert(kStages >= 2 * kLoaders - 1, "a loader could mistake the phase of a stage");
+    // free: it is, as every warp takes the stages in order and the loader has waited for one at most kLoaders earlier.
+    static_assert(kStages >= kLoaders, "a loader could mistake the phase of a stage");
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kRing + kMerge + kUnits * kQueries + 1024;
     // What beginning and ending a unit costs, in tiles: the share of a block counts it
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 float val[2][kVec], mm[2], ll[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = 2 * mw + e;
+                    const int r = mw + kMergers * e;
                     float mw_[kWarps];
                     mm[e] = -INFINITY;
                     ll[e] = 0.f;
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 }
                 __syncwarp();
                 if (lane == 0) mb_arrive(smem_u32(&s_free));
-                if (2 * mw >= u.rows) continue;
-                const int n_rows = min(2, u.rows - 2 * mw);
+                if (mw >= u.rows) continue;
+                const int n_rows = mw + kMergers < u.rows ? 2 : 1;
                 bool last = true;
                 if (u.c_lo != u.c_hi) {
                     // ---- the last block of the unit to arrive joins the records in block order
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (e >= n_rows) break;
-                        const int r = 2 * mw + e;
+                        const int r = mw + kMergers * e;
 #pragma unroll
                         for (int x = 0; x < kVec; ++x) __stcg(rec + r * HD + lane * kVec + x, val[e][x]);
                         if (lane == 0) __stcg(reinterpret_cast<float2*>(rec + kSplitRows * 128) + r, make_float2(mm[e], ll[e]));
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             if (e >= n_rows) break;
-                            const int r = 2 * mw + e;
+                            const int r = mw + kMergers * e;
                             mm[e] = -INFINITY;
                             ll[e] = 0.f;
 #pragma unroll
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (e >= n_rows) break;
-                    const int64_t m = u.m0 + 2 * mw + e, qi = a.Lq == 1 ? 0 : quot(m, G), h = (int64_t)u.g * G + (m - qi * G);
+                    const int64_t m = u.m0 + mw + kMergers * e, qi = a.Lq == 1 ? 0 : quot(m, G), h = (int64_t)u.g * G + (m - qi * G);
                     const int64_t at = u.b * a.o_batch + qi * a.o_stride + h * HD + lane * kVec;
                     const float inv = ll[e] == 0.f ? 0.f : vs / ll[e];
 #pragma unroll
@@ -496,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             }
             return;
         }
-        // ================================================ loads: of a tile the keys (a stage) and the values (the next)
+        // ================================================ loads: a stage is a tile's keys, the next one its values
         const uint32_t turn_of = warp - kWarps;
-        uint32_t n = 0, last = 0;                                         // tiles of all loaders so far; stages up to this one's last
+        uint32_t n = 0, last = 0;                                         // stages of all loaders so far; up to this one's last
         const int groups = args.groups, box = args.box;
         while (ok && next_unit(p)) {
             // of a lane's box (k * 32 + lane) of tile i: its page, -1 without one
@@ -508,8 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + a.by_ps.div((uint32_t)pos)) : p.b;
             };
             const int outer = a.table ? a.n_pages : a.B;
-            int i = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(i, 0);
-            for (; i < p.tiles && ok; i += kLoaders) {
+            int x = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(x >> 1, 0);
+            for (; x < 2 * p.tiles && ok; x += kLoaders) {
+                const int i = x >> 1, op = x & 1;
                 const int first = (p.i0 + i) * kTile, rest = p.len - first;
                 // of a box: its position within its page (or row)
                 auto inside = [&](int k) -> int {
@@ -517,60 +518,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                     return a.table ? pos - (int)(a.by_ps.div((uint32_t)pos) * a.by_ps.d) : pos;
                 };
                 const int id0 = (uint32_t)ahead < (uint32_t)outer ? ahead : -1, in0 = inside(0);
-                ahead = lookup(i + kLoaders, 0);                          // a tile ahead: not waited for here
+                ahead = lookup((x + kLoaders) >> 1, 0);                   // a stage ahead: not waited for here
+                const uint32_t st = n + x, slot = st % kSt, turn = st / kSt;
+                if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
+                if (!ok) break;
+                last = st + 1;
+                const uint32_t mb = smem_u32(&s_full[slot]), dst = ring + slot * S::kStage;
+                if (op == 0 && lane < kWarps) s_live[slot][lane] = 0;
+                __syncwarp();
 #pragma unroll 1
-                for (int op = 0; op < 2; ++op) {
-                    const uint32_t st = 2 * (n + i) + op, slot = st % kSt, turn = st / kSt;
-                    if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
-                    if (!ok) break;
-                    last = st + 1;
-                    const uint32_t mb = smem_u32(&s_full[slot]), dst = ring + slot * S::kStage;
-                    if (op == 0 && lane < kWarps) s_live[slot][lane] = 0;
-                    __syncwarp();
-#pragma unroll 1
-                    for (int k = 0; k * 32 < groups; ++k) {
-                        int id = id0, in = in0;
-                        if (k > 0) {
-                            id = lookup(i, k);
-                            if ((uint32_t)id >= (uint32_t)outer) id = -1;
-                            in = inside(k);
-                        }
-                        if (op == 0 && id >= 0) {
-                            // live positions of each warp's part of the tile
-                            const int at = (k * 32 + lane) * box, end = min(at + box, rest);
-                            for (int r = at; r < end;) {
-                                const int c = r / kChunk, stop = min(end, (c + 1) * kChunk), count = stop - r;
-                                atomicOr(&s_live[slot][c], (0xffffffffu >> (32 - count)) << (r - c * kChunk));
-                                r = stop;
-                            }
-                        }
-                        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-                        if (k > 0) __syncwarp();
-                        s_box[turn_of][lane] = make_int2(id, in);
-                        __syncwarp();
-                        // box by box from the elected lane (by several lanes of a warp at once: 250 cycles each)
-                        if (elect_one()) {
-                            if (have) mb_expect_more(mb, __popc(have) * box * S::kRow);
-                            const int boxes = min(32, groups - k * 32);
-                            uint32_t to = dst + k * 32 * box * S::kPart;
-                            for (int y = 0; y < boxes; ++y, to += box * S::kPart) {
-                                const int2 v = s_box[turn_of][y];
-                                if (v.x < 0) continue;
-#pragma unroll
-                                for (int part = 0; part < S::kParts; ++part)
-                                    tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, v.y, p.g, v.x, mb);
-                            }
+                for (int k = 0; k * 32 < groups; ++k) {
+                    int id = id0, in = in0;
+                    if (k > 0) {
+                        id = lookup(i, k);
+                        if ((uint32_t)id >= (uint32_t)outer) id = -1;
+                        in = inside(k);
+                    }
+                    if (op == 0 && id >= 0) {
+                        // live positions of each warp's part of the tile
+                        const int at = (k * 32 + lane) * box, end = min(at + box, rest);
+                        for (int r = at; r < end;) {
+                            const int c = r / kChunk, stop = min(end, (c + 1) * kChunk), count = stop - r;
+                            atomicOr(&s_live[slot][c], (0xffffffffu >> (32 - count)) << (r - c * kChunk));
+                            r = stop;
                         }
                     }
+                    const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+                    if (k > 0) __syncwarp();
+                    s_box[turn_of][lane] = make_int2(id, in);
                     __syncwarp();
-                    if (lane == 0) mb_arrive(mb);
+                    // box by box from the elected lane (by several lanes of a warp at once: 250 cycles each)
+                    if (elect_one()) {
+                        if (have) mb_expect_more(mb, __popc(have) * box * S::kRow);
+                        const int boxes = min(32, groups - k * 32);
+                        uint32_t to = dst + k * 32 * box * S::kPart;
+                        for (int y = 0; y < boxes; ++y, to += box * S::kPart) {
+                            const int2 v = s_box[turn_of][y];
+                            if (v.x < 0) continue;
+#pragma unroll
+                            for (int part = 0; part < S::kParts; ++part)
+                                tma4(to + part * (kTile * 128), op ? &args.v : &args.k, part * 64, v.y, p.g, v.x, mb);
+                        }
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mb_arrive(mb);
             }
-            n += max(p.tiles, 0);
+            n += 2 * max(p.tiles, 0);
         }
         if (!ok)                                                          // bounded: this warp's own copies
             for (uint32_t x = last > kSt ? last - kSt : 0; x < last; ++x) {
-                if ((x >> 1) % kLoaders != turn_of) continue;
+                if (x % kLoaders != turn_of) continue;
                 const long long t0 = clock64();
                 while (!mb_try(smem_u32(&s_full[x % kSt]), (x / kSt) & 1) && clock64() - t0 < kWaitClocks) {}
             }
