@@ -10,8 +10,8 @@
 // depend on the order of arrival).
 //
 // The kernel is bound by the key and value bytes: 48 requests of up to 32768 positions, 8 kv
-// heads of 128, bf16, 651 MB take 104 us, 6.3 TB/s, 0.92 of the copy rate (e4m3, 64 requests of
-// 2000 to 4100, 64 heads to 8: 73 us, 0.81).  Three warps walk the block's share
+// heads of 128, bf16, 651 MB take 101 us, 6.5 TB/s, 0.95 of the copy rate (e4m3, 64 requests of
+// 2000 to 4100, 64 heads to 8: 71 us, 0.83).  Three warps walk the block's share
 // and load by TMA, in turn, a tile's keys or its values (32 KB) into a ring, running
 // ahead across the ends of units; a fourth prepares the units (where they lie, their queries).
 // Eight warps work on a tile, 16 or 32 positions each, with a running maximum and sum of
