@@ -9,8 +9,9 @@
 struct sd_attn_ws {
     int device = 0, sms = 0;
     float* part = nullptr;
-    int* cnt = nullptr;
-    int* err = nullptr;              // pinned: a kernel's expired wait
+    int* cnt = nullptr;              // the counters, and behind them the word of AttendArgs::dead
+    int* err = nullptr;              // pinned: a kernel's expired wait, for the host
+    long long test_stall = 0;        // test hook (SD_TEST_STALL_US): cycles for one wait of the first uncaptured call
 };
 
 namespace sd {
@@ -27,6 +28,9 @@ struct AttendArgs {
     float scale;
     float* part;
     int *cnt, *err;
+    int* dead;                       // set with err.  A launch that finds it set (a replayed graph: no host call looks at err)
+                                     // leaves the counters alone, which are not zero then, and writes NaN
+    long long stall;                 // test hook: block 0 waits as many cycles for a barrier that nothing arrives at
 };
 
 constexpr int kSplitRows = 8;                                     // query rows of a unit
@@ -77,12 +81,12 @@ __device__ __forceinline__ bool mb_sleep(uint32_t mb, uint32_t parity) {
     return ok != 0;
 }
 // Bounded; gives up early once another warp of the block has given up.
-__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
+__device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile int* bad, long long limit = kWaitClocks) {
     if (mb_sleep(mb, parity)) return true;
     const long long t0 = clock64();
     while (!mb_sleep(mb, parity)) {
         if (*bad) return false;
-        if (clock64() - t0 > kWaitClocks) {
+        if (clock64() - t0 > limit) {
             *bad = 1;
             return false;
         }
@@ -90,8 +94,12 @@ __device__ __forceinline__ bool mb_wait(uint32_t mb, uint32_t parity, volatile i
     return true;
 }
 // The same by a whole warp, with one answer: what follows may be an instruction of all its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad) {
-    return __all_sync(0xffffffffu, mb_wait(mb, parity, bad));
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, volatile int* bad, long long limit = kWaitClocks) {
+    return __all_sync(0xffffffffu, mb_wait(mb, parity, bad, limit));
+}
+__device__ __forceinline__ void report_expired(const AttendArgs& a) {
+    *a.err = SD_ERR_TIMEOUT;
+    *a.dead = 1;
 }
 // One lane of a converged warp.  (The compiler keeps what such a branch computes in uniform registers, which a
 // comparison of lane numbers does not give.)

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     const AttendArgs& a = args.a;
     extern __shared__ unsigned char smraw[];
     __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt];
-    __shared__ __align__(8) unsigned long long s_ufull[kUnits], s_uempty[kUnits], s_done, s_free;
+    __shared__ __align__(8) unsigned long long s_ufull[kUnits], s_uempty[kUnits], s_done, s_free, s_never;
     __shared__ uint32_t s_live[kSt][kWarps];
     __shared__ Unit s_unit[kUnits];
     __shared__ int2 s_box[kLoaders][32];
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
         }
         mb_init(smem_u32(&s_done), kWarps);
         mb_init(smem_u32(&s_free), kMergers);
+        mb_init(smem_u32(&s_never), 1);
         for (int s = 0; s < kUnits; ++s) {
             mb_init(smem_u32(&s_ufull[s]), 1);
             mb_init(smem_u32(&s_uempty[s]), kWarps + kMergers);
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             // ============================================ mergers: two rows of every unit each, beside the next unit's tiles
             const int mw = warp - kWarps - kLoaders - 1;
             constexpr int kVec = HD / 32;                                 // columns of a lane
+            const bool dead = __ldcg(a.dead) != 0;                        // asked for here, needed behind the first unit's tiles
             for (uint32_t nu = 0;; ++nu) {
                 if (!warp_wait(smem_u32(&s_ufull[nu % kUnits]), (nu / kUnits) & 1, bad)) break;
                 const Unit u = s_unit[nu % kUnits];
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 if (mw >= u.rows) continue;
                 const int n_rows = mw + kMergers < u.rows ? 2 : 1;
                 bool last = true;
-                if (u.c_lo != u.c_hi) {
+                if (u.c_lo != u.c_hi && !dead) {
                     // ---- the last block of the unit to arrive joins the records in block order
                     float* rec = a.part + (int64_t)(2 * blockIdx.x + u.begins) * kSplitRecord;
 #pragma unroll
@@ -438,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                     }
                 }
                 if (!last) continue;
+                if (dead) ll[0] = ll[1] = NAN;
                 const float vs = a.v_scale ? __ldcg(a.v_scale + u.g) : 1.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                         a.lse[((int64_t)u.b * a.Lq + qi) * a.H + h] = ll[e] == 0.f ? -INFINITY : (mm[e] + log2f(ll[e]) - S::kShift) * kLn2;
                 }
             }
-            if (lane == 0 && *bad) *a.err = SD_ERR_TIMEOUT;
+            if (lane == 0 && *bad) report_expired(a);
             return;
         }
         Unit p;
@@ -563,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 }
                 __syncwarp();
                 if (lane == 0) mb_arrive(mb);
+                if (a.stall && blockIdx.x == 0 && turn_of == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
             }
             n += 2 * max(p.tiles, 0);
         }
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
         __syncwarp();
         if (lane == 0) mb_arrive(smem_u32(&s_done));
     }
-    if (tid == 0 && *bad) *a.err = SD_ERR_TIMEOUT;
+    if (tid == 0 && *bad) report_expired(a);
 }
 
 // K or V by strides, as [outer][head][position][hd]: boxes of `box` positions of up to 128 bytes of a row

@@ -1,4 +1,6 @@
 // sd_attend_pages and sd_attend_cross: arguments, workspace, and the choice of kernel.
+#include <algorithm>
+#include <cstdlib>
 #include <new>
 
 #include "attend_dev.cuh"
@@ -20,6 +22,8 @@ int check_q(const char* who, int dtype, int kv_dtype, const void* q, int64_t q_s
     return SD_OK;
 }
 
+size_t counters(int sms) { return (size_t)sms * kSplitRows / 2; }
+
 int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream) {
     DeviceScope scope(ws->device);
     if (scope.err != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(scope.err));
@@ -28,7 +32,15 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream)
     a.part = ws->part;
     a.cnt = ws->cnt;
     a.err = ws->err;
+    a.dead = ws->cnt + counters(ws->sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (ws->test_stall > 0) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusNone) {
+            a.stall = ws->test_stall;
+            ws->test_stall = 0;
+        }
+    }
     cudaError_t e = cudaSuccess;
     // Tensor-core tiles of 128 queries of a head: queries, keys and values of one 16-bit type, and more query rows to a
     // kv head than two units of the split kernel (16 rows of 1500 states, 16 heads of 64: 24 queries 32 us, 39 us
@@ -62,12 +74,18 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     cudaError_t e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, device);
     const size_t blocks = (size_t)ws->sms;
     if (e == cudaSuccess) e = cudaMalloc(&ws->part, blocks * kTcRecord * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, blocks * kSplitRows / 2 * sizeof(int));
+    const size_t words = counters(ws->sms) + 1;
+    if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, words * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
-    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, blocks * kSplitRows / 2 * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(ws->cnt, 0, words * sizeof(int));
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     if (e == cudaSuccess) e = cudaHostAlloc(&ws->err, sizeof(int), cudaHostAllocDefault);
     if (e == cudaSuccess) *ws->err = 0;
+    if (const char* ts = getenv("SD_TEST_STALL_US")) {
+        int khz = 0;
+        cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, device);
+        ws->test_stall = (long long)(khz > 0 ? khz : 2000000) * std::max(1, atoi(ts)) / 1000;
+    }
     if (e == cudaSuccess) e = prepare_attend_split();
     if (e == cudaSuccess) e = prepare_attend_tc();
     if (e != cudaSuccess) {

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
     constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     extern __shared__ unsigned char smraw[];
-    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_tail;
+    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_tail, s_never;
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad, s_row[32], s_len[32];
     const AttendArgs& a = t.a;
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
         mb_init(smem_u32(&s_qfull), 1);
         mb_init(smem_u32(&s_qempty), 1);
         mb_init(smem_u32(&s_tail), 1);
+        mb_init(smem_u32(&s_never), 1);
         for (int i = 0; i < 2; ++i) {
             mb_init(smem_u32(&s_sfull[i]), 1);
             mb_init(smem_u32(&s_pfull[i][0]), kM / 32);
@@ -352,8 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                     for (int p = 0; p < HD / 64; ++p)
                         tma4(dst + p * C::kPanel, (j & 1) ? &t.v : &t.k, p * 64, it.g, (it.i0 + (j >> 1)) * kN, it.b, mb);
                 }
+                if (a.stall && blockIdx.x == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
                 const int rest = it.len - (it.i0 + it.tiles - 1) * kN;
-                if (j == 2 * it.tiles - 1 && rest < kN) {
+                if (ok && j == 2 * it.tiles - 1 && rest < kN) {
                     // values behind the row's last position: 0 x anything must be 0
                     ok = warp_wait(mb, turn & 1, bad);
                     // one tail at a time: the products of the one before are complete (if its stage was loaded
@@ -460,13 +462,13 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + i * kN, to = tmem + lanes + C::kO + i * HD;
-        const float sl = a.scale * kLog2e;
+        const float sl = a.scale * kLog2e, l_first = __ldcg(a.dead) ? NAN : 0.f;
         uint32_t ns = 0, no = 0;
         bool ok = true;
         Item it;
         while (ok && next_item(it)) {
             if (i && !it.two) continue;
-            float m = -INFINITY, ref = 0.f, l = 0.f;
+            float m = -INFINITY, ref = 0.f, l = l_first;
             for (int j = 0; j < it.tiles; ++j) {
                 ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
                 if (!ok) break;
@@ -611,7 +613,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
     __syncthreads();
     tm_after();
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-    if (tid == 0 && s_bad) *a.err = SD_ERR_TIMEOUT;
+    if (tid == 0 && s_bad) report_expired(a);
 }
 
 // Joins the parts of the items that were cut: a block for each query tile of an item, the records in block order.

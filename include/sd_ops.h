@@ -260,8 +260,9 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
  * lengths, fixed at about 20 MB, allocated here on `device` (-1: the current one).
  * Calls with one workspace, replays of graphs that captured one among them, must
  * not overlap: one workspace for each stream.  A kernel whose bounded waits (about
- * two seconds each) expire leaves its results unfinished, and the next call with the
- * workspace returns SD_ERR_TIMEOUT, as does every later one. */
+ * two seconds each) expire leaves its results unfinished; every later call with the
+ * workspace returns SD_ERR_TIMEOUT, and what was captured or queued before runs on
+ * but writes NaN to all its results (out_dev and lse_dev). */
 typedef struct sd_attn_ws sd_attn_ws;
 /* Not while a stream is being captured. */
 int sd_attn_ws_create(int32_t device, sd_attn_ws** out);

@@ -1,0 +1,71 @@
+"""Paged and cross attention where a caller can be surprised: expired waits."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from .test_gpu_paged import (DT, HALF_STEP, attend_ref, bounds, build_cache, check_cross, gen, i32, make_states,  # noqa: E402
+                             randn, run_cross, run_paged, sd, ws)  # noqa: F401  (sd and ws are fixtures)
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = -6
+
+
+@pytest.mark.parametrize("kind,Lq,hd", [("pages", 1, 128), ("cross", 1, 64), ("cross", 300, 64), ("cross", 40, 128)])
+def test_an_expired_wait_is_reported_and_replays_give_nan(sd, monkeypatch, kind, Lq, hd):  # noqa: F811
+    """A test hook (SD_TEST_STALL_US) lets one load warp of the first uncaptured call wait 1 ms for a barrier that
+    nothing arrives at; the other waits of its block end on the recorded error.  The next call with the workspace is
+    refused.  A graph captured before has no host call that could refuse: its replays end and give NaN, not results
+    that some units joined from records of another pass.  Another workspace works."""
+    g = gen(50)
+    lens = [3000, 900]
+    monkeypatch.setenv("SD_TEST_STALL_US", "1000")
+    w = sd.AttnWorkspace()
+    monkeypatch.delenv("SD_TEST_STALL_US")
+    good = sd.AttnWorkspace()
+    ld = i32(lens)
+    lse = torch.zeros(2, Lq, 4, device="cuda")
+    if kind == "pages":
+        kc, vc, table, _ = build_cache(g, np.random.default_rng(50), lens, 2, hd, 16, "f16", "hnd")
+        q, cache = randn(g, 2, 4, hd, dt="f16"), sd.Pages.of(kc, vc)
+        out = torch.zeros_like(q)
+
+        def call(x):
+            sd.sd_attend_pages(x, cache, table, table.shape[1], ld, 2, sd.DTYPES["f16"], q, 4 * hd, 4, 0.1, out, 4 * hd,
+                               lse, torch.cuda.current_stream().cuda_stream)
+    else:
+        k, v = (randn(g, 2, 3000, 2, hd, dt="f16") for _ in range(2))
+        q, states = randn(g, 2, Lq, 4, hd, dt="f16"), sd.States.of(k, v, ld)
+        out = torch.zeros_like(q)
+
+        def call(x):
+            sd.sd_attend_cross(x, states, sd.DTYPES["f16"], q, q.stride(0), q.stride(1), Lq, 4, 0.1, out, q.stride(0),
+                               q.stride(1), lse, torch.cuda.current_stream().cuda_stream)
+    call(good)
+    torch.cuda.synchronize()
+    want, want_lse = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(w)                                                # captured: leaves the hook to the next call
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    call(w)                                                    # this one takes it
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with pytest.raises(sd.SdError) as e:
+            call(w)
+        assert e.value.code == TIMEOUT
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.all(torch.isnan(out)) and torch.all(torch.isnan(lse))
+    call(good)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
