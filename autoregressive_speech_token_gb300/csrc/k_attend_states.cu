@@ -22,6 +22,23 @@ int check_q(const char* who, int dtype, int kv_dtype, const void* q, int64_t q_s
     return SD_OK;
 }
 
+// Which kernel takes Lq queries of G heads to a kv head, where queries, keys and values have one 16-bit type: the
+// tensor-core kernel (true) or the split one.  Per kv head both walk the row's states once for each of their pieces,
+// the split kernel for every 8 (query, head) rows, the tensor-core kernel for every pair of tiles, a tile being up to
+// 128 queries of ONE head.  A walk of a pair takes as long as 3 of the split kernel's for heads of 64, 2 for heads of
+// 128.  GPU time in us, split / tensor cores, over 16 rows of 1500 states, bf16:
+//   heads of 64    64 to 1: 1 query 12 / 65, 8: 47 / 65    64 to 8: 8: 47 / 65, 12: 65 / 65, 16: 87 / 65
+//                  16 to 8: 12: 24.0 / 23.6, 16: 29 / 24   16 to 16: 16: 29 / 32, 24: 38 / 32
+//   heads of 128   64 to 1: 1: 17 / 74, 6: 62 / 74, 8: 79 / 74    32 to 8: 6: 38 / 41, 8: 47 / 41
+//                  16 to 8: 12: 38 / 27
+// Over bf16 the split kernel's probabilities have 16 bits, the other's 8: up to 16 rows to a kv head they keep them,
+// though 16 queries of 16 heads of 128 take 68 us there and 41 on tiles.  (fp16 probabilities have 11 in both.)
+bool on_tiles(int Lq, int G, int hd, bool bf) {
+    const int64_t rows = (int64_t)Lq * G, units = (rows + kSplitRows - 1) / kSplitRows;
+    const int64_t pairs = ((int64_t)G * (((int64_t)Lq + 127) / 128) + 1) / 2;
+    return units >= (hd == 64 ? 3 : 2) * pairs && (!bf || rows > 2 * kSplitRows);
+}
+
 size_t counters(int sms) { return (size_t)sms * kSplitRows / 2; }
 
 int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream) {
@@ -42,11 +59,8 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream)
         }
     }
     cudaError_t e = cudaSuccess;
-    // Tensor-core tiles of 128 queries of a head: queries, keys and values of one 16-bit type, and more query rows to a
-    // kv head than two units of the split kernel (16 rows of 1500 states, 16 heads of 64: 24 queries 32 us, 39 us
-    // split, 16 queries 32 and 29; 16 heads of 128 in 8 groups: 8 queries 25 and 30 us, 4 queries 24 and 19).
     bool taken = false;
-    if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && (int64_t)a.Lq * (a.H / a.Hkv) > 2 * kSplitRows)
+    if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && on_tiles(a.Lq, a.H / a.Hkv, hd, a.dtype == SD_BF16))
         e = launch_attend_tc(a, hd, ws->sms, st, &taken);
     if (!taken) e = launch_attend_split(a, hd, ws->sms, st);
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
