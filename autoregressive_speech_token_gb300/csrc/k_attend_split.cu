@@ -743,14 +743,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             }
             float ref[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e] - S::kShift;
+            for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e];
+            // 2^(s - m + shift), the shift behind the exact difference: m - shift is rounded from 2^24 on, up to 2^16 and
+            // beyond fp16
+            auto prob = [&](float s, float r) { return S::kShift == 0.f ? ex2(s - r) : ex2((s - r) + S::kShift); };
             // P^T as the B operand: each 8 positions x 8 heads transposed
             uint32_t ph[kH][2], pl[kH][2];
 #pragma unroll
             for (int h = 0; h < kH; ++h)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float p0 = ex2(s[h][2 * y] - ref[0]), p1 = ex2(s[h][2 * y + 1] - ref[1]);
+                    const float p0 = prob(s[h][2 * y], ref[0]), p1 = prob(s[h][2 * y + 1], ref[1]);
                     l[0] += p0;
                     l[1] += p1;
                     split2<S::kBf>(p0, p1, ph[h][y], pl[h][y]);

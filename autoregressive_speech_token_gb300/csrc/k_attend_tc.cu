@@ -42,6 +42,9 @@ constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "the shares exceed what the block was launched with");
 constexpr int kJoin = 4;                              // what cutting and joining items costs, in tiles
 constexpr float kSlack = 8.f;                        // log2 of the growth that moves the reference
+// Exponents from which a row subtracts its reference from the scores before they are scaled.  Below, s scale - ref in
+// one rounding is off by at most 2^-3 with ref's own, and probabilities stay below 2^16; above, by whole powers of two.
+constexpr float kFar = 0x1p20f;
 
 struct alignas(128) TcArgs {
     CUtensorMap q, k, v, o;
@@ -462,13 +465,15 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + i * kN, to = tmem + lanes + C::kO + i * HD;
-        const float sl = a.scale * kLog2e, l_first = __ldcg(a.dead) ? NAN : 0.f;
+        const float sl = a.scale * kLog2e, slack = fminf(kSlack / sl, 3.0e38f), l_first = __ldcg(a.dead) ? NAN : 0.f;
         uint32_t ns = 0, no = 0;
         bool ok = true;
         Item it;
         while (ok && next_item(it)) {
             if (i && !it.two) continue;
-            float m = -INFINITY, ref = 0.f, l = l_first;
+            // the score that the reference stands at, and the one from which it moves (far rows: they subtract in every
+            // tile); P = exp2((s - sub) sl - ref)
+            float top = -INFINITY, limit = -INFINITY, sub = 0.f, ref = 0.f, l = l_first;
             for (int j = 0; j < it.tiles; ++j) {
                 ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
                 if (!ok) break;
@@ -495,26 +500,36 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                 }
                 m0 = max3(m0, s[kN - 4], s[kN - 3]);
                 m1 = max3(m1, s[kN - 2], s[kN - 1]);
-                const float mx = fmaxf(max3(m0, m1, m2), m3) * sl;
-                const bool grow = mx > (m == -INFINITY ? -INFINITY : m + kSlack);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
-                    if (grow) m = mx;
-                    l *= f;
-                    if (j > 0) {
+                const float mx = fmaxf(max3(m0, m1, m2), m3);
+                if (__any_sync(0xffffffffu, mx > limit)) {
+                    const bool grow = mx > (sub != 0.f ? top : limit);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = !grow ? 1.f : top == -INFINITY ? 0.f : ex2((top - mx) * sl);
+                        if (grow) top = mx;
+                        l *= f;
+                        if (j > 0) {
 #pragma unroll
-                        for (int c = 0; c < HD; c += 16) {
-                            float o[16];
-                            tm_ld16(to + c, o);
-                            tm_wait_ld();
-                            after_wait(o);
+                            for (int c = 0; c < HD; c += 16) {
+                                float o[16];
+                                tm_ld16(to + c, o);
+                                tm_wait_ld();
+                                after_wait(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
+                                for (int e = 0; e < 16; ++e) o[e] *= f;
+                                tm_st16(to + c, reinterpret_cast<uint32_t*>(o));
+                            }
+                            tm_wait_st();
                         }
-                        tm_wait_st();
                     }
-                    ref = m == -INFINITY ? 0.f : m - kShift;
+                    const float m = top * sl;
+                    const bool far = fabsf(m) >= kFar && m != -INFINITY;
+                    sub = far ? top : 0.f;
+                    ref = (far || m == -INFINITY ? 0.f : m) - kShift;
+                    limit = far ? -INFINITY : top + slack;
+                    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                        for (int c = 0; c < kN; ++c) s[c] -= sub;
+                    }
                 }
                 float2 l0 = make_float2(0.f, 0.f), l1 = l0;
                 const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(-ref, -ref);
@@ -541,6 +556,7 @@ const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
             }
             if (!ok) break;
             // ---- the result
+            const float m = top * sl;
             const int x = it.first + i, h = it.g * G + x / t.nq, qi = (x % t.nq) * kM + r;
             if (it.tiles) {
                 ok = warp_wait(smem_u32(&s_ofull[i]), no & 1, bad);

@@ -1,5 +1,5 @@
 """Paged and cross attention where a caller can be surprised: expired waits, large groups
-of heads."""
+of heads, scores of any size."""
 
 import math
 
@@ -99,3 +99,28 @@ def test_few_queries_of_large_groups_keep_fine_probabilities(sd, ws, Lq, H, Hkv,
     check_cross(q, k, v, lens, scale, out, lse)
     share = check_plain(q, k, v, lens, scale, out)
     assert share < 0.75 if tiles else share > 0.95, share
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dt,kv,hd,Lq,e", [
+    ("f16", "f16", 64, 3, 9), ("f16", "f16", 128, 8, 11), ("f32", "f16", 64, 8, 10), ("f32", "f16", 128, 2, 30),
+    ("bf16", "f16", 64, 3, 11), ("bf16", "bf16", 128, 8, 40), ("f16", "f16", 64, 200, 9), ("f16", "f16", 128, 130, 11),
+    ("f16", "f16", 64, 200, 15), ("f16", "f16", 128, 40, 13), ("bf16", "bf16", 64, 200, 10), ("bf16", "bf16", 128, 130, 40)])
+def test_finite_scores_larger_than_their_steps(sd, ws, dt, kv, hd, Lq, e, sign):  # noqa: F811
+    """Scores of 2^23 and more, where the step between fp32 numbers is 1 or more: a reference subtracted after rounding
+    can be off by that many powers of two, beyond fp16's range.  One element of q and k is not 0, so the scores are
+    exact; every seventh position ties for the largest, and the result is the mean of their values."""
+    g = gen(52)
+    n = 300
+    q, k = torch.zeros(1, Lq, 1, hd, device="cuda"), torch.zeros(1, n, 1, hd, device="cuda")
+    top = torch.arange(n, device="cuda") % 7 == 3
+    q[0, :, 0, 5] = 2.0 ** e * (1 + torch.arange(Lq, device="cuda") % 8 / 8)
+    k[0, :, 0, 5] = torch.where(top, 2.0 ** 14, 2.0 ** 13) if sign > 0 else torch.where(top, -2.0 ** 14, -2.0 ** 15)
+    q, k, v = q.to(DT[dt]), k.to(DT[kv]), randn(g, 1, n, 1, hd, dt=kv)
+    out, lse = run_cross(sd, ws, q, k, v, [n], 1.0)
+    vt = v[0, top, 0].double()
+    ref, mag = vt.mean(0).expand(Lq, hd), vt.abs().mean(0).expand(Lq, hd)
+    tol, _ = bounds(ref, mag, torch.zeros(Lq, dtype=torch.float64, device="cuda"), n, dt, kv, hd)
+    assert torch.all((out[0, :, 0].double() - ref).abs() <= tol)
+    want = q[0, :, 0, 5].double() * sign * 2.0 ** 14
+    assert torch.all((lse[0, :, 0].double() - want).abs() <= want.abs() * 2.0 ** -21)
