@@ -69,19 +69,22 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t w) {
     asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(w));
     return d;
 }
-// x, y rounded to the product's type, and what the rounding left
+// What the rounding of q to fp16 left is kept 2^12 times as large (below 2): from 2^-25 on it would be subnormal
+constexpr float kLow = 4096.f;
+
+// x, y rounded to the product's type, and what the rounding left, times `up`
 template <bool BF>
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, float up = 1.f) {
     if constexpr (BF) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
         const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
+        const __nv_bfloat162 l = __floats2bfloat162_rn((x - f.x) * up, (y - f.y) * up);
         hi = *reinterpret_cast<const uint32_t*>(&h);
         lo = *reinterpret_cast<const uint32_t*>(&l);
     } else {
         const __half2 h = __floats2half2_rn(x, y);
         const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+        const __half2 l = __floats2half2_rn((x - f.x) * up, (y - f.y) * up);
         hi = *reinterpret_cast<const uint32_t*>(&h);
         lo = *reinterpret_cast<const uint32_t*>(&l);
     }
@@ -98,7 +101,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 // high and low product; an infinite high product has no low one (0 * inf)
-__device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? hi + lo : hi; }
+__device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? fmaf(lo, 1.f / kLow, hi) : hi; }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qh[k][e], ql[k][e]);
+                for (int e = 0; e < 2; ++e) split2<S::kBf>(x[k][e].x * down, x[k][e].y * down, qh[k][e], ql[k][e], kLow);
             scale[0] = __shfl_sync(0xffffffffu, row_scale, 8 * quad);
             scale[1] = __shfl_sync(0xffffffffu, row_scale, 8 * quad + 4);
         }

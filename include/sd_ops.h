@@ -281,9 +281,12 @@ void sd_attn_ws_destroy(sd_attn_ws* ws);
  * same with out_stride; pointers are 16-byte aligned, strides multiples of 16 bytes.
  * lse_dev [R][n_head] (may be NULL): the natural logarithm of the softmax's denominator,
  * -inf for len 0. n_head is a multiple of n_kv_head; an SD_E4M3 cache of head_dim 64
- * needs an even page_size. q enters the products with at least 22 bits (16-bit types
- * with all of them, down to 2^-24 of a row's largest element), probabilities with 22 for
- * SD_F32 results, 16 on SD_BF16 caches, 11 otherwise; sums and statistics are fp32. */
+ * needs an even page_size. SD_F32 q enters the products with 22 bits (elements below
+ * 2^-14 of their row's largest with an error of 2^-37 of it), 16-bit types exactly (SD_BF16
+ * with other caches: elements below 2^-17 with an error of 2^-25 of the largest).
+ * Probabilities enter with 22 bits for SD_F32 results, 16 on SD_BF16 caches, 11 otherwise
+ * (on SD_F16 and SD_E4M3 caches small ones have an error of up to 2^-40 of the largest);
+ * sums and statistics are fp32. */
 int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
                     const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride,
                     int32_t n_head, float scale, void* out_dev, int64_t out_stride, float* lse_dev, void* stream);

@@ -1,5 +1,5 @@
 """Paged and cross attention where a caller can be surprised: expired waits, large groups
-of heads, scores of any size."""
+of heads, scores of any size, queries of uneven elements."""
 
 import math
 
@@ -8,7 +8,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from .test_gpu_paged import (DT, HALF_STEP, attend_ref, bounds, build_cache, check_cross, gen, i32, make_states,  # noqa: E402
+from .test_gpu_paged import (DT, HALF_STEP, attend_ref, bounds, build_cache, check_cross, e4m3_values, gen, i32, make_states,  # noqa: E402
                              randn, run_cross, run_paged, sd, ws)  # noqa: F401  (sd and ws are fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +124,25 @@ def test_finite_scores_larger_than_their_steps(sd, ws, dt, kv, hd, Lq, e, sign):
     assert torch.all((out[0, :, 0].double() - ref).abs() <= tol)
     want = q[0, :, 0, 5].double() * sign * 2.0 ** 14
     assert torch.all((lse[0, :, 0].double() - want).abs() <= want.abs() * 2.0 ** -21)
+
+
+@pytest.mark.parametrize("cache,hd", [("f16", 64), ("f16", 128), ("e4m3", 128), ("e4m3", 64)])
+def test_fp32_queries_keep_their_bits_beside_a_large_element(sd, ws, cache, hd):  # noqa: F811
+    """One element of a row is 2^12 times the others, whose keys are large while its own is small: the small elements
+    make the scores, and an error relative to the row's largest would show."""
+    g = gen(53)
+    n, ps, H = 500, 16, 8
+    big = 8.0 if cache == "f16" else 5.0
+    kc, vc, table, rows = build_cache(g, np.random.default_rng(53), [n], 1, hd, ps, cache, "hnd")
+    q = randn(g, 1, H, hd) * 2.0 ** -12
+    q[..., 0] = 1.5
+    k = rows[0][0].to(torch.float16).float() * 2.0 ** big
+    k[..., 0] *= 2.0 ** -big * 2.0 ** -8
+    k = k.clamp(-448, 448).to(DT[cache]) if cache == "e4m3" else k.to(DT[cache])
+    slot = torch.arange(n, device="cuda")
+    kc[table[0, slot // ps].long(), :, slot % ps] = k
+    out, lse = run_paged(sd, ws, q, kc, vc, table, [n], 8.0)
+    ref, mag, size, ls = attend_ref(q[0].double(), e4m3_values(k[:, 0]), e4m3_values(rows[0][1][:, 0]), 8.0)
+    tol, tol_l = bounds(ref, mag, size, n, "f32", cache, hd)
+    assert torch.all((out[0].double() - ref).abs() <= tol), float(((out[0].double() - ref).abs() / tol).max())
+    assert torch.all((lse[0].double() - ls).abs() <= tol_l + ls.abs() * 2.0 ** -22)
