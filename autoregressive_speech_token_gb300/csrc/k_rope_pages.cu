@@ -4,7 +4,9 @@
 // Pair i of a head, (x_i, x_{i+hd/2}), turns by pos[axis(i)] theta^(-2i/hd).  The
 // frequency is kept as a 64-bit fraction of a turn: position times fraction modulo
 // 2^64 is the angle of any position without a long reduction (one integer
-// product; 64-bit floats would be needed otherwise).  Its upper 32 bits, taken
+// product; 64-bit floats would be needed otherwise).  The fraction is off by less than one of its
+// units, so the angle at position 2^31 by less than 2^-33 of a turn; a fraction rounded to a
+// double's 53 bits would be off by 2^-25 of a turn there.  Its upper 32 bits, taken
 // to the nearest quarter turn, leave |r| <= 1/8 turn, which fp32 holds to 2^-28
 // of a turn, and sincospif of it gives cos and sin to about their last bit.
 //
@@ -83,6 +85,29 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
                          << (16 * (i & 1));
         *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
+}
+
+// A number as the sum of two doubles: these steps are good to about 2^-100 of it, whatever a host compiler contracts.
+struct Twice {
+    double hi, lo;
+};
+inline Twice sum(double a, double b) {                     // |a| >= |b|
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+inline Twice times(Twice a, Twice b) {
+    const double p = a.hi * b.hi;
+    return sum(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, std::fma(a.hi, b.hi, -p))));
+}
+// One Newton step from the double root: x = r + (a - r^2) / (2 r)
+inline Twice root(Twice a) {
+    const double r = std::sqrt(a.hi);
+    return sum(r, (std::fma(-r, r, a.hi) + a.lo) / (2.0 * r));
+}
+// One correction of the double quotient
+inline Twice inverse(Twice a) {
+    const double r = 1.0 / a.hi;
+    return sum(r, std::fma(-r, a.lo, std::fma(-r, a.hi, 1.0)) * r);
 }
 
 template <typename T, typename TC, int HD, int kThreads>
@@ -218,6 +243,10 @@ int sd_rope_init(int32_t head_dim, double theta, int32_t n_axes, const int32_t* 
         }
         if (sum != half) return op_fail(SD_ERR_INVALID_ARG, "%s: the axes' pairs do not add up to head_dim/2", who);
     }
+    // theta^(-2/head_dim): 32 and 64 are powers of two, so square roots lead to it; the pairs are its powers, times 1/(2 pi)
+    Twice step = {theta, 0.0}, f = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
+    for (int n = 1; n < half; n *= 2) step = root(step);
+    step = inverse(step);
     *out = sd_rope{};
     out->head_dim = head_dim;
     out->n_axes = n_axes;
@@ -226,8 +255,10 @@ int sd_rope_init(int32_t head_dim, double theta, int32_t n_axes, const int32_t* 
         out->axis[i] = (uint8_t)a;
         --left[a];
         if (interleaved) a = (a + 1) % n_axes;
-        // turns per position, below 1/6, in units of 2^-64: exact scaling of a double
-        out->turn[i] = (uint64_t)ldexp(pow(theta, -2.0 * i / head_dim) / 6.283185307179586476925286766559, 64);
+        // turns per position, below 1/6, in units of 2^-64, rounded down; below 2^-11 the high part has a fraction
+        const double high = std::floor(std::ldexp(f.hi, 64));
+        out->turn[i] = (uint64_t)high + (uint64_t)(int64_t)std::floor(std::ldexp(f.lo, 64) + (std::ldexp(f.hi, 64) - high));
+        f = times(f, step);
     }
     return SD_OK;
 }
