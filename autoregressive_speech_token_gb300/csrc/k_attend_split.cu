@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                         __threadfence();
                     }
                     last = __shfl_sync(0xffffffffu, before, 0) == u.c_hi - u.c_lo;
+                    __syncwarp();                                         // orders the other lanes' reads of records behind lane 0's fence
                     if (last) {
                         if (lane == 0) a.cnt[u.c_lo * kMergers + mw] = 0;
 #pragma unroll
