@@ -125,10 +125,10 @@ int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_
                     int32_t n_head, float scale, void* out_dev, int64_t out_stride, float* lse_dev, void* stream) {
     using namespace sd;
     static const char* who = "sd_attend_pages";
+    if (R == 0) return SD_OK;
     sd_pages c;
     if (int rc = check_pages(who, cache, &c)) return rc;
     if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
-    if (R == 0) return SD_OK;
     if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
     if (int rc = check_q(who, dtype, c.dtype, q_dev, q_stride, out_dev, out_stride, n_head, c.n_kv_head, scale)) return rc;
     if (c.dtype == SD_E4M3 && c.head_dim == 64 && c.page_size % 2)
@@ -150,15 +150,16 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
                     int64_t out_stride, float* lse_dev, void* stream) {
     using namespace sd;
     static const char* who = "sd_attend_cross";
+    if (Lq == 0) return SD_OK;
     if (!states) return op_fail(SD_ERR_INVALID_ARG, "%s: states is NULL", who);
     sd_states s = *states;
+    if (s.B == 0) return SD_OK;
     if (s.dtype != SD_F16 && s.dtype != SD_BF16)
         return op_fail(SD_ERR_INVALID_ARG, "%s: states of type %d, not SD_F16 or SD_BF16", who, s.dtype);
     if (s.head_dim != 64 && s.head_dim != 128)
         return op_fail(SD_ERR_UNSUPPORTED, "%s: head_dim %d is not 64 or 128", who, s.head_dim);
     if (s.B < 0 || s.n_pos < 0 || s.n_kv_head < 1 || Lq < 0)
         return op_fail(SD_ERR_INVALID_ARG, "%s: B %d, n_pos %d, n_kv_head %d, Lq %d", who, s.B, s.n_pos, s.n_kv_head, Lq);
-    if (s.B == 0 || Lq == 0) return SD_OK;
     if (s.n_pos == 0) {                                            // nothing is read: any legal address and strides
         s.k_dev = s.v_dev = q_dev;
         s.head_stride = s.pos_stride = s.batch_stride = s.head_dim;

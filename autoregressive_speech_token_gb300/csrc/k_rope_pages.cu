@@ -269,12 +269,12 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
                         const sd_pages* cache, void* stream) {
     using namespace sd;
     static const char* who = "sd_rope_write_pages";
+    if (n == 0) return SD_OK;
     RopeArgs a;
     if (int rc = check_pages(who, cache, &a.c)) return rc;
     const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
     if (!b) return op_fail(SD_ERR_INVALID_ARG, "%s: type %d is not SD_F32, SD_F16 or SD_BF16", who, dtype);
     if (n < 0 || n_head < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: n %d, n_head %d", who, n, n_head);
-    if (n == 0) return SD_OK;
     if (!slot_dev || !k_dev || !v_dev || (rope && !pos_dev))
         return op_fail(SD_ERR_INVALID_ARG, "%s: NULL argument", who);
     if ((n_head > 0) != (q_dev != nullptr) || (n_head > 0) != (q_out_dev != nullptr))

@@ -164,8 +164,9 @@ int sd_attend_rows_static(const float* q_dev, const uint16_t* k_dev, const uint1
  * `stream` and return; nothing is allocated, copied or waited for, so they may be
  * captured into a graph.  They run on the calling thread's current device (the
  * attention entries: on their workspace's device); the stream and every pointer
- * belong to that device.  Return values report arguments and launches.  A call with
- * no rows (n, R, B or Lq 0) returns SD_OK and does nothing, whatever its pointers. */
+ * belong to that device.  Return values report arguments and launches.  A call of the
+ * write or of attention with no rows (n, R, B or Lq 0) returns SD_OK and does nothing,
+ * whatever its other arguments; sd_page_plan, which has something to write even then, refuses R 0. */
 
 /* Element types.  E4M3 is a cache type only. */
 enum { SD_F32 = 1, SD_F16 = 2, SD_BF16 = 3, SD_E4M3 = 4 };
