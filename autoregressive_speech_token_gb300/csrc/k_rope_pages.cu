@@ -203,7 +203,7 @@ cudaError_t launch_hd(const RopeArgs& a, cudaStream_t st) {
     // each and more threads, so that no thread takes a third piece.
     const bool many = a.n > 512;
     const int tokens = many ? 4 : 1;
-    const dim3 grid((a.n + tokens - 1) / tokens);
+    const dim3 grid((a.n - 1) / tokens + 1);
     const size_t smem = sizeof(float) * tokens * a.c.head_dim;
     if (a.c.head_dim == 64)
         return many ? launch_k(k_rope_pages<T, TC, 64, 128>, grid, dim3(128), smem, st, a, tokens)

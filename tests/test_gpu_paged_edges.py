@@ -146,3 +146,18 @@ def test_fp32_queries_keep_their_bits_beside_a_large_element(sd, ws, cache, hd):
     tol, tol_l = bounds(ref, mag, size, n, "f32", cache, hd)
     assert torch.all((out[0].double() - ref).abs() <= tol), float(((out[0].double() - ref).abs() / tol).max())
     assert torch.all((lse[0].double() - ls).abs() <= tol_l + ls.abs() * 2.0 ** -22)
+
+
+def test_write_of_the_most_tokens(sd):  # noqa: F811
+    """2^31 - 1 tokens, nearly all skipped, their rows one row of memory (stride 0)."""
+    n, hd = 2 ** 31 - 1, 64
+    slot = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slot[-1], slot[-4], slot[5] = 3, 9, 14
+    x = randn(gen(54), 1, 2 * hd, dt="f16")
+    kc, vc = (torch.zeros(1, 1, 16, hd, device="cuda", dtype=torch.float16) for _ in range(2))
+    sd.sd_rope_write_pages(None, None, 0, slot, n, sd.DTYPES["f16"], None, 0, None, 0, 0, x, x[:, hd:], 0,
+                           sd.Pages.of(kc, vc))
+    torch.cuda.synchronize()
+    used = torch.zeros(16, 1, dtype=torch.bool, device="cuda")
+    used[[3, 9, 14]] = True
+    assert torch.equal(kc[0, 0], torch.where(used, x[:, :hd], 0)) and torch.equal(vc[0, 0], torch.where(used, x[:, hd:], 0))
