@@ -161,3 +161,53 @@ def test_write_of_the_most_tokens(sd):  # noqa: F811
     used = torch.zeros(16, 1, dtype=torch.bool, device="cuda")
     used[[3, 9, 14]] = True
     assert torch.equal(kc[0, 0], torch.where(used, x[:, :hd], 0)) and torch.equal(vc[0, 0], torch.where(used, x[:, hd:], 0))
+
+
+@pytest.mark.parametrize("dt,kv,Lq,H,Hkv,hd", [("f16", "f16", 32, 16, 16, 64), ("bf16", "bf16", 200, 4, 2, 128),
+                                               ("f32", "f16", 32, 4, 4, 64), ("bf16", "bf16", 3, 8, 2, 128)])
+@pytest.mark.parametrize("same", ["batch", "rows", "both"])
+def test_queries_of_one_row_for_many(sd, ws, dt, kv, Lq, H, Hkv, hd, same):  # noqa: F811
+    """Learned queries for every row of the batch, or one query repeated: strides of 0."""
+    g = gen(55)
+    lens = [300, 0, 141]
+    k, v = make_states(g, lens, 300, Hkv, hd, kv, "blhd")
+    q = randn(g, 1 if same != "rows" else 3, Lq if same == "batch" else 1, H, hd, dt=dt).expand(3, Lq, H, hd)
+    out, lse = run_cross(sd, ws, q, k, v, lens, hd ** -0.5, pad=8)
+    check_cross(q, k, v, lens, hd ** -0.5, out, lse)
+    again, _ = run_cross(sd, ws, q.contiguous(), k, v, lens, hd ** -0.5)
+    assert torch.equal(out, again)
+
+
+def test_captured_calls_with_changed_lengths_against_plain(sd, ws):  # noqa: F811
+    """All heads of a replayed paged and a replayed cross call against 64 bits, the lengths changed since the capture
+    so that items are cut, left whole or empty."""
+    g = gen(56)
+    kc, vc, table, rows = build_cache(g, np.random.default_rng(56), [3000] * 4, 2, 128, 16, "f16", "hnd")
+    q, cq = randn(g, 4, 8, 128, dt="f16"), randn(g, 4, 40, 8, 128, dt="f16")
+    k, v = (randn(g, 4, 3000, 2, 128, dt="f16") for _ in range(2))
+    ld, cache = i32([3000] * 4), sd.Pages.of(kc, vc)
+    st = sd.States.of(k, v, ld)
+    out, cout = torch.zeros_like(q), torch.zeros_like(cq)
+    lse, clse = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 40, 8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = torch.cuda.current_stream().cuda_stream
+        sd.sd_attend_pages(ws, cache, table, table.shape[1], ld, 4, sd.DTYPES["f16"], q, 1024, 8, 0.1, out, 1024, lse, s)
+        sd.sd_attend_cross(ws, st, sd.DTYPES["f16"], cq, 40 * 1024, 1024, 40, 8, 0.1, cout, 40 * 1024, 1024, clse, s)
+    for n in ([3000, 5, 0, 700], [1, 2900, 64, 0], [0, 0, 0, 1], [1500] * 4, [128, 256, 257, 2999]):
+        ld.copy_(i32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_cross(cq, k, v, n, 0.1, cout, clse)
+        pk, pv = (torch.stack([r[x] for r in rows]) for x in (0, 1))
+        check_cross(q[:, None], pk, pv, n, 0.1, out[:, None], lse[:, None])
+
+
+def test_many_short_rows_cut_or_whole_against_plain(sd, ws):  # noqa: F811
+    """More rows than a warp's lanes with fewer items than SMs: parts are found by a walk over the rows."""
+    g = gen(57)
+    lens = [1500, 1, 0, 900] * 9
+    k, v = make_states(g, lens, 1500, 1, 64, "bf16", "blhd")
+    q = randn(g, len(lens), 30, 2, 64, dt="bf16")
+    out, lse = run_cross(sd, ws, q, k, v, lens, 0.125)
+    check_cross(q, k, v, lens, 0.125, out, lse)
