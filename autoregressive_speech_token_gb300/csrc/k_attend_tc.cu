@@ -5,13 +5,14 @@
 // kv head g), against all of that row's positions in tiles of 128.  One block per SM
 // takes whole items; where there are fewer items than SMs, they are cut into parts with a
 // block each, and a second kernel joins the parts in order (64 queries over 1500 states, 16
-// heads of 64: 12 us cut, 17 us whole; 128 over 32768, 16 heads of 128 in 8 groups: 39 and 324
+// heads of 64: 12 us cut, 17 us whole; 128 over 32768, 16 heads of 128 in 8 groups: 38 and 324
 // us).  Per position tile j and query tile i
 //   S_i = Q_i K_j^T (fp32, 128 columns of tensor memory)
 //   P_i = exp2(S_i scale log2(e) - m_i), rounded to the inputs' type, over S_i's columns
 //   O_i += P_i V_j (fp32, head_dim columns)
-// 8192 queries over 8000 and 8190 states, 16 heads of 128 in 8 groups, bf16: 610 us, 1.78 PFLOP/s,
-// bound by the tensor cores; heads of 64 by the exponentials (4 x 2048 over 2048: 80 us).
+// 8192 queries over 8000 and 8190 states, 16 heads of 128 in 8 groups, bf16: 608 us, 1.79 PFLOP/s, for some tens of
+// calls, 655 us, 1.66 PFLOP/s, for hundreds, as the power limit then lowers the clocks (a library product of 8192^3:
+// 1.92 and 1.73).  Bound by the tensor cores; heads of 64 by the exponentials (4 x 2048 over 2048: 81 us).
 //
 // One elected thread issues all products (from a lane compared by number it took 813 us
 // for that first case), one warp all loads.  Two warpgroups each own one query
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tc(const __grid_constant
                 tm_after();
                 auto scores = [&](int i, uint32_t stage) {
                     const uint64_t q = qdesc + (uint32_t)(i * (C::kTileBytes >> 4)), kd = kdesc + stage * (uint32_t)(C::kTileBytes >> 4);
-score_steps<HD, C::kPanel>(tmem + i * kN, q, kd, kIdescS);
+                    score_steps<HD, C::kPanel>(tmem + i * kN, q, kd, kIdescS);
                     commit(smem_u32(&s_sfull[i]));
                     any = true;
                 };
@@ -426,7 +427,7 @@ score_steps<HD, C::kPanel>(tmem + i * kN, q, kd, kIdescS);
                             ok = mb_wait(smem_u32(&s_pfull[i][half]), np[i] & 1, bad);
                             if (!ok) break;
                             tm_after();
-const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
+                            const uint32_t o = tmem + C::kO + i * HD, p = tmem + i * kN;
                             if (half == 0) result_steps<0, kN / 32>(o, p, vd, kIdescO, j > 0);
                             else result_steps<kN / 32, kN / 16>(o, p, vd, kIdescO, 1);
                         }

@@ -14,7 +14,8 @@
 // their sines and cosines are formed once, in shared memory, for all heads, while the
 // block's first loads are in flight; then each thread rotates 8 pairs of one head per
 // step with 16-byte loads and stores.  30011 tokens (483 MB) take 84 us, 0.85 of the copy rate,
-// into single positions of random pages.
+// into single positions of random pages.  Into e4m3 pages (424 MB) they take 93 us, 0.67: as many scattered rows,
+// half as long (with and without scales alike); fp32 tokens into fp16 pages (847 MB) 129 us, 0.97.
 #include <cmath>
 
 #include "pages_dev.cuh"

@@ -277,7 +277,8 @@ void sd_attn_ws_destroy(sd_attn_ws* ws);
  * the positions of a page id outside [0, n_pages) are left out, as if masked. Nothing
  * behind len is used, whatever it holds. (An infinite or NaN element of V at a used
  * position makes its output element infinite or NaN.) out_dev overlaps no other
- * argument. dtype (q and out): SD_F32 (with an SD_F16 or SD_E4M3 cache), SD_F16 or
+ * argument. (A row whose scores are all -inf gives zeros, like one without positions.)
+ * dtype (q and out): SD_F32 (with an SD_F16 or SD_E4M3 cache), SD_F16 or
  * SD_BF16. q_dev [R][n_head][head_dim] with rows q_stride elements apart, out_dev the
  * same with out_stride; pointers are 16-byte aligned, strides multiples of 16 bytes.
  * lse_dev [R][n_head] (may be NULL): the natural logarithm of the softmax's denominator,
