@@ -315,7 +315,7 @@ typedef struct sd_states {
  * NULL) as in sd_attend_pages. Precision as there; many queries of one 16-bit type with
  * their states enter probabilities with that type's bits (SD_BF16: 8): never with up to
  * 16 query rows to a kv head (Lq * n_head / n_kv_head) over SD_BF16 states, always from
- * 24 queries on. */
+ * 24 queries on, if the scale is positive. */
 int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, const void* q_dev, int64_t q_batch,
                     int64_t q_stride, int32_t Lq, int32_t n_head, float scale, void* out_dev, int64_t out_batch,
                     int64_t out_stride, float* lse_dev, void* stream);
