@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
         if (warp == kWarps + kLoaders) {
             // ============================================ units and their queries
             uint32_t n = 0;
+            if (a.stall && blockIdx.x == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
             for (; ok && next_unit(p); ++n) {
                 const uint32_t slot = n % kUnits;
                 if (n >= kUnits) ok = warp_wait(smem_u32(&s_uempty[slot]), (n / kUnits - 1) & 1, bad);
@@ -570,7 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 }
                 __syncwarp();
                 if (lane == 0) mb_arrive(mb);
-                if (a.stall && blockIdx.x == 0 && turn_of == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
             }
             n += 2 * max(p.tiles, 0);
         }
