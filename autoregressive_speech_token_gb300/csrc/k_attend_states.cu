@@ -67,6 +67,30 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream)
     return SD_OK;
 }
 
+// The arguments of attention over pages, checked
+int pages_args(const char* who, sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
+               const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride, int32_t n_head, float scale,
+               void* out_dev, int64_t out_stride, float* lse_dev, AttendArgs* out, int* hd) {
+    sd_pages c;
+    if (int rc = check_pages(who, cache, &c)) return rc;
+    if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
+    if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
+    if (int rc = check_q(who, dtype, c.dtype, q_dev, q_stride, out_dev, out_stride, n_head, c.n_kv_head, scale)) return rc;
+    if (c.dtype == SD_E4M3 && c.head_dim == 64 && c.page_size % 2)
+        return op_fail(SD_ERR_UNSUPPORTED, "%s: pages of an odd number of 64-byte rows", who);
+    if (!ws) return op_fail(SD_ERR_INVALID_ARG, "%s: ws is NULL", who);
+    AttendArgs& a = *out;
+    a.q = q_dev; a.k = c.k_dev; a.v = c.v_dev; a.out = out_dev; a.lse = lse_dev; a.table = table_dev; a.len = len_dev;
+    a.k_scale = c.k_scale_dev; a.v_scale = c.v_scale_dev; a.by_ps = FastDiv((uint32_t)c.page_size);
+    a.page_stride = c.page_stride; a.head_stride = c.head_stride; a.pos_stride = c.pos_stride;
+    a.q_batch = q_stride; a.q_stride = 0; a.o_batch = out_stride; a.o_stride = 0;
+    a.B = R; a.Lq = 1; a.H = n_head; a.Hkv = c.n_kv_head; a.n_pages = c.n_pages; a.table_stride = table_stride;
+    a.max_len = (int32_t)std::min<int64_t>((int64_t)table_stride * c.page_size, kMaxPositions);
+    a.dtype = dtype; a.kv_dtype = c.dtype; a.scale = scale;
+    *hd = c.head_dim;
+    return SD_OK;
+}
+
 }  // namespace
 }  // namespace sd
 
@@ -126,23 +150,30 @@ int sd_attend_pages(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_
     using namespace sd;
     static const char* who = "sd_attend_pages";
     if (R == 0) return SD_OK;
-    sd_pages c;
-    if (int rc = check_pages(who, cache, &c)) return rc;
-    if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
-    if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
-    if (int rc = check_q(who, dtype, c.dtype, q_dev, q_stride, out_dev, out_stride, n_head, c.n_kv_head, scale)) return rc;
-    if (c.dtype == SD_E4M3 && c.head_dim == 64 && c.page_size % 2)
-        return op_fail(SD_ERR_UNSUPPORTED, "%s: pages of an odd number of 64-byte rows", who);
-    if (!ws) return op_fail(SD_ERR_INVALID_ARG, "%s: ws is NULL", who);
     AttendArgs a = {};
-    a.q = q_dev; a.k = c.k_dev; a.v = c.v_dev; a.out = out_dev; a.lse = lse_dev; a.table = table_dev; a.len = len_dev;
-    a.k_scale = c.k_scale_dev; a.v_scale = c.v_scale_dev; a.by_ps = FastDiv((uint32_t)c.page_size);
-    a.page_stride = c.page_stride; a.head_stride = c.head_stride; a.pos_stride = c.pos_stride;
-    a.q_batch = q_stride; a.q_stride = 0; a.o_batch = out_stride; a.o_stride = 0;
-    a.B = R; a.Lq = 1; a.H = n_head; a.Hkv = c.n_kv_head; a.n_pages = c.n_pages; a.table_stride = table_stride;
-    a.max_len = (int32_t)std::min<int64_t>((int64_t)table_stride * c.page_size, kMaxPositions);
-    a.dtype = dtype; a.kv_dtype = c.dtype; a.scale = scale;
-    return launch(who, ws, a, c.head_dim, stream);
+    int hd = 0;
+    if (int rc = pages_args(who, ws, cache, table_dev, table_stride, len_dev, R, dtype, q_dev, q_stride, n_head, scale, out_dev,
+                            out_stride, lse_dev, &a, &hd))
+        return rc;
+    return launch(who, ws, a, hd, stream);
+}
+
+int sd_attend_shared(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
+                     const int32_t* len_dev, int32_t R, const int32_t* group_dev, const int32_t* shared_dev,
+                     int32_t n_groups, int32_t dtype, const void* q_dev, int64_t q_stride, int32_t n_head, float scale,
+                     void* out_dev, int64_t out_stride, float* lse_dev, void* stream) {
+    using namespace sd;
+    static const char* who = "sd_attend_shared";
+    if (R == 0) return SD_OK;
+    AttendArgs a = {};
+    int hd = 0;
+    if (int rc = pages_args(who, ws, cache, table_dev, table_stride, len_dev, R, dtype, q_dev, q_stride, n_head, scale, out_dev,
+                            out_stride, lse_dev, &a, &hd))
+        return rc;
+    if (n_groups < 0 || n_groups > R) return op_fail(SD_ERR_INVALID_ARG, "%s: n_groups %d of %d requests", who, n_groups, R);
+    if (n_groups > 0 && (!group_dev || !shared_dev))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: group_dev or shared_dev is NULL", who);
+    return launch(who, ws, a, hd, stream);
 }
 
 int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, const void* q_dev, int64_t q_batch,

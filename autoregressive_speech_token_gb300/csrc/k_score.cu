@@ -1,0 +1,517 @@
+// sd_score_rows: log probability and rank of a given token, entropy, and the most
+// probable alternatives of rows of logits.
+//
+// With d_j = z_j - m, m the row's largest logit, S = sum e^(d/T) and D = sum d e^(d/T),
+//   log p_j = d_j / T - log S,   H = log S - D / (S T)   (both terms of H are >= 0: nothing cancels).
+//
+// A row is read from memory once: every thread keeps a running maximum with the sums that belong to it.  Long rows, and
+// rows that are fewer than the SMs, are cut over a thread-block cluster, whose blocks exchange their maxima, sums and
+// best entries through distributed shared memory.
+//
+// The first n entries of (z descending, index ascending): every entry is the 64-bit key (order of z, ~index), 0 if it is
+// no alternative.  The best keys of groups of threads are ranked among each other.  The n-th of them is a bound: at least
+// n keys reach it, and only keys of the n groups whose best one does.  Those read their part again (from a cache), collect
+// what reaches the bound (a few more than n) and rank it.
+// Where too many reach it (adversarial order), the n best are taken one after the other.
+//
+// Bound by the one read where rows are many, by the chain of exchanges where they are few.
+#include <algorithm>
+
+#include "pages_dev.cuh"
+namespace sd {
+namespace {
+
+// Where an access refused itself: the address, for a debugger.  Every address below is aligned by construction (the same
+// code on the host, under a sanitizer, shows no other), yet without these checks one block of one row with token -1
+// ended with a "misaligned address" on GB300 (CUDA 13.0), and with them nothing is ever refused.  They stay until the
+// cause is known.
+__device__ unsigned long long g_refused[32];
+__device__ __forceinline__ bool aligned(const void* p, int n, int access) {
+    if ((reinterpret_cast<unsigned long long>(p) & (n - 1)) == 0) return true;
+    g_refused[access] = reinterpret_cast<unsigned long long>(p);
+    return false;
+}
+
+constexpr int kMaxTop = 32, kMaxCluster = 16, kList = 512;
+constexpr int kMaxVocab = 262144;
+
+struct ScoreArgs {
+    const void* z;
+    const int32_t* token;
+    float *logp, *entropy, *top_logp;
+    int32_t *rank, *top_id;
+    int64_t stride;
+    int32_t V, top;
+    float T, c;                                            // temperature; log2(e) / T
+};
+
+__device__ __forceinline__ float ex2_(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan_(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// Order of the values as unsigned numbers (both zeros alike); 0: no alternative (-inf, NaN)
+__device__ __forceinline__ uint32_t order_of(float x) {
+    if (!(x > -INFINITY)) return 0;
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o); }
+
+using Key = unsigned long long;
+__device__ __forceinline__ Key key_of(float x, int32_t index) {
+    const uint32_t o = order_of(x);
+    return o ? (Key)o << 32 | (uint32_t)~index : 0;
+}
+__device__ __forceinline__ Key max_key(Key a, Key b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+    return x;
+}
+__device__ __forceinline__ Key remote_key(uint32_t addr) {
+    Key x;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float remote_float(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_size() {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(x));
+    return (int)x;
+}
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(x));
+    return (int)x;
+}
+
+template <typename T>
+struct Type {
+    static constexpr int kN = 16 / sizeof(T);              // elements of a 16-byte vector
+    static constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr uint32_t kLow = sizeof(T) == 4 ? 0xff800000u : kBf ? 0xff80ff80u : 0xfc00fc00u;   // -inf
+    using Pair = std::conditional_t<kBf, __nv_bfloat162, __half2>;
+};
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int e) { return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w; }
+// Element e of a vector
+template <typename T>
+__device__ __forceinline__ float element(const uint4& w, int e) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(word_of(w, e));
+    else {
+        const uint32_t x = word_of(w, e >> 1);
+        if constexpr (Type<T>::kBf) return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
+        else return __half2float(__ushort_as_half((unsigned short)((e & 1) ? x >> 16 : x)));
+    }
+}
+// The larger of each two, of a number and NaN the number
+template <typename T>
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else {
+        using Pair = typename Type<T>::Pair;
+        const Pair m = __hmax2(*reinterpret_cast<const Pair*>(&a), *reinterpret_cast<const Pair*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+}
+
+__device__ __forceinline__ float number(float x) { return x; }
+__device__ __forceinline__ float number(__half x) { return __half2float(x); }
+__device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The elements of a vector that the row has, the others -inf
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const T* row, int first, int32_t V) {
+    uint32_t w[4] = {Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow};
+#pragma unroll
+    for (int e = 0; e < Type<T>::kN; ++e) {
+        const int j = first + e;
+        if (j < 0 || j >= V) continue;
+        if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(row[j]);
+        else {
+            const uint32_t b = *reinterpret_cast<const unsigned short*>(row + j);
+            w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | b << 16 : (w[e >> 1] & 0xffff0000u) | b;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kBatch = 4;                                  // vectors of a thread in flight
+
+template <typename T, int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
+    constexpr int kN = Type<T>::kN, kWarps = kThreads / 32, kGroups = kThreads / 4;
+    __shared__ Key s_best[kGroups], s_list[kList], s_top[kMaxTop], s_tau;
+    __shared__ float s_max[kWarps], s_S[kWarps], s_D[kWarps], s_mine[3];           // s_mine: this block's maximum, S, D
+    __shared__ int s_ahead[kWarps], s_mine_ahead, s_count;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = kCluster ? cluster_size() : 1, c = kCluster ? cluster_rank() : 0;
+    const int64_t row = blockIdx.x / C;
+    const T* z = static_cast<const T*>(a.z) + row * a.stride;
+    const int lead = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));     // elements between a 16-byte boundary and the row
+
+    // ---- this thread's vectors: v0 + tid, v0 + tid + kThreads, ... of the row; vector v begins with element v kN - lead
+    const int all = (a.V + lead + kN - 1) / kN, each = (all + C - 1) / C, v0 = c * each, nv = min(each, all - v0);
+    const int whole = (a.V + lead) / kN;                   // vectors [lead > 0, whole) lie within the row
+    auto vector = [&](int i) {
+        const int v = v0 + i;
+        return v >= (lead > 0) && v < whole && aligned(z + (v * kN - lead),16,0) ? *reinterpret_cast<const uint4*>(z + (v * kN - lead)) : load_edge(z, v * kN - lead, a.V);
+    };
+    const int32_t token = a.token && aligned(a.token+row,4,1) ? a.token[row] : -1;
+    const bool given = (uint32_t)token < (uint32_t)a.V;
+    const float zt = given && aligned(z+token,sizeof(T),2) ? number(z[token]) : -INFINITY;
+
+    // ---- running maximum and sums, and how many entries are ahead of the token.  The difference to the maximum is formed
+    // first: exact where it counts, whatever the logits' size.  Nothing 200 / c below it counts, which keeps it finite.
+    const float least = -200.f / a.c;
+    float m = -INFINITY, S = 0.f, D = 0.f;
+    int ahead = 0, best_j = 0;
+    uint4 best = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
+    auto add = [&](const uint4& w, int j) {
+        uint32_t mw = max_words<T>(max_words<T>(w.x, w.y), max_words<T>(w.z, w.w));
+        const float top = sizeof(T) == 4 ? __uint_as_float(mw) : fmaxf(element<T>(make_uint4(mw, 0, 0, 0), 0), element<T>(make_uint4(mw, 0, 0, 0), 1));
+        if (top > m) {
+            const float by = fmaxf(m - top, least), f = ex2_(by * a.c);
+            D = (D + S * by) * f;
+            S *= f;
+            m = top;
+            best = w;
+            best_j = j;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const float d = max_nan_(element<T>(w, e) - ref, least), p = ex2_(d * a.c);
+            S += p;
+            D = fmaf(d, p, D);
+        }
+        if (j > token) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) > zt;
+        } else if (j >= 0 && j + kN <= token) {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) >= zt;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                const float x = element<T>(w, e);
+                ahead += x > zt || (x == zt && (uint32_t)(j + e) < (uint32_t)token);
+            }
+        }
+    };
+    for (int i = tid; i < nv; i += kThreads * kBatch) {
+        uint4 w[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (i + b * kThreads < nv) w[b] = vector(i + b * kThreads);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (i + b * kThreads < nv) add(w[b], (v0 + i + b * kThreads) * kN - lead);
+    }
+
+    // ---- the block's maximum, and its sums
+    float mb = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    if (lane == 0 && aligned(s_max+warp,4,3)) s_max[warp] = mb;
+    if (a.top) {
+        // the best key of four threads
+        int at = 0;
+#pragma unroll
+        for (int e = kN - 1; e >= 0; --e) at = element<T>(best, e) == m ? best_j + e : at;
+        Key key = key_of(m, at);
+        key = max_key(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        key = max_key(key, __shfl_xor_sync(0xffffffffu, key, 2));
+        if ((tid & 3) == 0 && aligned(s_best+(tid>>2),8,4)) s_best[tid >> 2] = key;
+        if (tid == 0) {
+            s_count = 0;
+            s_tau = 0;
+        }
+        if (tid < kMaxTop && aligned(s_top+tid,8,5)) s_top[tid] = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mb = fmaxf(mb, s_max[w]);
+    if (m != mb) {                                         // (a thread without a number may have seen NaN: kept)
+        const float by = m == -INFINITY ? 0.f : fmaxf(m - mb, least), f = ex2_(by * a.c);
+        D = (D + S * by) * f;
+        S *= f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        S += __shfl_xor_sync(0xffffffffu, S, o);
+        D += __shfl_xor_sync(0xffffffffu, D, o);
+    }
+    ahead = __reduce_add_sync(0xffffffffu, ahead);
+    if (lane == 0) {
+        s_S[warp] = S;
+        s_D[warp] = D;
+        s_ahead[warp] = ahead;
+    }
+
+    // ---- the block's first entries
+    if (a.top) {
+        // group tid / 4 against a quarter of the groups
+        const Key key = s_best[tid >> 2];
+        int before = 0;
+#pragma unroll 8
+        for (int g = 0; g < kGroups / 4; ++g) before += s_best[g * 4 + (tid & 3)] > key;
+        before += __shfl_xor_sync(0xffffffffu, before, 1);
+        before += __shfl_xor_sync(0xffffffffu, before, 2);
+        if ((tid & 3) == 0 && key && before == a.top - 1) s_tau = key;          // keys are distinct
+        __syncthreads();
+        const Key tau = max_key(s_tau, 1);                 // fewer groups than n with an entry: all entries
+        if (key >= tau) {
+            const float bound = tau > 1 ? value_of((uint32_t)(tau >> 32)) : -INFINITY;
+            if (m >= bound) {
+#pragma unroll 2
+                for (int i = tid; i < nv; i += kThreads) {
+                    const uint4 w = vector(i);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        const float x = element<T>(w, e);
+                        if (!(x >= bound)) continue;
+                        const Key k = key_of(x, (v0 + i) * kN - lead + e);
+                        if (k >= tau) {
+                            const int at = atomicAdd(&s_count, 1);
+                            if (at < kList && aligned(s_list+at,8,6)) s_list[at] = k;
+                        }
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int n = s_count;
+        if (n <= kList) {
+            for (int i = tid; i < n; i += kThreads) {
+                const Key x = s_list[i];
+                int r = 0;
+                for (int j = 0; j < n; ++j) r += s_list[j] > x;
+                if (r < a.top && aligned(s_top+r,8,7)) s_top[r] = x;
+            }
+        } else {
+            Key last = ~(Key)0;
+            for (int k = 0; k < a.top; ++k) {
+                Key most = 0;
+                for (int i = tid; i < nv; i += kThreads) {
+                    const uint4 w = vector(i);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) {
+                        const Key x = key_of(element<T>(w, e), (v0 + i) * kN - lead + e);
+                        if (x < last) most = max_key(most, x);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) most = max_key(most, __shfl_xor_sync(0xffffffffu, most, o));
+                __syncthreads();
+                if (lane == 0) s_list[warp] = most;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) most = max_key(most, s_list[w]);
+                if (tid == 0) s_top[k] = most;
+                last = most;
+                if (!most) break;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        float s = 0.f, d = 0.f;
+        int n = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            s += s_S[w];
+            d += s_D[w];
+            n += s_ahead[w];
+        }
+        s_mine[0] = mb;
+        s_mine[1] = s;
+        s_mine[2] = d;
+        s_mine_ahead = n;
+    }
+
+    // ---- the row's: the cluster's first block gathers
+    Key* s_all = s_list;                                  // [block][kMaxTop]
+    static_assert(kList >= kMaxCluster * kMaxTop, "the lists of all blocks");
+    float m_of = -INFINITY, s_of = 0.f, d_of = 0.f;        // of block `lane`
+    int ahead_of = 0;
+    if constexpr (kCluster) {
+        cluster_sync();
+        if (c == 0) {
+            for (int i = tid; i < C * a.top; i += kThreads) {
+                const int r = i / a.top, k = i - r * a.top;
+                s_all[r * kMaxTop + k] = remote_key(remote(smem_addr(s_top + k), r));
+            }
+            if (lane < C) {
+                m_of = remote_float(remote(smem_addr(s_mine), lane));
+                s_of = remote_float(remote(smem_addr(s_mine + 1), lane));
+                d_of = remote_float(remote(smem_addr(s_mine + 2), lane));
+                ahead_of = __float_as_int(remote_float(remote(smem_addr(&s_mine_ahead), lane)));
+            }
+        }
+        cluster_sync();                                    // nothing of another block is read behind this
+    } else {
+        __syncthreads();
+        if (lane == 0) {
+            m_of = s_mine[0];
+            s_of = s_mine[1];
+            d_of = s_mine[2];
+            ahead_of = s_mine_ahead;
+        }
+    }
+    if (c != 0) return;
+    float M = m_of;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    {
+        const float by = m_of == -INFINITY ? 0.f : max_nan_(m_of - M, least), f = ex2_(by * a.c);
+        S = s_of * f;
+        D = (d_of + s_of * by) * f;
+        ahead = ahead_of;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        S += __shfl_xor_sync(0xffffffffu, S, o);
+        D += __shfl_xor_sync(0xffffffffu, D, o);
+    }
+    ahead = __reduce_add_sync(0xffffffffu, ahead);
+    const float log_s = logf(S);
+    // log p of a logit; a row without a finite logit has none
+    auto log_p = [&](float x) { return S == 0.f ? -INFINITY : (x - M) / a.T - log_s; };
+    if (tid == 0) {
+        if (a.logp && aligned(a.logp+row,4,8)) a.logp[row] = given ? log_p(zt) : 0.f;
+        if (a.rank && aligned(a.rank+row,4,9)) a.rank[row] = given ? ahead : -1;
+        if (a.entropy && aligned(a.entropy+row,4,10)) a.entropy[row] = S == 0.f ? 0.f : log_s - D / S / a.T;
+    }
+    if (!a.top) return;
+    auto put = [&](int r, Key x) {
+        if (!aligned(a.top_id+row * a.top + r,4,11) || !aligned(a.top_logp+row * a.top + r,4,12)) return;
+        a.top_id[row * a.top + r] = x ? (int32_t)~(uint32_t)x : -1;
+        a.top_logp[row * a.top + r] = x ? log_p(value_of((uint32_t)(x >> 32))) : -INFINITY;
+    };
+    if constexpr (!kCluster) {
+        if (tid < a.top) put(tid, s_top[tid]);
+        return;
+    }
+    // keys of all blocks: the place in the own list, and how many of each other list are ahead
+    for (int i = tid; i < C * a.top; i += kThreads) {
+        const int r = i / a.top, k = i - r * a.top;
+        const Key x = s_all[r * kMaxTop + k];
+        if (!x) continue;
+        int place = k;
+        for (int q = 0; q < C && place < a.top; ++q) {
+            if (q == r) continue;
+            int lo = 0, hi = a.top;                        // sorted, falling
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (s_all[q * kMaxTop + mid] > x) lo = mid + 1;
+                else hi = mid;
+            }
+            place += lo;
+        }
+        if (place < a.top) put(place, x);
+    }
+    // places that no entry takes
+    int have = 0;
+    for (int q = 0; q < C; ++q) {
+        int lo = 0, hi = a.top;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_all[q * kMaxTop + mid]) lo = mid + 1;
+            else hi = mid;
+        }
+        have += lo;
+    }
+    if (tid < a.top && tid >= have) put(tid, 0);
+}
+
+template <typename T, int kThreads, bool kCluster>
+cudaError_t launch_as(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
+    auto kernel = k_score<T, kThreads, kCluster>;
+    if (!kCluster) return launch_k(kernel, dim3((unsigned)rows), dim3(kThreads), 0, st, a);
+    if (C > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)rows * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = use_pdl() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <typename T, int kThreads>
+cudaError_t launch(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
+    return C > 1 ? launch_as<T, kThreads, true>(a, rows, C, st) : launch_as<T, kThreads, false>(a, rows, C, st);
+}
+
+template <typename T>
+cudaError_t choose(const ScoreArgs& a, int rows, int sms, cudaStream_t st) {
+    const int64_t bytes = ((int64_t)a.V + 2 * Type<T>::kN - 2) / Type<T>::kN * 16;      // a row may begin and end inside a vector
+    int C = 1;
+    while (C < kMaxCluster && bytes > (int64_t)C * 65536) C *= 2;
+    // few rows: over more SMs, as long as a block keeps 16 KB
+    while (C < kMaxCluster && (int64_t)rows * C * 2 <= sms && bytes > (int64_t)C * 16384) C *= 2;
+    if ((int64_t)rows * C > INT32_MAX) return cudaErrorInvalidValue;
+    return bytes <= 16384 && rows > 2 * sms ? launch<T, 128>(a, rows, C, st) : launch<T, 512>(a, rows, C, st);
+}
+
+}  // namespace
+}  // namespace sd
+
+extern "C" int sd_score_rows(const void* logits_dev, int64_t stride, int32_t dtype, int32_t rows, int32_t V,
+                             float temperature, const int32_t* token_dev, float* logp_dev, int32_t* rank_dev,
+                             float* entropy_dev, int32_t top_n, int32_t* top_id_dev, float* top_logp_dev, void* stream) {
+    using namespace sd;
+    static const char* who = "sd_score_rows";
+    if (rows == 0) return SD_OK;
+    const int b = dtype == SD_E4M3 ? 0 : dtype_bytes(dtype);
+    if (!b) return op_fail(SD_ERR_INVALID_ARG, "%s: type %d is not SD_F32, SD_F16 or SD_BF16", who, dtype);
+    if (rows < 0 || V < 1 || top_n < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: rows %d, V %d, top_n %d", who, rows, V, top_n);
+    if (V > kMaxVocab || top_n > kMaxTop)
+        return op_fail(SD_ERR_UNSUPPORTED, "%s: V %d (up to %d), top_n %d (up to %d)", who, V, kMaxVocab, top_n, kMaxTop);
+    if (!logits_dev || (reinterpret_cast<uintptr_t>(logits_dev) % b))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: logits_dev is NULL or not aligned to its elements", who);
+    if (rows > 1 && stride < V) return op_fail(SD_ERR_INVALID_ARG, "%s: stride %lld is below V %d", who, (long long)stride, V);
+    if (!(temperature >= 1e-30f && temperature <= 1e30f))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: temperature %g", who, (double)temperature);
+    if (!token_dev && (logp_dev || rank_dev))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: logp_dev and rank_dev need token_dev", who);
+    if (top_n > 0 && (!top_id_dev || !top_logp_dev))
+        return op_fail(SD_ERR_INVALID_ARG, "%s: top_id_dev or top_logp_dev is NULL", who);
+    ScoreArgs a = {};
+    a.z = logits_dev; a.token = token_dev; a.logp = logp_dev; a.entropy = entropy_dev; a.top_logp = top_logp_dev;
+    a.rank = rank_dev; a.top_id = top_id_dev; a.stride = rows > 1 ? stride : 0; a.V = V; a.top = top_n; a.T = temperature;
+    a.c = (float)(1.4426950408889634 / (double)temperature);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (e == cudaSuccess)
+        e = dtype == SD_F32 ? choose<float>(a, rows, sms, st)
+            : dtype == SD_F16 ? choose<__half>(a, rows, sms, st) : choose<__nv_bfloat16>(a, rows, sms, st);
+    if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    return SD_OK;
+}
+

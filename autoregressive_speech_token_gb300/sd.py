@@ -29,7 +29,8 @@ EXPORTS = ["sd_create", "sd_load_weights", "sd_prefill", "sd_prefill_shared", "s
            "sd_decode_n", "sd_get_logits", "sd_reset", "sd_destroy", "sd_last_error", "sd_get_info",
            "sd_qmat_create", "sd_qmat_destroy", "sd_qmat_dequant", "sd_qmat_gemv", "sd_qmat_gemm", "sd_qmat_gemm16", "sd_qmat_gemm_tc", "sd_sample_rows", "sd_sample_rows_ladder",
            "sd_attend_rows", "sd_attend_rows_static", "sd_page_plan", "sd_rope_init", "sd_rope_write_pages",
-           "sd_attn_ws_create", "sd_attn_ws_destroy", "sd_attend_pages", "sd_attend_cross"]
+           "sd_attn_ws_create", "sd_attn_ws_destroy", "sd_attend_pages", "sd_attend_cross", "sd_page_work", "sd_page_fork",
+           "sd_page_compact", "sd_page_copy", "sd_attend_shared", "sd_score_rows"]
 
 
 class SdError(RuntimeError):
@@ -110,6 +111,19 @@ class Pages(C.Structure):
         return p
 
 
+class PageArray:
+    """The caches of several layers, of one type, shape and strides: the array that sd_page_copy takes."""
+
+    def __init__(self, caches):
+        self.held = list(caches)
+        self.n = len(self.held)
+        self.array = (Pages * self.n)(*self.held)
+
+    @classmethod
+    def of(cls, caches) -> "PageArray":
+        return cls(caches)
+
+
 class Rope(C.Structure):
     """sd_rope: rotary frequencies and the axis of each pair."""
     _fields_ = [("turn", C.c_uint64 * 64), ("axis", C.c_uint8 * 64), ("head_dim", C.c_int32), ("n_axes", C.c_int32)]
@@ -184,6 +198,13 @@ def load_library(path: str | None = None):
                             C.c_int),
         "sd_attend_cross": ([vp, C.POINTER(States), i32, vp, i64, i64, i32, i32, C.c_float, vp, i64, i64, vp, vp],
                             C.c_int),
+        "sd_page_work": ([i32, i32, i32], i64),
+        "sd_page_fork": ([vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp], C.c_int),
+        "sd_page_compact": ([vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp], C.c_int),
+        "sd_page_copy": ([vp, i32, vp, vp, i32, vp], C.c_int),
+        "sd_attend_shared": ([vp, C.POINTER(Pages), vp, i32, vp, i32, vp, vp, i32, i32, vp, i64, i32, C.c_float, vp, i64,
+                              vp, vp], C.c_int),
+        "sd_score_rows": ([vp, i64, i32, i32, i32, C.c_float, vp, vp, vp, vp, i32, vp, vp, vp], C.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -452,6 +473,51 @@ def sd_attend_cross(ws, states: States, dtype: int, q_dev, q_batch: int, q_strid
     _check(load_library().sd_attend_cross(getattr(ws, "handle", ws), states, dtype, _ptr(q_dev), q_batch, q_stride, Lq,
                                           n_head, scale, _ptr(out_dev), out_batch, out_stride, _ptr(lse_dev), stream),
            None)
+
+
+def sd_page_work(R: int, N: int, n_pages: int) -> int:
+    """int32 words of the work area of sd_page_fork (N new rows) and sd_page_compact (N 0)."""
+    return load_library().sd_page_work(R, N, n_pages)
+
+
+def sd_page_fork(table_dev, table_stride: int, len_dev, R: int, parent_dev, N: int, free_dev, n_free: int,
+                 page_size: int, n_pages: int, table_out_dev, len_out_dev, copy_dev, ref_dev, free_out_dev, info_dev,
+                 work_dev, stream=None) -> None:
+    _check(load_library().sd_page_fork(_ptr(table_dev), table_stride, _ptr(len_dev), R, _ptr(parent_dev), N,
+                                       _ptr(free_dev), n_free, page_size, n_pages, _ptr(table_out_dev),
+                                       _ptr(len_out_dev), _ptr(copy_dev), _ptr(ref_dev), _ptr(free_out_dev),
+                                       _ptr(info_dev), _ptr(work_dev), stream), None)
+
+
+def sd_page_compact(table_dev, table_stride: int, len_dev, R: int, page_size: int, n_pages: int, table_out_dev,
+                    copy_dev, ref_dev, free_out_dev, info_dev, work_dev, stream=None) -> None:
+    _check(load_library().sd_page_compact(_ptr(table_dev), table_stride, _ptr(len_dev), R, page_size, n_pages,
+                                          _ptr(table_out_dev), _ptr(copy_dev), _ptr(ref_dev), _ptr(free_out_dev),
+                                          _ptr(info_dev), _ptr(work_dev), stream), None)
+
+
+def sd_page_copy(caches, copy_dev, count_dev, max_copies: int, stream=None) -> None:
+    """caches: a PageArray, or a sequence of Pages (one for each layer)."""
+    a = caches if isinstance(caches, PageArray) else PageArray.of(caches)
+    _check(load_library().sd_page_copy(C.addressof(a.array) if a.n else None, a.n, _ptr(copy_dev), _ptr(count_dev),
+                                       max_copies, stream), None)
+
+
+def sd_attend_shared(ws, cache: Pages, table_dev, table_stride: int, len_dev, R: int, group_dev, shared_dev,
+                     n_groups: int, dtype: int, q_dev, q_stride: int, n_head: int, scale: float, out_dev,
+                     out_stride: int, lse_dev=None, stream=None) -> None:
+    """ws: a handle of sd_attn_ws_create or an AttnWorkspace."""
+    _check(load_library().sd_attend_shared(getattr(ws, "handle", ws), cache, _ptr(table_dev), table_stride,
+                                           _ptr(len_dev), R, _ptr(group_dev), _ptr(shared_dev), n_groups, dtype,
+                                           _ptr(q_dev), q_stride, n_head, scale, _ptr(out_dev), out_stride,
+                                           _ptr(lse_dev), stream), None)
+
+
+def sd_score_rows(logits_dev, stride: int, dtype: int, rows: int, V: int, temperature: float, token_dev, logp_dev,
+                  rank_dev, entropy_dev, top_n: int = 0, top_id_dev=None, top_logp_dev=None, stream=None) -> None:
+    _check(load_library().sd_score_rows(_ptr(logits_dev), stride, dtype, rows, V, temperature, _ptr(token_dev),
+                                        _ptr(logp_dev), _ptr(rank_dev), _ptr(entropy_dev), top_n, _ptr(top_id_dev),
+                                        _ptr(top_logp_dev), stream), None)
 
 
 # ------------------------------------------------------------------ convenience wrapper

@@ -320,6 +320,89 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
                     int64_t q_stride, int32_t Lq, int32_t n_head, float scale, void* out_dev, int64_t out_batch,
                     int64_t out_stride, float* lse_dev, void* stream);
 
+/* ---- Rollouts: rows that continue one another's cache, and what picks among them.  Conventions as
+ * above: stream-ordered, nothing allocated or waited for, buffers of the current device
+ * (sd_attend_shared: of its workspace's device).  The buffers of a call must not overlap,
+ * but for what is said. */
+
+/* int32 words of work_dev (8-byte aligned, any contents) for sd_page_fork with R rows, N new rows and n_pages
+ * pages, and for sd_page_compact (N 0).  0 for negative counts or n_pages below 1. */
+int64_t sd_page_work(int32_t R, int32_t N, int32_t n_pages);
+
+/* Rows of the next step from rows of this one (rollouts of a prompt, beams, requests that end).  New row
+ * i < N continues old row p = parent_dev[i], any number of new rows the same one; a parent outside
+ * [0, R) gives an empty row.  Row p has len_dev[p] positions in the pages table_dev [R][table_stride]
+ * names.  Their full pages are shared.  The partly filled page stays with the lowest of the rows that
+ * continue p; each other one takes the next page of free_dev[n_free], in the order of the rows, and the
+ * positions have to be copied there.  Outputs:
+ *   table_out_dev [N][table_stride]  pages of the new rows, -1 behind their last
+ *   len_out_dev [N]        their positions
+ *   copy_dev [N][3]        source page, destination page and positions of each copy (sd_page_copy)
+ *   ref_dev [n_pages]      how many new rows name the page
+ *   free_out_dev [n_pages] the free pages from now on: the rest of free_dev, then the pages that
+ *                          old rows named and no new row does, in ascending order
+ *   info_dev [4]           copies; free pages; what went wrong (bits); longest new row
+ * What lies behind the copies and the free pages stays as it was.  Bits of info_dev[2]:
+ *   2 the free list is too short: the rows it does not serve end before their partly filled page
+ *   4 a row is longer than its table row (limited to it)
+ *   8 a negative length (read as 0)
+ *  16 a page id outside [0, n_pages) in use or taken: -1 in the new row, counted nowhere; a copy
+ *     from or to it names -1, and a row that took it ends before that page
+ * A partly filled page belongs to one old row, and no free page is in use.  R, N and n_free may be 0 (the
+ * pointers that belong to them may be NULL then).  page_size 1 to 65536, n_pages * page_size at most 2^31 - 1. */
+int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* len_dev, int32_t R,
+                 const int32_t* parent_dev, int32_t N, const int32_t* free_dev, int32_t n_free, int32_t page_size,
+                 int32_t n_pages, int32_t* table_out_dev, int32_t* len_out_dev, int32_t* copy_dev, int32_t* ref_dev,
+                 int32_t* free_out_dev, int32_t* info_dev, int32_t* work_dev, void* stream);
+
+/* The pages in use moved to the front of the pool: with L of them, the page in use with the k-th lowest id
+ * from L on moves to the k-th lowest id below L that is not in use.  A page is in use if one of
+ * the R rows names it.  Outputs:
+ *   table_out_dev [R][table_stride]  the rows with the new ids, -1 behind their last page
+ *   copy_dev [n_pages / 2][3]  the moves: source, destination, page_size (sd_page_copy); the
+ *                              rest stays as it was
+ *   ref_dev [n_pages]          how many rows name the page now
+ *   free_out_dev [n_pages]     L, L + 1, ..., n_pages - 1; the rest stays as it was
+ *   info_dev [4]               moves; n_pages - L; bits 4, 8 and 16 as in sd_page_fork; L */
+int sd_page_compact(const int32_t* table_dev, int32_t table_stride, const int32_t* len_dev, int32_t R,
+                    int32_t page_size, int32_t n_pages, int32_t* table_out_dev, int32_t* copy_dev, int32_t* ref_dev,
+                    int32_t* free_out_dev, int32_t* info_dev, int32_t* work_dev, void* stream);
+
+/* Copies pages within each of n_caches (up to 128; the layers') caches of one type, shape and strides: for each
+ * c < min(count_dev[0], max_copies), positions [0, copy_dev[c][2]) of page copy_dev[c][0] to page
+ * copy_dev[c][1], keys and values of all heads.  The positions are limited to [0, page_size]; a copy
+ * from or to a page id outside [0, n_pages) is skipped, one of a page to itself does nothing.
+ * No copy's destination is another copy's source or destination.  max_copies or n_caches 0 does nothing. */
+int sd_page_copy(const sd_pages* caches, int32_t n_caches, const int32_t* copy_dev, const int32_t* count_dev,
+                 int32_t max_copies, void* stream);
+
+/* sd_attend_pages for requests that share their first pages (rollouts of one prompt): the same results, with the
+ * common keys and values read once for a group instead of once a request.  Group x is
+ * requests group_dev[x] to group_dev[x + 1] - 1 (x < n_groups; ascending, between 0 and R; group_dev has
+ * n_groups + 1 numbers, all on the device), whose table rows name the same pages in their first
+ * shared_dev[x] entries; the page ids are taken from any of those rows.  A request in no group, or with shorter
+ * length than the group's pages, is served too.  n_groups 0: sd_attend_pages.  Everything else as in sd_attend_pages.
+ * (With SD_F32 queries an infinite key at a shared position may give NaN.) */
+int sd_attend_shared(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
+                     const int32_t* len_dev, int32_t R, const int32_t* group_dev, const int32_t* shared_dev,
+                     int32_t n_groups, int32_t dtype, const void* q_dev, int64_t q_stride, int32_t n_head, float scale,
+                     void* out_dev, int64_t out_stride, float* lse_dev, void* stream);
+
+/* Scores of rows of logits [rows][V] (rows `stride` elements apart, dtype SD_F32, SD_F16 or SD_BF16, any
+ * alignment of whole elements), p = softmax(z / temperature):
+ *   logp_dev[r]     log p of token token_dev[r]
+ *   rank_dev[r]     how many entries are ahead of it: with a larger logit, or the same and a lower index
+ *   entropy_dev[r]  -sum p log p (natural logarithms)
+ *   top_id_dev, top_logp_dev [rows][top_n]   the first top_n entries in that order, and their log p
+ * logp_dev, rank_dev and entropy_dev may be NULL; token_dev if the first two are.  A token outside [0, V)
+ * (padding) has logp 0 and rank -1.  A logit of -inf (masked) has p 0 and is no alternative: places without one
+ * hold -1 and -inf.  A row of -inf alone: logp -inf, entropy 0.  NaN or +inf in a row makes its
+ * logp, entropy and top_logp NaN; NaN is ahead of nothing and no alternative.  Sums are fp32.  1 <= V <= 262144,
+ * 0 <= top_n <= 32, temperature between 1e-30 and 1e30. */
+int sd_score_rows(const void* logits_dev, int64_t stride, int32_t dtype, int32_t rows, int32_t V, float temperature,
+                  const int32_t* token_dev, float* logp_dev, int32_t* rank_dev, float* entropy_dev, int32_t top_n,
+                  int32_t* top_id_dev, float* top_logp_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
