@@ -11,10 +11,17 @@ struct sd_attn_ws {
     float* part = nullptr;
     int* cnt = nullptr;              // the counters, and behind them the word of AttendArgs::dead
     int* err = nullptr;              // pinned: a kernel's expired wait, for the host
+    float *recs = nullptr, *common = nullptr;   // shared pages: partial results of parts, and of rows
+    int* skip = nullptr;             // and how many pages of a request are shared
+    long long share_bytes = 0;       // key and value bytes that sharing has to save (SD_SHARE_MIN_BYTES for the tests)
     long long test_stall = 0;        // test hook (SD_TEST_STALL_US): cycles for one wait of the first uncaptured call
 };
 
 namespace sd {
+
+constexpr int kSharedRecord = 128 + 4;                            // floats of a row's partial result: output, maximum, sum
+constexpr int kSharedRows = 65536;                                // query rows (request, head) that a workspace has records for
+constexpr int kSharedBlock = 256;                                 // and more for each block, for the item that it continues
 
 struct AttendArgs {
     const void *q, *k, *v;
@@ -30,6 +37,8 @@ struct AttendArgs {
     int *cnt, *err;
     int* dead;                       // set with err.  A launch that finds it set (a replayed graph: no host call looks at err)
                                      // leaves the counters alone, which are not zero then, and writes NaN
+    float *recs, *common;            // shared pages: partial results of parts, and of rows [request][head]
+    int32_t* skip;                   // pages of a request that are attended to for its group; NULL: none are
     long long stall;                 // test hook: block 0 waits as many cycles for a barrier that nothing arrives at
 };
 
@@ -42,6 +51,10 @@ constexpr int kMaxPositions = INT32_MAX - 1023;                   // of a row: t
 cudaError_t prepare_attend_split();                               // shared-memory limits on the current device
 cudaError_t prepare_attend_tc();
 cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t st, bool* taken);
+cudaError_t prepare_attend_shared();
+// *taken false: strides that a tensor map cannot hold, nothing launched
+cudaError_t launch_attend_shared(const AttendArgs& a, const int32_t* group, const int32_t* shared, int n_groups, int hd, int sms,
+                                 cudaStream_t st, int64_t worth, bool* taken);
 cudaError_t launch_attend_split(const AttendArgs& a, int hd, int sms, cudaStream_t st);
 
 // ---- device side
@@ -134,6 +147,25 @@ inline EncodeFn tensor_map_encoder() {
         return reinterpret_cast<EncodeFn>(p);
     }();
     return fn;
+}
+
+// K or V by strides, as [outer][head][position][hd]: boxes of `box` positions of up to 128 bytes of a row
+inline bool map_kv(CUtensorMap* map, int dtype, const void* base, int hd, int positions, int heads, int outer, int64_t pos_stride,
+            int64_t head_stride, int64_t outer_stride, int box) {
+    EncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int bytes = dtype == SD_E4M3 ? 1 : 2, row = hd * bytes;
+    const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)positions, (cuuint64_t)heads, (cuuint64_t)outer};
+    // the stride of a dimension of one element is not used: any legal value
+    const cuuint64_t strides[3] = {(cuuint64_t)(positions > 1 ? pos_stride * bytes : row),
+                                   (cuuint64_t)(heads > 1 ? head_stride * bytes : row),
+                                   (cuuint64_t)(outer > 1 ? outer_stride * bytes : row)};
+    const cuuint32_t boxes[4] = {(cuuint32_t)(row < 128 ? hd : 128 / bytes), (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = dtype == SD_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == SD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(map, type, 4, const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace sd

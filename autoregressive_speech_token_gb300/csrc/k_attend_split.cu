@@ -170,7 +170,7 @@ struct Shape {
 // What the warps on a unit need to know: m0 its first query row, tiles [i0, i0 + tiles) its part in this block
 struct Unit {
     int64_t m0;
-    int b, g, len, rows, i0, tiles, c_lo, c_hi, begins;
+    int b, g, len, rows, i0, tiles, c_lo, c_hi, begins, skip;
 };
 
 template <int HD, int KV>
@@ -218,7 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     pdl_wait();
 
     const bool few = a.B <= 32;                                           // a lane for each row, in every warp
-    auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
+    // positions of a row behind the ones that its group attends to together
+    auto length = [&](int b) {
+        const int n = min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len);
+        return a.skip ? (int)max(n - (int64_t)__ldcg(a.skip + b) * a.by_ps.d, (int64_t)0) : n;
+    };
     auto tiles = [&](int len) { return (len + kTile - 1) / kTile; };
 
     // ---- this block's share.  Where every unit can have a block of its own, units are cut into parts of `per` tiles
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     auto next_unit = [&](Unit& p) -> bool {
         if (t >= t_end) return false;
         p.b = b_at;
+        p.skip = a.skip ? __ldcg(a.skip + b_at) : 0;
         p.len = few ? __shfl_sync(0xffffffffu, len0, b_at) : b_at < kThreads ? s_len[b_at] : length(b_at);
         const int real_tiles = tiles(p.len), nt = padded(real_tiles);
         const int64_t u = quot(t - base, nt), u0 = base + u * nt;        // the unit's tiles [u0, u0 + nt)
@@ -364,6 +369,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 __syncwarp();
                 if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
                 if (!u.rows) break;
+                // what the shared pages give to the warp's rows: loaded here, needed behind the unit's tiles
+                float pre[2][kVec], pm[2] = {-INFINITY, -INFINITY}, pl[2] = {0.f, 0.f};
+                if (u.skip) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = mw + kMergers * e;
+                        if (r >= u.rows) continue;
+                        const float* p = a.common + ((int64_t)u.b * a.H + u.g * G + u.m0 + r) * kSharedRecord;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 128));
+                        pm[e] = ml.x;
+                        pl[e] = ml.y;
+#pragma unroll
+                        for (int x = 0; x < kVec; ++x) pre[e][x] = __ldcg(p + lane * kVec + x);
+                    }
+                }
                 if (!warp_wait(smem_u32(&s_done), nu & 1, bad)) break;
                 float val[2][kVec], mm[2], ll[2];
 #pragma unroll
@@ -444,6 +464,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                     }
                 }
                 if (!last) continue;
+                if (u.skip) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (pl[e] == 0.f) continue;
+                        const float mx = fmaxf(mm[e], pm[e]);
+                        const float f0 = mm[e] == -INFINITY ? 1.f : ex2(mm[e] - mx);
+                        const float f1 = (pm[e] == -INFINITY ? 1.f : ex2(pm[e] - mx)) * ex2(S::kShift);
+                        ll[e] = ll[e] * f0 + pl[e] * f1;
+#pragma unroll
+                        for (int x = 0; x < kVec; ++x) val[e][x] = val[e][x] * f0 + pre[e][x] * f1;
+                        mm[e] = mx;
+                    }
+                }
                 if (dead) ll[0] = ll[1] = NAN;
                 const float vs = a.v_scale ? __ldcg(a.v_scale + u.g) : 1.f;
 #pragma unroll
@@ -513,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             auto lookup = [&](int i, int k) -> int {
                 const int pos = (p.i0 + i) * kTile + (k * 32 + lane) * box;
                 if (i >= p.tiles || k * 32 + lane >= groups || pos >= p.len) return -1;
-                return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + a.by_ps.div((uint32_t)pos)) : p.b;
+                return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + p.skip + a.by_ps.div((uint32_t)pos)) : p.b;
             };
             const int outer = a.table ? a.n_pages : a.B;
             int x = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(x >> 1, 0);
@@ -839,25 +872,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
         if (lane == 0) mb_arrive(smem_u32(&s_done));
     }
     if (tid == 0 && *bad) report_expired(a);
-}
-
-// K or V by strides, as [outer][head][position][hd]: boxes of `box` positions of up to 128 bytes of a row
-bool map_kv(CUtensorMap* map, int dtype, const void* base, int hd, int positions, int heads, int outer, int64_t pos_stride,
-            int64_t head_stride, int64_t outer_stride, int box) {
-    EncodeFn enc = tensor_map_encoder();
-    if (!enc) return false;
-    const int bytes = dtype == SD_E4M3 ? 1 : 2, row = hd * bytes;
-    const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)positions, (cuuint64_t)heads, (cuuint64_t)outer};
-    // the stride of a dimension of one element is not used: any legal value
-    const cuuint64_t strides[3] = {(cuuint64_t)(positions > 1 ? pos_stride * bytes : row),
-                                   (cuuint64_t)(heads > 1 ? head_stride * bytes : row),
-                                   (cuuint64_t)(outer > 1 ? outer_stride * bytes : row)};
-    const cuuint32_t boxes[4] = {(cuuint32_t)(row < 128 ? hd : 128 / bytes), (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
-    const CUtensorMapDataType type = dtype == SD_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : dtype == SD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return enc(map, type, 4, const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, int KV>

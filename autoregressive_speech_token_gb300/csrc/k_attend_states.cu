@@ -1,5 +1,6 @@
 // sd_attend_pages and sd_attend_cross: arguments, workspace, and the choice of kernel.
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <new>
 
@@ -39,9 +40,29 @@ bool on_tiles(int Lq, int G, int hd, bool bf) {
     return units >= (hd == 64 ? 3 : 2) * pairs && (!bf || rows > 2 * kSplitRows);
 }
 
+constexpr long long kShareBytes = 48ll << 20;                     // key and value bytes that sharing has to save
+
 size_t counters(int sms) { return (size_t)sms * kSplitRows / 2; }
 
-int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream) {
+// Groups of requests with common pages; n 0: none
+struct Groups {
+    const int32_t *group, *shared;
+    int n;
+};
+
+// The requests of a group are served together where that saves enough.  It costs a launch of its own, and joining the
+// parts; whether the lengths are worth it is known on the device only, but not where all of the table is not.
+// Types: the products are 16-bit, e4m3 pages are not read by this kernel.  Scales so far from 1 that the rows' own could
+// leave fp32 are left to the other one, as are tables with more query rows than the workspace has records for.
+bool share(const sd_attn_ws* ws, const AttendArgs& a, int hd, const Groups& groups) {
+    if (!groups.n || a.B < 2 || a.kv_dtype == SD_E4M3) return false;
+    const float s = fabsf(a.scale);
+    if (!(s >= 0x1p-60f && s <= 0x1p60f)) return false;
+    if ((int64_t)a.B * a.H > kSharedRows) return false;
+    return 4.0 * hd * a.Hkv * (a.B - 1) * (double)a.max_len >= (double)ws->share_bytes;
+}
+
+int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream, const Groups& groups = {}) {
     DeviceScope scope(ws->device);
     if (scope.err != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(scope.err));
     if (*static_cast<volatile int*>(ws->err))
@@ -62,6 +83,15 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream)
     bool taken = false;
     if (!a.table && a.dtype == a.kv_dtype && a.scale > 0.f && a.max_len > 0 && on_tiles(a.Lq, a.H / a.Hkv, hd, a.dtype == SD_BF16))
         e = launch_attend_tc(a, hd, ws->sms, st, &taken);
+    if (share(ws, a, hd, groups)) {
+        a.recs = ws->recs;
+        a.common = ws->common;
+        a.skip = ws->skip;
+        bool shared = false;
+        e = launch_attend_shared(a, groups.group, groups.shared, groups.n, hd, ws->sms, st, ws->share_bytes / (4 * hd), &shared);
+        if (!shared) a.skip = nullptr;
+        if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    }
     if (!taken) e = launch_attend_split(a, hd, ws->sms, st);
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return SD_OK;
@@ -112,6 +142,9 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     cudaError_t e = cudaDeviceGetAttribute(&ws->sms, cudaDevAttrMultiProcessorCount, device);
     const size_t blocks = (size_t)ws->sms;
     if (e == cudaSuccess) e = cudaMalloc(&ws->part, blocks * kTcRecord * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->recs, (kSharedRows + blocks * kSharedBlock) * kSharedRecord * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->common, (size_t)kSharedRows * kSharedRecord * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->skip, kSharedRows * sizeof(int));
     const size_t words = counters(ws->sms) + 1;
     if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, words * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
@@ -119,6 +152,8 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     if (e == cudaSuccess) e = cudaHostAlloc(&ws->err, sizeof(int), cudaHostAllocDefault);
     if (e == cudaSuccess) *ws->err = 0;
+    ws->share_bytes = kShareBytes;
+    if (const char* sb = getenv("SD_SHARE_MIN_BYTES")) ws->share_bytes = atoll(sb);
     if (const char* ts = getenv("SD_TEST_STALL_US")) {
         int khz = 0;
         cudaDeviceGetAttribute(&khz, cudaDevAttrClockRate, device);
@@ -126,6 +161,7 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     }
     if (e == cudaSuccess) e = prepare_attend_split();
     if (e == cudaSuccess) e = prepare_attend_tc();
+    if (e == cudaSuccess) e = prepare_attend_shared();
     if (e != cudaSuccess) {
         sd_attn_ws_destroy(ws);
         return op_fail(e == cudaErrorMemoryAllocation ? SD_ERR_OOM : SD_ERR_CUDA, "sd_attn_ws_create: %s",
@@ -139,6 +175,9 @@ void sd_attn_ws_destroy(sd_attn_ws* ws) {
     if (!ws) return;
     sd::DeviceScope scope(ws->device);
     cudaFree(ws->part);
+    cudaFree(ws->recs);
+    cudaFree(ws->common);
+    cudaFree(ws->skip);
     cudaFree(ws->cnt);
     cudaFreeHost(ws->err);
     delete ws;
@@ -173,7 +212,7 @@ int sd_attend_shared(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table
     if (n_groups < 0 || n_groups > R) return op_fail(SD_ERR_INVALID_ARG, "%s: n_groups %d of %d requests", who, n_groups, R);
     if (n_groups > 0 && (!group_dev || !shared_dev))
         return op_fail(SD_ERR_INVALID_ARG, "%s: group_dev or shared_dev is NULL", who);
-    return launch(who, ws, a, hd, stream);
+    return launch(who, ws, a, hd, stream, {group_dev, shared_dev, n_groups});
 }
 
 int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, const void* q_dev, int64_t q_batch,

@@ -23,9 +23,13 @@ def sd():
     return pkg
 
 
-@pytest.fixture(scope="module")
-def ws(sd):
-    w = sd.AttnWorkspace()
+@pytest.fixture(scope="module", params=["always", "where_it_saves"])
+def ws(sd, request):
+    """Sharing whatever it saves, and by the library's own rule."""
+    with pytest.MonkeyPatch.context() as m:
+        if request.param == "always":
+            m.setenv("SD_SHARE_MIN_BYTES", "0")
+        w = sd.AttnWorkspace()
     yield w
     w.close()
 
@@ -395,9 +399,11 @@ def check_rows(q, rows, out, lse, Hkv, scale, dt, cache, sc=(None, None)):
             h = slice(kv * G, (kv + 1) * G)
             ref, mag, size, ls = attend_ref(q[r, h].double(), kk, vv, scale)
             tol, tol_l = bounds(ref, mag, size, k.shape[0], dt, cache, hd)
-            assert torch.all((out[r, h].double() - ref).abs() <= tol), (r, kv, (out[r, h].double() - ref).abs().max())
+            good = bool(torch.all((out[r, h].double() - ref).abs() <= tol))
+            assert good, (r, kv, (out[r, h].double() - ref).abs().max().item())
             d = lse[r, h].double()
-            assert torch.all((d == ls) | ((d - ls).abs() <= tol_l + ls.abs() * 2.0 ** -22)), (r, kv)
+            good = bool(torch.all((d == ls) | ((d - ls).abs() <= tol_l + ls.abs() * 2.0 ** -22)))
+            assert good, (r, kv, d.tolist(), ls.tolist())
 
 
 SHARED = [
@@ -508,7 +514,8 @@ def test_shared_groups_out_of_range_are_limited(sd, ws):
         check_rows(q, rows, out, lse, 2, 0.125, "f16", "f16")
 
 
-def test_shared_with_strides_streams_and_graphs(sd):
+def test_shared_with_strides_streams_and_graphs(sd, monkeypatch):
+    monkeypatch.setenv("SD_SHARE_MIN_BYTES", "0")
     g = gen(10)
     spec = [(64, [1100 + 3 * i for i in range(16)]), (40, [900, 700])]
     kc, vc, table, rows, lens, starts, shared = build_groups(g, np.random.default_rng(1), spec, [50], 4, 128, 16, "bf16", "hnd")
