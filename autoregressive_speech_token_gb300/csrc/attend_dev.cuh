@@ -6,19 +6,30 @@
 
 // Partial results: a record a block of the tensor-core kernel, or two of the split kernel with its arrival counters.
 // The counters are zero between calls (the last arriver of a unit clears its own).
+namespace sd {
+struct SharedRow;
+}
 struct sd_attn_ws {
     int device = 0, sms = 0;
     float* part = nullptr;
     int* cnt = nullptr;              // the counters, and behind them the word of AttendArgs::dead
     int* err = nullptr;              // pinned: a kernel's expired wait, for the host
-    float *recs = nullptr, *common = nullptr;   // shared pages: partial results of parts, and of rows
-    int* skip = nullptr;             // and how many pages of a request are shared
+    float* recs = nullptr;           // shared pages: partial results
+    sd::SharedRow* desc = nullptr;   // and of which each request has its own, behind them the word of AttendArgs::shared
     long long share_bytes = 0;       // key and value bytes that sharing has to save (SD_SHARE_MIN_BYTES for the tests)
     long long test_stall = 0;        // test hook (SD_TEST_STALL_US): cycles for one wait of the first uncaptured call
 };
 
 namespace sd {
 
+// Of a request whose first `skip` pages are attended to for its whole group of `size` requests from r0 on: the rows
+// (request - r0, head) of a kv head are in items of `rows`, each of `tiles` tiles behind kShareLead empty ones; the group's
+// first tile is `base` of all, and a block took `per` of them.
+struct SharedRow {
+    int32_t skip, r0, size, tiles, rows, unused;
+    int64_t base, per;
+};
+constexpr int kShareLead = 3;                                     // what beginning and ending an item costs, in tiles
 constexpr int kSharedRecord = 128 + 4;                            // floats of a row's partial result: output, maximum, sum
 constexpr int kSharedRows = 65536;                                // query rows (request, head) that a workspace has records for
 constexpr int kSharedBlock = 256;                                 // and more for each block, for the item that it continues
@@ -37,8 +48,9 @@ struct AttendArgs {
     int *cnt, *err;
     int* dead;                       // set with err.  A launch that finds it set (a replayed graph: no host call looks at err)
                                      // leaves the counters alone, which are not zero then, and writes NaN
-    float *recs, *common;            // shared pages: partial results of parts, and of rows [request][head]
-    int32_t* skip;                   // pages of a request that are attended to for its group; NULL: none are
+    float* recs;                     // shared pages
+    SharedRow* desc;
+    int32_t* shared;                 // 1: the kernels for shared pages serve this call, 0: the split kernel does; NULL: it does
     long long stall;                 // test hook: block 0 waits as many cycles for a barrier that nothing arrives at
 };
 
@@ -52,6 +64,8 @@ cudaError_t prepare_attend_split();                               // shared-memo
 cudaError_t prepare_attend_tc();
 cudaError_t launch_attend_tc(const AttendArgs& a, int hd, int sms, cudaStream_t st, bool* taken);
 cudaError_t prepare_attend_shared();
+cudaError_t prepare_attend_own();
+cudaError_t launch_attend_own(const AttendArgs& a, int hd, cudaStream_t st);
 // *taken false: strides that a tensor map cannot hold, nothing launched
 cudaError_t launch_attend_shared(const AttendArgs& a, const int32_t* group, const int32_t* shared, int n_groups, int hd, int sms,
                                  cudaStream_t st, int64_t worth, bool* taken);
@@ -65,6 +79,11 @@ constexpr long long kWaitClocks = 4000000000ll;                   // about two s
 // a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division costs a few hundred cycles)
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// Where the records of a part of an item lie, as 4-column pieces [piece][row] and behind them (maximum, sum) of each row: the
+// part that begins the item has the place of its rows among all (request, head) rows, the others their block's.
+__device__ __forceinline__ float* shared_records(const AttendArgs& a, bool begins, int64_t first_row, int block) {
+    return a.recs + (begins ? first_row : (int64_t)a.B * a.H + (int64_t)block * kSharedBlock) * kSharedRecord;
 }
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mb_init(uint32_t mb, uint32_t n) {

@@ -4,8 +4,7 @@
 // An item is (group, kv head, up to 256 query rows), a row being (request, head of the kv head's group), against all
 // of the group's common positions in tiles of 128.  The tiles of all items, laid end to end, are dealt
 // evenly to one block per SM; a block writes, for each of its parts of an item, every row's partial
-// result (unnormalised output, maximum, sum).  A second kernel joins the parts of each row, and the split kernel, which
-// follows with the requests' own positions, adds its own.
+// result (unnormalised output, maximum, sum).  The next kernel (k_attend_own.cu) joins them with the requests' own positions.
 //
 //   S_i = Q_i K_j^T     P_i = exp2(S_i scale log2(e) - m_i), over S_i's columns     O_i += P_i V_j
 //
@@ -36,7 +35,7 @@ struct alignas(128) SharedArgs {
     CUtensorMap k, v;
     AttendArgs a;
     const int32_t *group, *shared;
-    int32_t n_groups, box, blocks;                    // blocks of the first kernel
+    int32_t n_groups, box;
     int64_t worth;                                    // key and value rows that sharing has to save
 };
 
@@ -70,10 +69,14 @@ __device__ __forceinline__ Group group_of(const SharedArgs& t, int x, int rows) 
 struct Groups32 {
     Group mine;
     bool few;
-    int64_t first, T;                                             // tiles before the lane's group; of all (0: sharing saves too little)
-    int items;                                                    // items before the lane's group
+    int64_t first, T;                                             // tiles before the lane's group; of all (0: sharing does not pay)
 };
+// A group's tiles, with the empty ones before each item
+__device__ __forceinline__ int64_t span(const Group& p) { return p.tiles ? (int64_t)(p.tiles + kShareLead) * p.items : 0; }
 // By all threads of a block of `threads`; s_sum has two words for each warp.
+//
+// Sharing pays if it saves `worth` rows of keys and values, and if no request has so many positions of its own that the
+// one block that takes them (some 40 GB/s) ends behind the time that all others need for what is saved (some 5 TB/s).
 __device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int threads, int64_t* s_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Groups32 g = {};
@@ -82,28 +85,38 @@ __device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int
     auto saves = [&](const Group& p) { return p.tiles ? (int64_t)(p.size - 1) * p.pages * t.a.by_ps.d * t.a.Hkv : 0; };
     if (g.few) {
         if (lane < t.n_groups) g.mine = group_of(t, lane, rows);
-        tiles = (int64_t)g.mine.tiles * g.mine.items;
+        tiles = span(g.mine);
         saved = saves(g.mine);
         int64_t at = tiles;
-        int items = g.mine.tiles ? g.mine.items : 0;
-        const int own = items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, at, o);
-            const int z = __shfl_up_sync(0xffffffffu, items, o);
-            if (lane >= o) {
-                at += y;
-                items += z;
-            }
+            if (lane >= o) at += y;
             saved += __shfl_xor_sync(0xffffffffu, saved, o);
         }
         g.first = at - tiles;
-        g.items = items - own;
         g.T = __shfl_sync(0xffffffffu, at, 31);
+        // the most positions that a request has of its own: a thread for each request
+        int most = 0;
+        for (int b = threadIdx.x; b - lane < t.a.B; b += threads) {
+            const int len = b < t.a.B ? min(max(__ldcg(t.a.len + b), 0), t.a.max_len) : 0;
+            int64_t skip = 0;
+            for (int x = 0; x < t.n_groups; ++x) {
+                const int r0 = __shfl_sync(0xffffffffu, g.mine.r0, x), size = __shfl_sync(0xffffffffu, g.mine.size, x);
+                const int pages = __shfl_sync(0xffffffffu, g.mine.tiles ? g.mine.pages : 0, x);
+                if (b >= r0 && b < r0 + size) skip = (int64_t)pages * t.a.by_ps.d;
+            }
+            most = max(most, (int)max(len - skip, (int64_t)0));
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) s_sum[warp] = most;
+        __syncthreads();
+        for (int w = 0; w < threads / 32; ++w) most = max(most, (int)s_sum[w]);
+        if (t.worth > 0 && saved < 128 * (int64_t)most) g.T = 0;
     } else {
         for (int x = threadIdx.x; x < t.n_groups; x += threads) {
             const Group p = group_of(t, x, rows);
-            tiles += (int64_t)p.tiles * p.items;
+            tiles += span(p);
             saved += saves(p);
         }
 #pragma unroll
@@ -137,17 +150,20 @@ __device__ __forceinline__ Group group_at(const SharedArgs& t, const Groups32& g
 }
 __device__ __forceinline__ int64_t tiles_of_block(int64_t T, int blocks) { return max(quot(T + blocks - 1, blocks), (int64_t)1); }
 
-// Where a part's records lie, as 4-column pieces [piece][row] and behind them (maximum, sum) of each row: the part that
-// begins the item has the place of its rows among all (request, head) rows, the others their block's.
-__device__ __forceinline__ float* records(const AttendArgs& a, bool begins, int64_t first_row, int block) {
-    return a.recs + (begins ? first_row : (int64_t)a.B * a.H + (int64_t)block * kSharedBlock) * kSharedRecord;
-}
-
 // A piece of work of a block: tiles [i0, i0 + tiles) of an item; tiles 0: no more
 struct Item {
     int r0, g, i0, tiles, pages, m0, rows, size;
 };
 constexpr int kItems = 2;                                         // prepared ahead
+
+// O += P V: P of 32 positions lies in the first 16 columns of their scores (its low part in the other 16)
+template <int K, int kEnd>
+__device__ __forceinline__ void chunk_steps(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (K < kEnd) {
+        mma_ts<(K / 2) * 32 + (K % 2) * 8, K * (2048 >> 4)>(d, a, b, idesc, acc);
+        chunk_steps<K + 1, kEnd>(d, a, b, idesc, 1);
+    }
+}
 
 template <int HD, bool BF, bool LOW>
 __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_constant__ SharedArgs t) {
@@ -180,16 +196,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     const Groups32 groups = groups_of(t, kRows, kThreads, reinterpret_cast<int64_t*>(s_row));
     const int64_t T = groups.T, per = tiles_of_block(T, gridDim.x);
     const int64_t t_begin = blockIdx.x * per, t_end = min(T, t_begin + per);
-    // what the split kernel needs to know of each request
+    // which kernel follows, and what it needs to know of each request: a warp for a request
+    if (blockIdx.x == 0 && tid == 0) *a.shared = T > 0;
+    if (!T) return;
     for (int b = blockIdx.x + gridDim.x * warp; b < a.B; b += gridDim.x * (kThreads / 32)) {
-        int skip = 0;
-        if (T)
-            for (int x0 = 0; x0 < t.n_groups && !skip; x0 += 32) {
-                Group p = groups.mine;
-                if (!groups.few) p = x0 + lane < t.n_groups ? group_of(t, x0 + lane, kRows) : Group{};
-                skip = __reduce_max_sync(0xffffffffu, p.tiles && b >= p.r0 && b < p.r0 + p.size ? p.pages : 0);
+        SharedRow d = {};
+        int64_t base = 0;
+        for (int x0 = 0; x0 < t.n_groups; x0 += 32) {
+            Group p = groups.mine;
+            int64_t first = groups.first;
+            if (!groups.few) {
+                p = x0 + lane < t.n_groups ? group_of(t, x0 + lane, kRows) : Group{};
+                int64_t sum = span(p);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                first = base + sum - span(p);
+                base += __shfl_sync(0xffffffffu, sum, 31);
             }
-        if (lane == 0) a.skip[b] = skip;
+            const uint32_t here = __ballot_sync(0xffffffffu, p.tiles && b >= p.r0 && b < p.r0 + p.size);
+            if (!here) continue;
+            const int x = __ffs(here) - 1;
+            d.skip = __shfl_sync(0xffffffffu, p.pages, x);
+            d.r0 = __shfl_sync(0xffffffffu, p.r0, x);
+            d.size = __shfl_sync(0xffffffffu, p.size, x);
+            d.tiles = __shfl_sync(0xffffffffu, p.tiles, x);
+            d.base = __shfl_sync(0xffffffffu, first, x);
+            break;
+        }
+        d.rows = kRows;
+        d.per = per;
+        if (lane == 0) a.desc[b] = d;
     }
     if (t_begin >= T) return;
 
@@ -321,14 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             int x = 0;
             int64_t at = t_begin, base = 0;
             if (groups.few) {
-                const int64_t n = (int64_t)groups.mine.tiles * groups.mine.items;
+                const int64_t n = span(groups.mine);
                 x = __ffs(__ballot_sync(0xffffffffu, n && groups.first <= at && at < groups.first + n)) - 1;
                 base = __shfl_sync(0xffffffffu, groups.first, x & 31);
             } else {
                 // 32 groups at a time, up to the one that holds the first tile
                 for (int x0 = 0; x0 < t.n_groups; x0 += 32) {
                     const Group p = x0 + lane < t.n_groups ? group_of(t, x0 + lane, kRows) : Group{};
-                    const int64_t n = (int64_t)p.tiles * p.items;
+                    const int64_t n = span(p);
                     int64_t sum = n;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -347,24 +386,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             Group p = group_at(t, groups, x, kRows);
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
-                while (at < t_end && at >= base + (int64_t)p.tiles * p.items && x + 1 < t.n_groups) {
-                    base += (int64_t)p.tiles * p.items;
-                    p = group_at(t, groups, ++x, kRows);
-                }
                 it.tiles = 0;
-                if (at < t_end && p.tiles) {
-                    const int pairs = p.items / a.Hkv;
-                    const int64_t u = quot(at - base, p.tiles);
+                while (at < t_end && it.tiles <= 0) {
+                    if (at >= base + span(p)) {
+                        if (x + 1 >= t.n_groups) break;
+                        base += span(p);
+                        p = group_at(t, groups, ++x, kRows);
+                        continue;
+                    }
+                    const int pairs = p.items / a.Hkv, width = p.tiles + kShareLead;
+                    const int64_t u = quot(at - base, width), u0 = base + u * width, end = min(u0 + width, t_end);
                     it.r0 = p.r0;
                     it.size = p.size;
                     it.pages = p.pages;
                     it.g = (int)u / pairs;
                     it.m0 = ((int)u - it.g * pairs) * kRows;
                     it.rows = min(kRows, p.size * G - it.m0);
-                    it.i0 = (int)(at - base - u * p.tiles);
-                    it.tiles = (int)min((int64_t)p.tiles - it.i0, t_end - at);
-                    at += it.tiles;
+                    it.i0 = (int)max(at - u0 - kShareLead, (int64_t)0);
+                    it.tiles = (int)(end - u0) - kShareLead - it.i0;      // none: empty ones alone in this block
+                    at = end;
                 }
+                it.tiles = max(it.tiles, 0);
                 const uint32_t slot = n % kItems;
                 if (n >= kItems) ok = warp_wait(smem_u32(&s_iempty[slot]), (n / kItems - 1) & 1, bad);
                 if (!ok) break;
@@ -394,12 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     // the products of P's first half begin while its second half is formed
                     if (!mb_wait(smem_u32(&s_pfull[i][0]), np >> i & 1, bad)) return false;
                     tm_after();
-                    result_steps<0, kN / 32>(o, pr, vd, kIdescO, !first);
-                    if constexpr (LOW) result_steps<0, kN / 32>(o, pr + 64, vd, kIdescO, 1);
+                    chunk_steps<0, kN / 32>(o, pr, vd, kIdescO, !first);
+                    if constexpr (LOW) chunk_steps<0, kN / 32>(o, pr + 16, vd, kIdescO, 1);
                     if (!mb_wait(smem_u32(&s_pfull[i][1]), np >> i & 1, bad)) return false;
                     tm_after();
-                    result_steps<kN / 32, kN / 16>(o, pr, vd, kIdescO, 1);
-                    if constexpr (LOW) result_steps<kN / 32, kN / 16>(o, pr + 64, vd, kIdescO, 1);
+                    chunk_steps<kN / 32, kN / 16>(o, pr, vd, kIdescO, 1);
+                    if constexpr (LOW) chunk_steps<kN / 32, kN / 16>(o, pr + 16, vd, kIdescO, 1);
                     np ^= 1u << i;
                     return true;
                 };
@@ -595,36 +637,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                 if (!ok) break;
                 ++ns;
                 tm_after();
-                float s[kN];
-#pragma unroll
-                for (int c = 0; c < kN; c += 32) tm_ld32(ts + c, s + c);
+                // Chunks of 32 positions in loops that are not unrolled: the scores are read twice instead of held in 128
+                // registers, and the code is a quarter as long (its first pass, out of an empty instruction cache,
+                // took 9000 cycles unrolled)
                 const uint32_t* mask = s_mask[(n + j) % kMasks];
                 const int rest = limit - j * kN;
-                uint32_t live[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    live[c] = *const_cast<const volatile uint32_t*>(mask + c);
+                auto live_of = [&](int c) {                        // chunk c's positions that the row has
+                    uint32_t x = *const_cast<const volatile uint32_t*>(mask + c);
                     const int left = rest - 32 * c;
-                    if (left < 32) live[c] &= left <= 0 ? 0u : 0xffffffffu >> (32 - left);
-                }
-                tm_wait_ld();
+                    if (left < 32) x &= left <= 0 ? 0u : 0xffffffffu >> (32 - left);
+                    return x;
+                };
+                auto load = [&](int c, float* s) {
+                    tm_ld32(ts + 32 * c, s);
+                    const uint32_t live = live_of(c);
+                    tm_wait_ld();
+                    after_wait(s);
+                    after_wait(s + 16);
+                    if (__any_sync(0xffffffffu, live != 0xffffffffu)) {
 #pragma unroll
-                for (int c = 0; c < kN; c += 16) after_wait(s + c);
-                if (__any_sync(0xffffffffu, (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu)) {
+                        for (int e = 0; e < 32; ++e) s[e] = (live >> e) & 1 ? s[e] : -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kN / 32; ++c) {
+                    float s[32];
+                    load(c, s);
+                    float m0 = s[0], m1 = s[1];
 #pragma unroll
-                    for (int c = 0; c < kN; ++c) s[c] = (live[c >> 5] >> (c & 31)) & 1 ? s[c] : -INFINITY;
+                    for (int e = 2; e + 4 <= 32; e += 4) {
+                        m0 = max3(m0, s[e], s[e + 1]);
+                        m1 = max3(m1, s[e + 2], s[e + 3]);
+                    }
+                    mx = fmaxf(mx, fmaxf(max3(m0, s[30], s[31]), m1));
                 }
-                float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-                for (int c = 4; c + 8 <= kN; c += 8) {
-                    m0 = max3(m0, s[c], s[c + 1]);
-                    m1 = max3(m1, s[c + 2], s[c + 3]);
-                    m2 = max3(m2, s[c + 4], s[c + 5]);
-                    m3 = max3(m3, s[c + 6], s[c + 7]);
-                }
-                m0 = max3(m0, s[kN - 4], s[kN - 3]);
-                m1 = max3(m1, s[kN - 2], s[kN - 1]);
-                const float mx = fmaxf(max3(m0, m1, m2), m3);
                 if (__any_sync(0xffffffffu, mx > mark)) {
                     const bool grow = mx > (sub != 0.f ? top : mark);
                     if (__any_sync(0xffffffffu, grow)) {
@@ -632,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                         if (grow) top = mx;
                         l *= f;
                         if (j >= step) {                           // O_i holds something
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < HD; c += 16) {
                                 float o[16];
                                 tm_ld16(to + i * HD + c, o);
@@ -650,19 +697,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     sub = far ? top : 0.f;
                     ref = (far || m == -INFINITY ? 0.f : m) - kShift;
                     mark = far ? -INFINITY : top + slack;
-                    if (__any_sync(0xffffffffu, far)) {
-#pragma unroll
-                        for (int c = 0; c < kN; ++c) s[c] -= sub;
-                    }
                 }
+                const bool any_far = __any_sync(0xffffffffu, sub != 0.f);
                 float2 l0 = make_float2(0.f, 0.f), l1 = l0;
                 const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(-ref, -ref);
+#pragma unroll 1
+                for (int c = 0; c < kN / 32; ++c) {
+                    float s[32];
+                    load(c, s);
+                    if (any_far) {
 #pragma unroll
-                for (int c = 0; c < kN; c += 32) {
+                        for (int e = 0; e < 32; ++e) s[e] -= sub;
+                    }
                     uint32_t pr[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float2 x = fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, ref2);
+                        float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sl2, ref2);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         if (e & 1) l1 = add2(l1, x); else l0 = add2(l0, x);
@@ -674,13 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                             lo[e] = pack2<BF>(x.x - f.x, x.y - f.y);
                         }
                     }
-                    tm_st16(ts + c / 2, pr);
-                    if constexpr (LOW) tm_st16(ts + 64 + c / 2, lo);
-                    if (c == kN / 2 - 32 || c == kN - 32) {
+                    tm_st16(ts + 32 * c, pr);
+                    if constexpr (LOW) tm_st16(ts + 32 * c + 16, lo);
+                    if (c & 1) {
                         tm_wait_st();
                         tm_before();
                         __syncwarp();
-                        if (lane == 0) mb_arrive(smem_u32(&s_pfull[i][c == kN - 32]));
+                        if (lane == 0) mb_arrive(smem_u32(&s_pfull[i][c >> 1]));
                     }
                 }
                 l += (l0.x + l0.y) + (l1.x + l1.y);
@@ -731,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             } else {
                 l *= f0;
             }
-            float* rec = records(a, it.i0 == 0, (int64_t)it.r0 * a.H + it.g * (it.size * G) + it.m0, blockIdx.x);
+            float* rec = shared_records(a, it.i0 == 0, (int64_t)it.r0 * a.H + it.g * (it.size * G) + it.m0, blockIdx.x);
 #pragma unroll
             for (int c = 0; c < HD; c += 16) {
                 float o[16];
@@ -769,116 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     if (tid == 0 && s_bad) report_expired(a);
 }
 
-// Joins the parts of every row, in the order of the blocks: a block takes 128 rows of an item and 16 of their columns.
-constexpr int kJoinThreads = 256;
-template <int HD>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_shared_join(const __grid_constant__ SharedArgs t, int rows) {
-    __shared__ int64_t s_sum[2 * kJoinThreads / 32];
-    pdl_trigger();
-    pdl_wait();
-    const AttendArgs& a = t.a;
-    const int G = a.H / a.Hkv, lane = threadIdx.x & 31;
-    const Groups32 groups = groups_of(t, rows, kJoinThreads, s_sum);
-    if (!groups.T) return;
-    const int64_t per = tiles_of_block(groups.T, t.blocks);
-    constexpr int kCols = HD / 16;
-    const int tiles_of_item = rows / kM, pieces_of_item = tiles_of_item * kCols;
-    // this block's pieces are of rising items: the groups are walked once
-    int x0 = 0, before = 0;                                       // groups and items before the 32 that the warp's lanes hold
-    int64_t base32 = 0;
-    Group p32 = groups.mine;
-    int first_item = groups.items;                                // items and tiles before the lane's group
-    int64_t first_tile = groups.first;
-    auto scan = [&]() {
-        p32 = x0 + lane < t.n_groups ? group_of(t, x0 + lane, rows) : Group{};
-        int n = p32.tiles ? p32.items : 0;
-        int64_t m = (int64_t)p32.tiles * p32.items;
-        const int own = n;
-        const int64_t own_m = m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, n, o);
-            const int64_t z = __shfl_up_sync(0xffffffffu, m, o);
-            if (lane >= o) {
-                n += y;
-                m += z;
-            }
-        }
-        first_item = before + n - own;
-        first_tile = base32 + m - own_m;
-    };
-    if (!groups.few) scan();
-    for (int64_t piece = blockIdx.x;; piece += gridDim.x) {
-        const int64_t w = piece / pieces_of_item;
-        uint32_t here;
-        for (;;) {
-            here = __ballot_sync(0xffffffffu, p32.tiles && first_item <= w && w < (int64_t)first_item + p32.items);
-            if (here || x0 + 32 >= t.n_groups) break;
-            before = __shfl_sync(0xffffffffu, first_item + (p32.tiles ? p32.items : 0), 31);
-            base32 = __shfl_sync(0xffffffffu, first_tile + (int64_t)p32.tiles * p32.items, 31);
-            x0 += 32;
-            scan();
-        }
-        if (!here) return;
-        const int x = __ffs(here) - 1;
-        const int r0 = __shfl_sync(0xffffffffu, p32.r0, x), size = __shfl_sync(0xffffffffu, p32.size, x);
-        const int tiles = __shfl_sync(0xffffffffu, p32.tiles, x), items = __shfl_sync(0xffffffffu, p32.items, x);
-        const int u = (int)(w - __shfl_sync(0xffffffffu, first_item, x)), pairs = items / a.Hkv, g = u / pairs, m0 = (u - g * pairs) * rows;
-        const int n = min(rows, size * G - m0);
-        const int64_t t0 = __shfl_sync(0xffffffffu, first_tile, x) + (int64_t)u * tiles;
-        const int c_lo = (int)quot(t0, per), c_hi = (int)quot(t0 + tiles - 1, per);
-        const int rest = (int)(piece - w * pieces_of_item), i = rest / kCols;
-        const int local = i * kM + threadIdx.x % kM, c8 = (rest - i * kCols) * 2 + threadIdx.x / kM;
-        if (local >= n) continue;
-        auto record = [&](int c) { return records(a, c == c_lo, (int64_t)r0 * a.H + g * (size * G) + m0, c); };
-        float m = -INFINITY, l = 0.f, o[8] = {};
-        constexpr int kBatch = 6;                                 // records whose loads are in flight together
-        for (int c = c_lo; c <= c_hi; c += kBatch) {
-            float2 ml[kBatch];
-            float4 v[kBatch][2];
-            float mx = m;
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const float* p = record(min(c + y, c_hi));
-                ml[y] = __ldcg(reinterpret_cast<const float2*>(p + (int64_t)HD * n) + local);
-                v[y][0] = __ldcg(reinterpret_cast<const float4*>(p) + 2 * c8 * n + local);
-                v[y][1] = __ldcg(reinterpret_cast<const float4*>(p) + (2 * c8 + 1) * n + local);
-            }
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                if (c + y > c_hi) ml[y] = make_float2(-INFINITY, 0.f);
-                mx = fmaxf(mx, ml[y].x);
-            }
-            const float keep = m == -INFINITY ? 1.f : ex2(m - mx);
-            m = mx;
-            l *= keep;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] *= keep;
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                if (ml[y].y == 0.f) continue;                     // nothing in this part (NaN is something)
-                const float f = ml[y].x == -INFINITY ? 1.f : ex2(ml[y].x - m);
-                l = fmaf(f, ml[y].y, l);
-                o[0] = fmaf(v[y][0].x, f, o[0]); o[1] = fmaf(v[y][0].y, f, o[1]); o[2] = fmaf(v[y][0].z, f, o[2]); o[3] = fmaf(v[y][0].w, f, o[3]);
-                o[4] = fmaf(v[y][1].x, f, o[4]); o[5] = fmaf(v[y][1].y, f, o[5]); o[6] = fmaf(v[y][1].z, f, o[6]); o[7] = fmaf(v[y][1].w, f, o[7]);
-            }
-        }
-        const int row = m0 + local, qi = row / G;
-        float* out = a.common + ((int64_t)(r0 + qi) * a.H + g * G + (row - qi * G)) * kSharedRecord;
-        __stcg(reinterpret_cast<float4*>(out) + 2 * c8, make_float4(o[0], o[1], o[2], o[3]));
-        __stcg(reinterpret_cast<float4*>(out) + 2 * c8 + 1, make_float4(o[4], o[5], o[6], o[7]));
-        if (c8 == 0) __stcg(reinterpret_cast<float2*>(out + 128), make_float2(m, l));
-    }
-}
-
 template <int HD, bool BF, bool LOW>
 cudaError_t launch_one(const SharedArgs& t, int blocks, cudaStream_t st) {
-    const cudaError_t e = launch_k(k_attend_shared<HD, BF, LOW>, dim3(blocks), dim3(kThreads), Cfg<HD>::kSmem, st, t);
-    if (e != cudaSuccess) return e;
-    const int rows = LOW ? kM : 2 * kM;
-    // at most so many pieces: 128 rows of an item, 16 columns
-    const int64_t pieces = (int64_t)t.a.Hkv * (t.n_groups + (int64_t)t.a.B * (t.a.H / t.a.Hkv) / rows) * (rows / kM) * (HD / 16);
-    return launch_k(k_attend_shared_join<HD>, dim3((int)std::min<int64_t>(pieces, 3 * blocks)), dim3(kJoinThreads), 0, st, t, rows);
+    return launch_k(k_attend_shared<HD, BF, LOW>, dim3(blocks), dim3(kThreads), Cfg<HD>::kSmem, st, t);
 }
 template <int HD, bool BF>
 cudaError_t launch_low(const SharedArgs& t, bool low, int blocks, cudaStream_t st) {
@@ -911,7 +854,7 @@ cudaError_t launch_attend_shared(const AttendArgs& a, const int32_t* group, cons
     if (!*taken) return cudaSuccess;
     t.a = a;
     t.group = group; t.shared = shared; t.n_groups = n_groups; t.box = box;
-    t.worth = worth; t.blocks = sms;
+    t.worth = worth;
     const bool low = a.dtype != a.kv_dtype;
     if (hd == 64) return bf ? launch_low<64, true>(t, low, sms, st) : launch_low<64, false>(t, low, sms, st);
     return bf ? launch_low<128, true>(t, low, sms, st) : launch_low<128, false>(t, low, sms, st);

@@ -26,7 +26,7 @@
 // registers.  Where fp16 or bf16 does not hold q (fp32) or the probabilities (fp32 results, bf16
 // caches), a second product adds what the rounding left.  (tcgen05 needs 64 or 128 query
 // rows, of which 1 to 8 would hold work.)
-#include "attend_dev.cuh"
+#include "mma_dev.cuh"
 
 namespace sd {
 namespace {
@@ -43,96 +43,6 @@ struct alignas(128) SplitArgs {
     AttendArgs a;
     int32_t box, groups;      // positions of a box (all of one page), boxes of a tile's keys or values and column part
 };
-
-__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t* r) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t* r) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-template <bool BF>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// two e4m3 values (a 16-bit half of w) as fp16x2: exact
-__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t w) {
-    uint32_t d;
-    asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(w));
-    return d;
-}
-// What the rounding of q to fp16 left is kept 2^12 times as large (below 2): from 2^-25 on it would be subnormal
-constexpr float kLow = 4096.f;
-
-// x, y rounded to the product's type, and what the rounding left, times `up`
-template <bool BF>
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, float up = 1.f) {
-    if constexpr (BF) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn((x - f.x) * up, (y - f.y) * up);
-        hi = *reinterpret_cast<const uint32_t*>(&h);
-        lo = *reinterpret_cast<const uint32_t*>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(x, y);
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn((x - f.x) * up, (y - f.y) * up);
-        hi = *reinterpret_cast<const uint32_t*>(&h);
-        lo = *reinterpret_cast<const uint32_t*>(&l);
-    }
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t round2(float x, float y) {
-    uint32_t hi, lo;
-    split2<BF>(x, y, hi, lo);
-    return hi;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-// high and low product; an infinite high product has no low one (0 * inf)
-__device__ __forceinline__ float add_low(float hi, float lo) { return hi - hi == 0.f ? fmaf(lo, 1.f / kLow, hi) : hi; }
-
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t lds1(uint32_t at) {
-    uint32_t x;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-    return x;
-}
-__device__ __forceinline__ float2 lds2(uint32_t at) {
-    float2 x;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
-    return x;
-}
-// N (2 or 4) consecutive elements
-template <int N>
-__device__ __forceinline__ void storev(void* p, int64_t i, int dt, const float* v) {
-    if (dt == SD_F32) {
-#pragma unroll
-        for (int x = 0; x < N; x += 2) *reinterpret_cast<float2*>(static_cast<float*>(p) + i + x) = make_float2(v[x], v[x + 1]);
-    } else {
-        uint32_t w[N / 2];
-#pragma unroll
-        for (int x = 0; x < N; x += 2) w[x / 2] = dt == SD_F16 ? round2<false>(v[x], v[x + 1]) : round2<true>(v[x], v[x + 1]);
-        uint16_t* q = static_cast<uint16_t*>(p) + i;
-        if constexpr (N == 4) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
-}
 
 constexpr int kUnits = 4;                             // units prepared ahead
 constexpr int kMinTiles = 2;                          // of a part of a unit, where blocks are not short
@@ -170,7 +80,7 @@ struct Shape {
 // What the warps on a unit need to know: m0 its first query row, tiles [i0, i0 + tiles) its part in this block
 struct Unit {
     int64_t m0;
-    int b, g, len, rows, i0, tiles, c_lo, c_hi, begins, skip;
+    int b, g, len, rows, i0, tiles, c_lo, c_hi, begins;
 };
 
 template <int HD, int KV>
@@ -216,13 +126,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     }
     pdl_trigger();
     pdl_wait();
+    if (a.shared && __ldcg(a.shared)) return;                             // the kernels for shared pages have done it
 
     const bool few = a.B <= 32;                                           // a lane for each row, in every warp
-    // positions of a row behind the ones that its group attends to together
-    auto length = [&](int b) {
-        const int n = min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len);
-        return a.skip ? (int)max(n - (int64_t)__ldcg(a.skip + b) * a.by_ps.d, (int64_t)0) : n;
-    };
+    auto length = [&](int b) { return min(max(a.len ? __ldcg(a.len + b) : a.max_len, 0), a.max_len); };
     auto tiles = [&](int len) { return (len + kTile - 1) / kTile; };
 
     // ---- this block's share.  Where every unit can have a block of its own, units are cut into parts of `per` tiles
@@ -326,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
     auto next_unit = [&](Unit& p) -> bool {
         if (t >= t_end) return false;
         p.b = b_at;
-        p.skip = a.skip ? __ldcg(a.skip + b_at) : 0;
         p.len = few ? __shfl_sync(0xffffffffu, len0, b_at) : b_at < kThreads ? s_len[b_at] : length(b_at);
         const int real_tiles = tiles(p.len), nt = padded(real_tiles);
         const int64_t u = quot(t - base, nt), u0 = base + u * nt;        // the unit's tiles [u0, u0 + nt)
@@ -369,21 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                 __syncwarp();
                 if (lane == 0) mb_arrive(smem_u32(&s_uempty[nu % kUnits]));
                 if (!u.rows) break;
-                // what the shared pages give to the warp's rows: loaded here, needed behind the unit's tiles
-                float pre[2][kVec], pm[2] = {-INFINITY, -INFINITY}, pl[2] = {0.f, 0.f};
-                if (u.skip) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = mw + kMergers * e;
-                        if (r >= u.rows) continue;
-                        const float* p = a.common + ((int64_t)u.b * a.H + u.g * G + u.m0 + r) * kSharedRecord;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 128));
-                        pm[e] = ml.x;
-                        pl[e] = ml.y;
-#pragma unroll
-                        for (int x = 0; x < kVec; ++x) pre[e][x] = __ldcg(p + lane * kVec + x);
-                    }
-                }
                 if (!warp_wait(smem_u32(&s_done), nu & 1, bad)) break;
                 float val[2][kVec], mm[2], ll[2];
 #pragma unroll
@@ -464,19 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
                     }
                 }
                 if (!last) continue;
-                if (u.skip) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (pl[e] == 0.f) continue;
-                        const float mx = fmaxf(mm[e], pm[e]);
-                        const float f0 = mm[e] == -INFINITY ? 1.f : ex2(mm[e] - mx);
-                        const float f1 = (pm[e] == -INFINITY ? 1.f : ex2(pm[e] - mx)) * ex2(S::kShift);
-                        ll[e] = ll[e] * f0 + pl[e] * f1;
-#pragma unroll
-                        for (int x = 0; x < kVec; ++x) val[e][x] = val[e][x] * f0 + pre[e][x] * f1;
-                        mm[e] = mx;
-                    }
-                }
                 if (dead) ll[0] = ll[1] = NAN;
                 const float vs = a.v_scale ? __ldcg(a.v_scale + u.g) : 1.f;
 #pragma unroll
@@ -546,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_split(const __grid_const
             auto lookup = [&](int i, int k) -> int {
                 const int pos = (p.i0 + i) * kTile + (k * 32 + lane) * box;
                 if (i >= p.tiles || k * 32 + lane >= groups || pos >= p.len) return -1;
-                return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + p.skip + a.by_ps.div((uint32_t)pos)) : p.b;
+                return a.table ? __ldcg(a.table + (int64_t)p.b * a.table_stride + a.by_ps.div((uint32_t)pos)) : p.b;
             };
             const int outer = a.table ? a.n_pages : a.B;
             int x = (int)((turn_of + kLoaders - n % kLoaders) % kLoaders), ahead = lookup(x >> 1, 0);

@@ -85,11 +85,12 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream,
         e = launch_attend_tc(a, hd, ws->sms, st, &taken);
     if (share(ws, a, hd, groups)) {
         a.recs = ws->recs;
-        a.common = ws->common;
-        a.skip = ws->skip;
+        a.desc = ws->desc;
+        a.shared = reinterpret_cast<int32_t*>(ws->desc + kSharedRows);
         bool shared = false;
         e = launch_attend_shared(a, groups.group, groups.shared, groups.n, hd, ws->sms, st, ws->share_bytes / (4 * hd), &shared);
-        if (!shared) a.skip = nullptr;
+        if (!shared) a.shared = nullptr;
+        if (shared && e == cudaSuccess) e = launch_attend_own(a, hd, st);
         if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     }
     if (!taken) e = launch_attend_split(a, hd, ws->sms, st);
@@ -101,7 +102,7 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream,
 int pages_args(const char* who, sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
                const int32_t* len_dev, int32_t R, int32_t dtype, const void* q_dev, int64_t q_stride, int32_t n_head, float scale,
                void* out_dev, int64_t out_stride, float* lse_dev, AttendArgs* out, int* hd) {
-    sd_pages c;
+    sd_pages c = {};
     if (int rc = check_pages(who, cache, &c)) return rc;
     if (R < 0 || table_stride < 1) return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d", who, R, table_stride);
     if (!table_dev || !len_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
@@ -143,8 +144,7 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     const size_t blocks = (size_t)ws->sms;
     if (e == cudaSuccess) e = cudaMalloc(&ws->part, blocks * kTcRecord * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&ws->recs, (kSharedRows + blocks * kSharedBlock) * kSharedRecord * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(&ws->common, (size_t)kSharedRows * kSharedRecord * sizeof(float));
-    if (e == cudaSuccess) e = cudaMalloc(&ws->skip, kSharedRows * sizeof(int));
+    if (e == cudaSuccess) e = cudaMalloc(&ws->desc, kSharedRows * sizeof(SharedRow) + sizeof(int32_t));
     const size_t words = counters(ws->sms) + 1;
     if (e == cudaSuccess) e = cudaMalloc(&ws->cnt, words * sizeof(int));
     // on the legacy stream, and waited for: the first call may be on any stream
@@ -162,6 +162,7 @@ int sd_attn_ws_create(int32_t device, sd_attn_ws** out) {
     if (e == cudaSuccess) e = prepare_attend_split();
     if (e == cudaSuccess) e = prepare_attend_tc();
     if (e == cudaSuccess) e = prepare_attend_shared();
+    if (e == cudaSuccess) e = prepare_attend_own();
     if (e != cudaSuccess) {
         sd_attn_ws_destroy(ws);
         return op_fail(e == cudaErrorMemoryAllocation ? SD_ERR_OOM : SD_ERR_CUDA, "sd_attn_ws_create: %s",
@@ -176,8 +177,7 @@ void sd_attn_ws_destroy(sd_attn_ws* ws) {
     sd::DeviceScope scope(ws->device);
     cudaFree(ws->part);
     cudaFree(ws->recs);
-    cudaFree(ws->common);
-    cudaFree(ws->skip);
+    cudaFree(ws->desc);
     cudaFree(ws->cnt);
     cudaFreeHost(ws->err);
     delete ws;
