@@ -25,8 +25,8 @@ namespace sd {
 // Of a request whose first `skip` pages are attended to for its whole group of `size` requests from r0 on: the rows
 // (request - r0, head) of a kv head are in items of `rows`, each of `tiles` tiles behind kShareLead empty ones; the group's
 // first tile is `base` of all, and a block took `per` of them.
-struct SharedRow {
-    int32_t skip, r0, size, tiles, rows, unused;
+struct alignas(16) SharedRow {
+    int32_t skip, r0, size, tiles, rows, unused[3];
     int64_t base, per;
 };
 constexpr int kShareLead = 3;                                     // what beginning and ending an item costs, in tiles

@@ -34,13 +34,21 @@ __global__ void __launch_bounds__(kThreads, 3) k_attend_own(const __grid_constan
     extern __shared__ unsigned char smraw[];
     pdl_trigger();
     pdl_wait();
-    if (!__ldcg(a.shared)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.H / a.Hkv, RT = (G + kSplitRows - 1) / kSplitRows, ps = (int)a.by_ps.d;
     const int unit = blockIdx.x, rg = unit / RT, tile = unit - rg * RT, b = rg / a.Hkv, g = rg - b * a.Hkv;
     const int rows = min(kSplitRows, G - tile * kSplitRows), h0 = g * G + tile * kSplitRows;
-    const SharedRow d = a.desc[b];
-    const int own = (int)max(min(max(__ldcg(a.len + b), 0), a.max_len) - (int64_t)d.skip * ps, (int64_t)0);
+    // asked for together: whatever is not in L2 costs microseconds here
+    const int serve = __ldcg(a.shared), len = __ldcg(a.len + b);
+    SharedRow d;
+    {
+        const int4 x = __ldcg(reinterpret_cast<const int4*>(a.desc + b)), y = __ldcg(reinterpret_cast<const int4*>(a.desc + b) + 1);
+        const longlong2 z = *reinterpret_cast<const longlong2*>(reinterpret_cast<const int4*>(a.desc + b) + 2);
+        d.skip = x.x; d.r0 = x.y; d.size = x.z; d.tiles = x.w;
+        d.rows = y.x; d.base = z.x; d.per = z.y;
+    }
+    if (!serve) return;
+    const int own = (int)max(min(max(len, 0), a.max_len) - (int64_t)d.skip * ps, (int64_t)0);
     const bool dead = __ldcg(a.dead) != 0;
     const uint32_t sm = (smem_u32(smraw) + 127u) & ~127u, mine = sm + warp * (kStages * 2 * S::kBytes);
 

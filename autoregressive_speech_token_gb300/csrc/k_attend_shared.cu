@@ -73,12 +73,16 @@ struct Groups32 {
 };
 // A group's tiles, with the empty ones before each item
 __device__ __forceinline__ int64_t span(const Group& p) { return p.tiles ? (int64_t)(p.tiles + kShareLead) * p.items : 0; }
-// By all threads of a block of `threads`; s_sum has two words for each warp.
+// By the kOthers threads behind the softmax warps; s_sum has two words for each warp.
 //
 // Sharing pays if it saves `worth` rows of keys and values, and if no request has so many positions of its own that the
 // one block that takes them (some 40 GB/s) ends behind the time that all others need for what is saved (some 5 TB/s).
-__device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int threads, int64_t* s_sum) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+constexpr int kOthers = kThreads - 32 * kSoftWarps;
+__device__ __forceinline__ void others_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kOthers) : "memory"); }
+__device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int64_t* s_sum) {
+    constexpr int threads = kOthers;
+    const int tid = threadIdx.x - 32 * kSoftWarps, lane = tid & 31, warp = tid >> 5;
+    int len0 = tid < t.a.B ? __ldcg(t.a.len + tid) : 0;           // asked for beside the groups
     Groups32 g = {};
     g.few = t.n_groups <= 32;
     int64_t tiles = 0, saved = 0;
@@ -98,8 +102,8 @@ __device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int
         g.T = __shfl_sync(0xffffffffu, at, 31);
         // the most positions that a request has of its own: a thread for each request
         int most = 0;
-        for (int b = threadIdx.x; b - lane < t.a.B; b += threads) {
-            const int len = b < t.a.B ? min(max(__ldcg(t.a.len + b), 0), t.a.max_len) : 0;
+        for (int b = tid; b - lane < t.a.B; b += threads) {
+            const int len = b < t.a.B ? min(max(b == tid ? len0 : __ldcg(t.a.len + b), 0), t.a.max_len) : 0;
             int64_t skip = 0;
             for (int x = 0; x < t.n_groups; ++x) {
                 const int r0 = __shfl_sync(0xffffffffu, g.mine.r0, x), size = __shfl_sync(0xffffffffu, g.mine.size, x);
@@ -110,11 +114,11 @@ __device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int
         }
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) s_sum[warp] = most;
-        __syncthreads();
+        others_sync();
         for (int w = 0; w < threads / 32; ++w) most = max(most, (int)s_sum[w]);
         if (t.worth > 0 && saved < 128 * (int64_t)most) g.T = 0;
     } else {
-        for (int x = threadIdx.x; x < t.n_groups; x += threads) {
+        for (int x = tid; x < t.n_groups; x += threads) {
             const Group p = group_of(t, x, rows);
             tiles += span(p);
             saved += saves(p);
@@ -128,7 +132,7 @@ __device__ __forceinline__ Groups32 groups_of(const SharedArgs& t, int rows, int
             s_sum[2 * warp] = tiles;
             s_sum[2 * warp + 1] = saved;
         }
-        __syncthreads();
+        others_sync();
         saved = 0;
         for (int w = 0; w < threads / 32; ++w) {
             g.T += s_sum[2 * w];
@@ -154,7 +158,7 @@ __device__ __forceinline__ int64_t tiles_of_block(int64_t T, int blocks) { retur
 struct Item {
     int r0, g, i0, tiles, pages, m0, rows, size;
 };
-constexpr int kItems = 2;                                         // prepared ahead
+constexpr int kItems = 3;                                         // prepared ahead
 
 // O += P V: P of 32 positions lies in the first 16 columns of their scores (its low part in the other 16)
 template <int K, int kEnd>
@@ -180,8 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     __shared__ uint32_t s_mask[kMasks][4], s_tmem;
     __shared__ int2 s_box[2][32];
     __shared__ __align__(8) float s_row[2 * kM];
-    // a row's scale, from the first warpgroup to the second, and later its maximum, and its sum, back; sums at the start
+    // a row's scale, from the first warpgroup to the second, and later its maximum, and its sum, back
     float *s_scale = s_row, *s_top = s_row, *s_sum = s_row + kM;
+    int64_t* s_red = reinterpret_cast<int64_t*>(s_box);           // the loaders' from the first piece on, which follows the sums
     __shared__ int s_bad;
     const AttendArgs& a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -190,47 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     const int G = a.H / a.Hkv, ps = (int)a.by_ps.d;
     volatile int* bad = &s_bad;
     pdl_trigger();
-    pdl_wait();
-
-    // ---- groups, their tiles, and whether it is worth it
-    const Groups32 groups = groups_of(t, kRows, kThreads, reinterpret_cast<int64_t*>(s_row));
-    const int64_t T = groups.T, per = tiles_of_block(T, gridDim.x);
-    const int64_t t_begin = blockIdx.x * per, t_end = min(T, t_begin + per);
-    // which kernel follows, and what it needs to know of each request: a warp for a request
-    if (blockIdx.x == 0 && tid == 0) *a.shared = T > 0;
-    if (!T) return;
-    for (int b = blockIdx.x + gridDim.x * warp; b < a.B; b += gridDim.x * (kThreads / 32)) {
-        SharedRow d = {};
-        int64_t base = 0;
-        for (int x0 = 0; x0 < t.n_groups; x0 += 32) {
-            Group p = groups.mine;
-            int64_t first = groups.first;
-            if (!groups.few) {
-                p = x0 + lane < t.n_groups ? group_of(t, x0 + lane, kRows) : Group{};
-                int64_t sum = span(p);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += y;
-                }
-                first = base + sum - span(p);
-                base += __shfl_sync(0xffffffffu, sum, 31);
-            }
-            const uint32_t here = __ballot_sync(0xffffffffu, p.tiles && b >= p.r0 && b < p.r0 + p.size);
-            if (!here) continue;
-            const int x = __ffs(here) - 1;
-            d.skip = __shfl_sync(0xffffffffu, p.pages, x);
-            d.r0 = __shfl_sync(0xffffffffu, p.r0, x);
-            d.size = __shfl_sync(0xffffffffu, p.size, x);
-            d.tiles = __shfl_sync(0xffffffffu, p.tiles, x);
-            d.base = __shfl_sync(0xffffffffu, first, x);
-            break;
-        }
-        d.rows = kRows;
-        d.per = per;
-        if (lane == 0) a.desc[b] = d;
-    }
-    if (t_begin >= T) return;
 
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
@@ -241,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             mb_init(smem_u32(&s_full[s]), 1);
             mb_init(smem_u32(&s_empty[s]), 1);
         }
-        mb_init(smem_u32(&s_qfull), kSoftWarps);
+        mb_init(smem_u32(&s_qfull), LOW ? kSoftWarps : 1);
         mb_init(smem_u32(&s_qempty), 1);
         mb_init(smem_u32(&s_half), kM / 32);
         mb_init(smem_u32(&s_joined), kM / 32);
@@ -277,27 +241,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     };
     Item it;
 
+    pdl_wait();
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        // ---------------------------------------------------- groups, their tiles, and whether it is worth it
+        const Groups32 groups = groups_of(t, kRows, s_red);
+        const int64_t T = groups.T, per = tiles_of_block(T, gridDim.x);
+        const int64_t t_begin = blockIdx.x * per, t_end = min(T, t_begin + per);
         if (warp == kKeyWarp || warp == kValueWarp) {
             // ------------------------------------------------ loads: a tile's keys (entry 2 j of the ring) or values (2 j + 1)
             const int op = warp - kKeyWarp;
             uint32_t n = 0, last = 0;                              // tiles of the items before; entries up to this warp's last
             bool ok = true;
             const int box = t.box, groups = kN / box;
-            while (ok && take(it, false)) {
-                const int32_t* table = a.table + (int64_t)it.r0 * a.table_stride;
-                const int64_t limit = min((int64_t)it.pages * ps, (int64_t)a.max_len);
-                auto lookup = [&](int j, int k) -> int {           // page of this lane's box, -1 without one
-                    const int64_t pos = (int64_t)(it.i0 + j) * kN + (k * 32 + lane) * box;
-                    if (j >= it.tiles || k * 32 + lane >= groups || pos >= limit) return -1;
-                    return __ldcg(table + a.by_ps.div((uint32_t)pos));
-                };
-                int ahead = lookup(0, 0);
+            auto lookup = [&](const Item& it, int j, int k) -> int {   // page of this lane's box, -1 without one
+                const int64_t pos = (int64_t)(it.i0 + j) * kN + (k * 32 + lane) * box;
+                if (j >= it.tiles || k * 32 + lane >= groups || pos >= min((int64_t)it.pages * ps, (int64_t)a.max_len)) return -1;
+                return __ldcg(a.table + (int64_t)it.r0 * a.table_stride + a.by_ps.div((uint32_t)pos));
+            };
+            Item next;
+            bool have_next = take(next, false);
+            int next_id = have_next ? lookup(next, 0, 0) : -1;
+            while (ok && have_next) {
+                it = next;
+                int ahead = next_id;
+                // the next piece and its first pages: not waited for before this piece's last tile
+                have_next = take(next, false);
+                next_id = have_next ? lookup(next, 0, 0) : -1;
                 for (int j = 0; j < it.tiles && ok; ++j) {
                     const int first = (it.i0 + j) * kN;
                     const int id0 = ahead;
-                    ahead = lookup(j + 1, 0);                      // a tile ahead: not waited for here
+                    ahead = lookup(it, j + 1, 0);                  // a tile ahead: not waited for here
                     const uint32_t e = 2 * (n + j) + op, slot = e % kSt, turn = e / kSt;
                     if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
                     if (!ok) break;
@@ -310,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     __syncwarp();
 #pragma unroll 1
                     for (int k = 0; k * 32 < groups; ++k) {
-                        int id = k == 0 ? id0 : lookup(j, k);
+                        int id = k == 0 ? id0 : lookup(it, j, k);
                         if ((uint32_t)id >= (uint32_t)a.n_pages) id = -1;
                         const int row = (k * 32 + lane) * box, pos = first + row;
                         const int in = pos - (int)(a.by_ps.div((uint32_t)pos) * a.by_ps.d);
@@ -359,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             // ---------------------------------------------------- pieces, ahead of everyone
             int x = 0;
             int64_t at = t_begin, base = 0;
-            if (groups.few) {
+            if (t_begin >= T) {
+            } else if (groups.few) {
                 const int64_t n = span(groups.mine);
                 x = __ffs(__ballot_sync(0xffffffffu, n && groups.first <= at && at < groups.first + n)) - 1;
                 base = __shfl_sync(0xffffffffu, groups.first, x & 31);
@@ -383,9 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     base += __shfl_sync(0xffffffffu, sum, 31);
                 }
             }
-            Group p = group_at(t, groups, x, kRows);
+            Group p = t_begin < T ? group_at(t, groups, x, kRows) : Group{};
             bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
+            auto make = [&](Item& it) {
                 it.tiles = 0;
                 while (at < t_end && it.tiles <= 0) {
                     if (at >= base + span(p)) {
@@ -407,14 +382,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     at = end;
                 }
                 it.tiles = max(it.tiles, 0);
+            };
+            auto post = [&](uint32_t n, const Item& it) {
                 const uint32_t slot = n % kItems;
                 if (n >= kItems) ok = warp_wait(smem_u32(&s_iempty[slot]), (n / kItems - 1) & 1, bad);
-                if (!ok) break;
-                if (lane == 0) {
+                if (ok && lane == 0) {
                     s_item[slot] = it;
                     mb_arrive(smem_u32(&s_ifull[slot]));
                 }
-                if (!it.tiles) break;
+                __syncwarp();
+            };
+            Item later;
+            make(it);
+            post(0, it);
+            // a piece is known one piece before its queries are loaded: its keys need not wait for them
+            for (uint32_t n = 0; ok && it.tiles; ++n, it = later) {
+                make(later);
+                post(n + 1, later);
+                if (!ok) break;
+                if constexpr (LOW) {
+                    // its queries on their way: what is not in L2 waits behind everything that the loaders have asked for
+                    for (int r = lane; r < it.rows; r += 32) {
+                        const int row = it.m0 + r, b = it.r0 + row / G, bytes = a.dtype == SD_F32 ? 4 : 2;
+                        const char* q = static_cast<const char*>(a.q) + (b * a.q_batch + (int64_t)(it.g * G + row % G) * HD) * bytes;
+                        for (int x = 0; x < HD * bytes; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
+                    }
+                } else {
+                    // its queries to shared memory, as soon as the last scores of the piece before are formed
+                    if (n > 0) ok = warp_wait(smem_u32(&s_qempty), (n - 1) & 1, bad);
+                    if (!ok) break;
+                    const int tiles = it.rows > kM ? 2 : 1, col = lane % (HD / 8);
+                    for (int r = lane / (HD / 8); r < tiles * kM; r += 32 / (HD / 8)) {
+                        const int row = it.m0 + min(r, it.rows - 1), b = it.r0 + row / G;
+                        const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch + (int64_t)(it.g * G + row % G) * HD + col * 8;
+                        const uint32_t dst = sm + (r >> 7) * C::kTileBytes + (col >> 3) * C::kPanel + (r & 127) * 128 + (((col & 7) ^ (r & 7)) << 4);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(q) : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(smem_u32(&s_qfull));
+                }
+            }
+            // which kernel follows, and what it needs to know of each request
+            if (blockIdx.x == 0 && lane == 0) *a.shared = T > 0;
+            for (int b = blockIdx.x; b < a.B && T; b += gridDim.x) {
+                SharedRow d = {};
+                int64_t start = 0;
+                for (int x0 = 0; x0 < t.n_groups; x0 += 32) {
+                    Group q = groups.mine;
+                    int64_t first = groups.first;
+                    if (!groups.few) {
+                        q = x0 + lane < t.n_groups ? group_of(t, x0 + lane, kRows) : Group{};
+                        int64_t sum = span(q);
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                            if (lane >= o) sum += y;
+                        }
+                        first = start + sum - span(q);
+                        start += __shfl_sync(0xffffffffu, sum, 31);
+                    }
+                    const uint32_t here = __ballot_sync(0xffffffffu, q.tiles && b >= q.r0 && b < q.r0 + q.size);
+                    if (!here) continue;
+                    const int x = __ffs(here) - 1;
+                    d.skip = __shfl_sync(0xffffffffu, q.pages, x);
+                    d.r0 = __shfl_sync(0xffffffffu, q.r0, x);
+                    d.size = __shfl_sync(0xffffffffu, q.size, x);
+                    d.tiles = __shfl_sync(0xffffffffu, q.tiles, x);
+                    d.base = __shfl_sync(0xffffffffu, first, x);
+                    break;
+                }
+                d.rows = kRows;
+                d.per = per;
+                if (lane == 0) a.desc[b] = d;
             }
         } else if (warp == kMmaWarp) {
             if (elect_one()) {
@@ -536,34 +577,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
         const float s0 = fabsf(a.scale) * kLog2e;
         uint32_t ns = 0, no = 0, nq = 0, n = 0, halves = 0;
         bool ok = true;
-        while (ok && take(it, false)) {
+        // The first turn is a dry one, over whatever tensor memory holds and before any product is issued, beside the other
+        // warps' look at the groups: it brings the loop into the instruction cache.  Once the loads of all blocks are
+        // under way a miss waits behind them, and the first tile took 9000 cycles.
+        bool dry = true;
+        auto row_of = [&](const Item& x) { return x.m0 + (!LOW && x.rows > kM ? i * kM : 0) + r; };
+        auto row_in = [&](const Item& x) { return (!LOW && x.rows > kM ? i * kM : 0) + r < x.rows; };
+        // the length of this thread's row of a piece
+        auto ask = [&](const Item& x) { return row_in(x) ? __ldcg(a.len + x.r0 + row_of(x) / G) : 0; };
+        Item next = {};
+        int next_len = 0;
+        bool have_next = true;
+        while (ok) {
+            int len = 0;
+            if (dry) {
+                it = Item{};
+                it.tiles = i + 1;
+            } else {
+                if (!have_next) break;
+                it = next;
+                len = next_len;
+                have_next = take(next, false);
+                if (have_next) next_len = ask(next);
+            }
             const bool two = !LOW && it.rows > kM;
             // ---- this thread's row: request b, head h, and how many of the common positions it has
-            const int local = (two ? i * kM : 0) + r;
-            const bool mine = local < it.rows;
-            const int mrow = mine ? it.m0 + local : 0, qi = mrow / G, b = it.r0 + qi, h = it.g * G + (mrow - qi * G);
-            const int len = mine ? __ldcg(a.len + b) : 0;
-            // ---- queries to shared memory
-            if (nq > 0) ok = warp_wait(smem_u32(&s_qempty), (nq - 1) & 1, bad);
-            if (!ok) break;
+            const bool mine = row_in(it);
+            const int local = (two ? i * kM : 0) + r, mrow = mine ? row_of(it) : 0, qi = mrow / G, b = it.r0 + qi, h = it.g * G + (mrow - qi * G);
             float sl = s0;
-            if (two || i == 0) {
-                const uint32_t dst = sm + (two ? i : 0) * C::kTileBytes + r * 128;
+            if (!dry) {
+            if constexpr (LOW) {
+              // ---- queries to shared memory, in two parts
+              if (nq > 0) ok = warp_wait(smem_u32(&s_qempty), (nq - 1) & 1, bad);
+              if (!ok) break;
+              if (i == 0) {
+                const uint32_t dst = sm + r * 128;
                 const int64_t src = b * a.q_batch + (int64_t)h * HD;
-                if constexpr (!LOW) {
-                    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-                    uint4 q[HD / 8];
-#pragma unroll
-                    for (int c = 0; c < HD / 8; ++c)
-                        q[c] = mine ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + src + c * 8)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < HD / 8; ++c) {
-                        const uint4 w = q[c];
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(dst + (c >> 3) * C::kPanel + (((c & 7) ^ (r & 7)) << 4)), "r"(w.x ^ flip), "r"(w.y ^ flip), "r"(w.z ^ flip),
-                                     "r"(w.w ^ flip) : "memory");
-                    }
-                } else {
+                {
                     float y[HD];                                   // the row, all loads in flight together
                     if (!mine) {
 #pragma unroll
@@ -616,61 +666,77 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     s_scale[r] = sl;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            __syncwarp();
-            if (lane == 0) mb_arrive(smem_u32(&s_qfull));
-            if (LOW) {
-                ok = warp_wait(smem_u32(&s_qfull), nq & 1, bad);   // the other warpgroup's rows
-                if (!ok) break;
-                sl = s_scale[r];
+              }
+              __syncwarp();
+              if (lane == 0) mb_arrive(smem_u32(&s_qfull));
+              ok = warp_wait(smem_u32(&s_qfull), nq & 1, bad);     // the other warpgroup's rows
+              if (!ok) break;
+              sl = s_scale[r];
             }
             ++nq;
+            }
             // how many of the common positions the row has, from the piece's first
-            const int limit = (int)min((int64_t)max(len, 0), min((int64_t)it.pages * ps, (int64_t)a.max_len)) - it.i0 * kN;
+            const int limit = dry || !mine ? 1 << 30 : (int)min((int64_t)max(len, 0), min((int64_t)it.pages * ps, (int64_t)a.max_len)) - it.i0 * kN;
             const float slack = fminf(kSlack / sl, 3.0e38f);
             // the score that the reference stands at, and the one from which it moves (far rows: they subtract in every
             // tile); P = exp2((s - sub) sl - ref)
             float top = -INFINITY, mark = -INFINITY, sub = 0.f, ref = 0.f, l = 0.f;
             const int step = two ? 1 : 2;
             for (int j = two ? 0 : i; j < it.tiles; j += step) {
-                ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
-                if (!ok) break;
-                ++ns;
+                if (!dry) {
+                    ok = warp_wait(smem_u32(&s_sfull[i]), ns & 1, bad);
+                    if (!ok) break;
+                    ++ns;
+                }
                 tm_after();
-                // Chunks of 32 positions in loops that are not unrolled: the scores are read twice instead of held in 128
-                // registers, and the code is a quarter as long (its first pass, out of an empty instruction cache,
-                // took 9000 cycles unrolled)
-                const uint32_t* mask = s_mask[(n + j) % kMasks];
+                // What is seldom done stays short, in loops over tensor memory: out of an empty instruction cache every 128
+                // bytes of code cost some hundred cycles
                 const int rest = limit - j * kN;
-                auto live_of = [&](int c) {                        // chunk c's positions that the row has
-                    uint32_t x = *const_cast<const volatile uint32_t*>(mask + c);
-                    const int left = rest - 32 * c;
-                    if (left < 32) x &= left <= 0 ? 0u : 0xffffffffu >> (32 - left);
-                    return x;
-                };
-                auto load = [&](int c, float* s) {
-                    tm_ld32(ts + 32 * c, s);
-                    const uint32_t live = live_of(c);
-                    tm_wait_ld();
-                    after_wait(s);
-                    after_wait(s + 16);
-                    if (__any_sync(0xffffffffu, live != 0xffffffffu)) {
+                {
+                    const volatile uint32_t* mask = s_mask[(n + j) % kMasks];
+                    const uint32_t full = mask[0] & mask[1] & mask[2] & mask[3];
+                    if (__any_sync(0xffffffffu, rest < kN) || (full != 0xffffffffu && !dry)) {
+#pragma unroll 1
+                        for (int c = 0; c < kN; c += 16) {
+                            float x[16];
+                            tm_ld16(ts + c, x);
+                            uint32_t live = mask[c >> 5] >> (c & 16);
+                            const int left = rest - c;
+                            if (left < 16) live &= left <= 0 ? 0u : (1u << left) - 1;
+                            tm_wait_ld();
+                            after_wait(x);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = (live >> e) & 1 ? s[e] : -INFINITY;
+                            for (int e = 0; e < 16; ++e) x[e] = (live >> e) & 1 ? x[e] : -INFINITY;
+                            tm_st16(ts + c, reinterpret_cast<uint32_t*>(x));
+                        }
+                        tm_wait_st();
                     }
+                }
+                // 64 positions at a time, twice the same code: the scores are read again for the exponentials
+                constexpr int kHalf = kN / 2;
+                float s[kHalf];
+                auto load = [&](int c0) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 32) tm_ld32(ts + c0 + c, s + c);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16) after_wait(s + c);
                 };
                 float mx = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kN / 32; ++c) {
-                    float s[32];
-                    load(c, s);
-                    float m0 = s[0], m1 = s[1];
+                for (int c0 = 0; c0 < kN; c0 += kHalf) {
+                    load(c0);
+                    float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-                    for (int e = 2; e + 4 <= 32; e += 4) {
-                        m0 = max3(m0, s[e], s[e + 1]);
-                        m1 = max3(m1, s[e + 2], s[e + 3]);
+                    for (int c = 4; c + 8 <= kHalf; c += 8) {
+                        m0 = max3(m0, s[c], s[c + 1]);
+                        m1 = max3(m1, s[c + 2], s[c + 3]);
+                        m2 = max3(m2, s[c + 4], s[c + 5]);
+                        m3 = max3(m3, s[c + 6], s[c + 7]);
                     }
-                    mx = fmaxf(mx, fmaxf(max3(m0, s[30], s[31]), m1));
+                    m0 = max3(m0, s[kHalf - 4], s[kHalf - 3]);
+                    m1 = max3(m1, s[kHalf - 2], s[kHalf - 1]);
+                    mx = fmaxf(mx, fmaxf(max3(m0, m1, m2), m3));
                 }
                 if (__any_sync(0xffffffffu, mx > mark)) {
                     const bool grow = mx > (sub != 0.f ? top : mark);
@@ -697,43 +763,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     sub = far ? top : 0.f;
                     ref = (far || m == -INFINITY ? 0.f : m) - kShift;
                     mark = far ? -INFINITY : top + slack;
+                    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll 1
+                        for (int c = 0; c < kN; c += 16) {
+                            float x[16];
+                            tm_ld16(ts + c, x);
+                            tm_wait_ld();
+                            after_wait(x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[e] -= sub;
+                            tm_st16(ts + c, reinterpret_cast<uint32_t*>(x));
+                        }
+                        tm_wait_st();
+                    }
                 }
-                const bool any_far = __any_sync(0xffffffffu, sub != 0.f);
                 float2 l0 = make_float2(0.f, 0.f), l1 = l0;
                 const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(-ref, -ref);
 #pragma unroll 1
-                for (int c = 0; c < kN / 32; ++c) {
-                    float s[32];
-                    load(c, s);
-                    if (any_far) {
+                for (int c0 = 0; c0 < kN; c0 += kHalf) {
+                    load(c0);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] -= sub;
-                    }
-                    uint32_t pr[16], lo[16];
+                    for (int c = 0; c < kHalf; c += 32) {
+                        uint32_t pr[16], lo[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sl2, ref2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        if (e & 1) l1 = add2(l1, x); else l0 = add2(l0, x);
-                        pr[e] = pack2<BF>(x.x, x.y);
-                        if constexpr (LOW) {
-                            float2 f;
-                            if constexpr (BF) f = make_float2(__uint_as_float(pr[e] << 16), __uint_as_float(pr[e] & 0xffff0000u));
-                            else f = __half22float2(*reinterpret_cast<const __half2*>(&pr[e]));
-                            lo[e] = pack2<BF>(x.x - f.x, x.y - f.y);
+                        for (int e = 0; e < 16; ++e) {
+                            float2 x = fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, ref2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if (e & 1) l1 = add2(l1, x); else l0 = add2(l0, x);
+                            pr[e] = pack2<BF>(x.x, x.y);
+                            if constexpr (LOW) {
+                                float2 f;
+                                if constexpr (BF) f = make_float2(__uint_as_float(pr[e] << 16), __uint_as_float(pr[e] & 0xffff0000u));
+                                else f = __half22float2(*reinterpret_cast<const __half2*>(&pr[e]));
+                                lo[e] = pack2<BF>(x.x - f.x, x.y - f.y);
+                            }
                         }
+                        tm_st16(ts + c0 + c, pr);
+                        if constexpr (LOW) tm_st16(ts + c0 + c + 16, lo);
                     }
-                    tm_st16(ts + 32 * c, pr);
-                    if constexpr (LOW) tm_st16(ts + 32 * c + 16, lo);
-                    if (c & 1) {
-                        tm_wait_st();
-                        tm_before();
-                        __syncwarp();
-                        if (lane == 0) mb_arrive(smem_u32(&s_pfull[i][c >> 1]));
-                    }
+                    tm_wait_st();
+                    tm_before();
+                    __syncwarp();
+                    if (lane == 0 && !dry) mb_arrive(smem_u32(&s_pfull[i][c0 > 0]));
                 }
                 l += (l0.x + l0.y) + (l1.x + l1.y);
+            }
+            if (dry) {
+                dry = false;
+                have_next = take(next, false);
+                if (have_next) next_len = ask(next);
+                continue;
             }
             if (!ok) break;
             n += it.tiles;
@@ -855,7 +935,7 @@ cudaError_t launch_attend_shared(const AttendArgs& a, const int32_t* group, cons
     t.a = a;
     t.group = group; t.shared = shared; t.n_groups = n_groups; t.box = box;
     t.worth = worth;
-    const bool low = a.dtype != a.kv_dtype;
+    const bool low = a.dtype != a.kv_dtype || a.scale < 0.f;
     if (hd == 64) return bf ? launch_low<64, true>(t, low, sms, st) : launch_low<64, false>(t, low, sms, st);
     return bf ? launch_low<128, true>(t, low, sms, st) : launch_low<128, false>(t, low, sms, st);
 }
