@@ -29,7 +29,7 @@ struct alignas(16) SharedRow {
     int32_t skip, r0, size, tiles, rows, unused[3];
     int64_t base, per;
 };
-constexpr int kShareLead = 3;                                     // what beginning and ending an item costs, in tiles
+constexpr int kShareLead = 8;                                     // what beginning and ending an item costs, in tiles
 constexpr int kSharedRecord = 128 + 4;                            // floats of a row's partial result: output, maximum, sum
 constexpr int kSharedRows = 65536;                                // query rows (request, head) that a workspace has records for
 constexpr int kSharedBlock = 256;                                 // and more for each block, for the item that it continues

@@ -2,9 +2,9 @@
 // the join with what k_attend_shared.cu found for its group.
 //
 // Own parts are short (what a rollout has said since the fork) and there are many: a unit is (request, kv head, up
-// to 8 query rows) with a block of four warps, three blocks to an SM, so that the latencies of one unit pass under
-// others.  (The split kernel, one block to an SM, takes 3.4 us a unit: 24 us for 64 x 16 units of 51 positions.)  A warp
-// takes every fourth chunk of 16 or 32 positions by itself: its copies (cp.async into two stages, 0 where
+// to 8 query rows) with a block of two or four warps, twelve warps to an SM, so that the latencies of one unit pass
+// under others.  (The split kernel, one block to an SM, takes 3.4 us a unit: 24 us for 64 x 16 units of 51 positions.)  A warp
+// takes chunks of 16 or 32 positions in turn with the others, by itself: its copies (cp.async into two stages, 0 where
 // no position is), scores and sums need no other warp until the unit ends.  The products are mma.sync in transposed form,
 // S^T = K q^T and O^T = V^T P^T, as in the split kernel, with the same precision.
 #include "mma_dev.cuh"
@@ -12,10 +12,13 @@
 namespace sd {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 2;
+constexpr int kStages = 2;
 
 template <int HD>
 struct Own {
+    // Two warps a unit, six blocks to an SM, for heads of 64; four warps and three blocks for heads of 128, whose rows keep a
+    // warp twice as long (64 x 16 units of 51 positions 19 and 22 us, 97 x 8 units of 430 positions of 128: 33 and 28 us)
+    static constexpr int kWarps = HD == 64 ? 2 : 4, kThreads = 32 * kWarps, kBlocks = 12 / kWarps, kPerRow = kThreads / kSplitRows;
     static constexpr int kChunk = HD == 128 ? 16 : 32;            // positions of a warp at a time
     static constexpr int kRow = HD * 2, kCols = HD / 8;           // bytes and 16-byte columns of a position
     static constexpr int kBytes = kChunk * kRow;                  // a chunk's keys, or its values
@@ -26,9 +29,10 @@ struct Own {
 };
 
 template <int HD, bool BF>
-__global__ void __launch_bounds__(kThreads, 3) k_attend_own(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(Own<HD>::kThreads, Own<HD>::kBlocks) k_attend_own(const __grid_constant__ AttendArgs a) {
     using S = Own<HD>;
-    constexpr int kSteps = HD / 16, kOut = HD / 16, kChunk = S::kChunk, kH = kChunk / 16, kVec = HD / 16;
+    constexpr int kWarps = S::kWarps, kPerRow = S::kPerRow;
+    constexpr int kSteps = HD / 16, kOut = HD / 16, kChunk = S::kChunk, kH = kChunk / 16, kVec = HD / kPerRow;
     constexpr float kShift = BF ? 0.f : 15.f;
     constexpr uint32_t kAll = 0xffffffffu >> (32 - kChunk);
     extern __shared__ unsigned char smraw[];
@@ -89,8 +93,55 @@ __global__ void __launch_bounds__(kThreads, 3) k_attend_own(const __grid_constan
     }
     int ahead = lookup(warp + kStages * kWarps);
 
-    // ---- what the group's common pages give to row tid / 16: the records of the blocks that had part of them, in order
-    const int rr = tid >> 4, c0 = (tid & 15) * kVec;
+    // ---- the queries as the B operand: row `row`, 4 elements of each 16 a lane
+    const int row = lane >> 2, quad = lane & 3, mi = lane >> 3, mr = lane & 7;
+    const bool q_low = a.dtype == SD_F32 || (BF && a.dtype == SD_F16), p_low = a.dtype == SD_F32 || BF;
+    uint32_t qh[kSteps][2], ql[kSteps][2];
+    float scale[2];                                               // of this lane's two columns of the scores
+    {
+        float2 x[kSteps][2];
+        const int64_t src = b * a.q_batch + (int64_t)(h0 + row) * HD;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t at = src + 16 * k + 2 * quad + 8 * e;
+                x[k][e] = make_float2(0.f, 0.f);
+                if (row < rows) {
+                    if (a.dtype == SD_F32) x[k][e] = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at);
+                    else {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at);
+                        x[k][e] = a.dtype == SD_BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                                                     : __half22float2(*reinterpret_cast<const __half2*>(&w));
+                    }
+                }
+            }
+        float down = 1.f, row_scale = a.scale * kLog2e;
+        if (!BF && a.dtype != SD_F16) {
+            // wider exponents than fp16's: the row by a power of two to a largest element in [1, 2)
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fmaxf(fabsf(x[k][e].x), fabsf(x[k][e].y)));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
+            if (mx > 0.f && mx < INFINITY) {
+                down = __uint_as_float((uint32_t)(254 - e) << 23);
+                row_scale *= __uint_as_float((uint32_t)e << 23);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) split2<BF>(x[k][e].x * down, x[k][e].y * down, qh[k][e], ql[k][e], kLow);
+        scale[0] = __shfl_sync(0xffffffffu, row_scale, 8 * quad);
+        scale[1] = __shfl_sync(0xffffffffu, row_scale, 8 * quad + 4);
+    }
+
+    // ---- what the group's common pages give to row rr: the records of the blocks that had part of them, in order
+    const int rr = tid / kPerRow, c0 = tid % kPerRow * kVec;
     float pre[kVec], pm = -INFINITY, pl = 0.f;
 #pragma unroll
     for (int x = 0; x < kVec; ++x) pre[x] = 0.f;
@@ -137,53 +188,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_attend_own(const __grid_constan
                 }
             }
         }
-    }
-
-    // ---- the queries as the B operand: row `row`, 4 elements of each 16 a lane
-    const int row = lane >> 2, quad = lane & 3, mi = lane >> 3, mr = lane & 7;
-    const bool q_low = a.dtype == SD_F32 || (BF && a.dtype == SD_F16), p_low = a.dtype == SD_F32 || BF;
-    uint32_t qh[kSteps][2], ql[kSteps][2];
-    float scale[2];                                               // of this lane's two columns of the scores
-    {
-        float2 x[kSteps][2];
-        const int64_t src = b * a.q_batch + (int64_t)(h0 + row) * HD;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t at = src + 16 * k + 2 * quad + 8 * e;
-                x[k][e] = make_float2(0.f, 0.f);
-                if (row < rows) {
-                    if (a.dtype == SD_F32) x[k][e] = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at);
-                    else {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at);
-                        x[k][e] = a.dtype == SD_BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
-                                                     : __half22float2(*reinterpret_cast<const __half2*>(&w));
-                    }
-                }
-            }
-        float down = 1.f, row_scale = a.scale * kLog2e;
-        if (!BF && a.dtype != SD_F16) {
-            // wider exponents than fp16's: the row by a power of two to a largest element in [1, 2)
-            float mx = 0.f;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fmaxf(fabsf(x[k][e].x), fabsf(x[k][e].y)));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
-            if (mx > 0.f && mx < INFINITY) {
-                down = __uint_as_float((uint32_t)(254 - e) << 23);
-                row_scale *= __uint_as_float((uint32_t)e << 23);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) split2<BF>(x[k][e].x * down, x[k][e].y * down, qh[k][e], ql[k][e], kLow);
-        scale[0] = __shfl_sync(0xffffffffu, row_scale, 8 * quad);
-        scale[1] = __shfl_sync(0xffffffffu, row_scale, 8 * quad + 4);
     }
 
     // ---- this warp's chunks.  Its results: rows 2 quad and 2 quad + 1, dimensions `row` and `row` + 8 of each 16
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_attend_own(const __grid_constan
     const int64_t at = b * a.o_batch + (int64_t)h * HD + c0;
 #pragma unroll
     for (int x = 0; x < kVec; x += 4) storev<4>(a.out, at + x, a.dtype, val + x);
-    if ((tid & 15) == 0 && a.lse) a.lse[(int64_t)b * a.H + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - kShift) * kLn2;
+    if (c0 == 0 && a.lse) a.lse[(int64_t)b * a.H + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - kShift) * kLn2;
 }
 
 template <int HD, bool BF>
@@ -370,10 +374,10 @@ cudaError_t launch_attend_own(const AttendArgs& a, int hd, cudaStream_t st) {
     const int G = a.H / a.Hkv;
     const dim3 grid(a.B * a.Hkv * ((G + kSplitRows - 1) / kSplitRows));           // at most kSharedRows
     const bool bf = a.kv_dtype == SD_BF16;
-    if (hd == 64) return bf ? launch_k(k_attend_own<64, true>, grid, dim3(kThreads), Own<64>::kSmem, st, a)
-                            : launch_k(k_attend_own<64, false>, grid, dim3(kThreads), Own<64>::kSmem, st, a);
-    return bf ? launch_k(k_attend_own<128, true>, grid, dim3(kThreads), Own<128>::kSmem, st, a)
-              : launch_k(k_attend_own<128, false>, grid, dim3(kThreads), Own<128>::kSmem, st, a);
+    if (hd == 64) return bf ? launch_k(k_attend_own<64, true>, grid, dim3(Own<64>::kThreads), Own<64>::kSmem, st, a)
+                            : launch_k(k_attend_own<64, false>, grid, dim3(Own<64>::kThreads), Own<64>::kSmem, st, a);
+    return bf ? launch_k(k_attend_own<128, true>, grid, dim3(Own<128>::kThreads), Own<128>::kSmem, st, a)
+              : launch_k(k_attend_own<128, false>, grid, dim3(Own<128>::kThreads), Own<128>::kSmem, st, a);
 }
 
 }  // namespace sd

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
     constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
     extern __shared__ unsigned char smraw[];
-    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_half, s_joined, s_never, s_ifull[kItems], s_iempty[kItems];
+    __shared__ __align__(8) unsigned long long s_full[kSt], s_empty[kSt], s_qfull, s_qempty, s_sfull[2], s_pfull[2][2], s_ofull[2], s_half, s_joined, s_never, s_dry, s_ifull[kItems], s_iempty[kItems];
     __shared__ Item s_item[kItems];
     __shared__ uint32_t s_mask[kMasks][4], s_tmem;
     __shared__ int2 s_box[2][32];
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
         mb_init(smem_u32(&s_half), kM / 32);
         mb_init(smem_u32(&s_joined), kM / 32);
         mb_init(smem_u32(&s_never), 1);
+        mb_init(smem_u32(&s_dry), kSoftWarps);
         for (int i = 0; i < kItems; ++i) {
             mb_init(smem_u32(&s_ifull[i]), 1);
             mb_init(smem_u32(&s_iempty[i]), kSoftWarps + 3);
@@ -411,12 +412,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     // its queries to shared memory, as soon as the last scores of the piece before are formed
                     if (n > 0) ok = warp_wait(smem_u32(&s_qempty), (n - 1) & 1, bad);
                     if (!ok) break;
-                    const int tiles = it.rows > kM ? 2 : 1, col = lane % (HD / 8);
-                    for (int r = lane / (HD / 8); r < tiles * kM; r += 32 / (HD / 8)) {
-                        const int row = it.m0 + min(r, it.rows - 1), b = it.r0 + row / G;
-                        const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch + (int64_t)(it.g * G + row % G) * HD + col * 8;
-                        const uint32_t dst = sm + (r >> 7) * C::kTileBytes + (col >> 3) * C::kPanel + (r & 127) * 128 + (((col & 7) ^ (r & 7)) << 4);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(q) : "memory");
+                    // (rows that are not there keep what the memory holds: no other row sees it)
+                    constexpr int kStep = 32 / (HD / 8);           // rows of a turn
+                    const int col = lane % (HD / 8), r0 = lane / (HD / 8), row = it.m0 + r0;
+                    int qi = row / G, hh = row - qi * G;
+                    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(it.g * G) * HD + col * 8;
+                    const uint32_t dst = sm + (col >> 3) * C::kPanel;
+#pragma unroll 4
+                    for (int r = r0; r < it.rows; r += kStep) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                     ::"r"(dst + (r >> 7) * C::kTileBytes + (r & 127) * 128 + (((col & 7) ^ (r & 7)) << 4)),
+                                     "l"(q + (it.r0 + qi) * a.q_batch + hh * HD) : "memory");
+                        for (hh += kStep; hh >= G; hh -= G) ++qi;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -488,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                 };
                 auto loaded = [&](uint32_t e) { return mb_wait(smem_u32(&s_full[e % kSt]), (e / kSt) & 1, bad); };
                 auto release = [&](uint32_t e) { commit(smem_u32(&s_empty[e % kSt])); };
+                ok = mb_wait(smem_u32(&s_dry), 0, bad);            // the dry turn writes where scores go
+                tm_after();
                 while (ok && take(it, true)) {
                     ok = mb_wait(smem_u32(&s_qfull), nq & 1, bad);
                     if (!ok) break;
@@ -811,6 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
             }
             if (dry) {
                 dry = false;
+                tm_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(smem_u32(&s_dry));
                 have_next = take(next, false);
                 if (have_next) next_len = ask(next);
                 continue;

@@ -40,7 +40,11 @@ bool on_tiles(int Lq, int G, int hd, bool bf) {
     return units >= (hd == 64 ? 3 : 2) * pairs && (!bf || rows > 2 * kSplitRows);
 }
 
-constexpr long long kShareBytes = 48ll << 20;                     // key and value bytes that sharing has to save
+// Key and value bytes that sharing has to save, which repeated reads find in L2 else.  Shared / each by itself, us, 16 query
+// heads: 16 x 2400 positions, 8 kv heads of 128, fp16 (147 MB) 25 / 23, 16 x 5000 (307 MB) 27 / 39, 64 x 1000 (256 MB)
+// 28 / 36.  fp32 queries, whose products are two, gain at half of that: 16 x 1200, 16 kv heads of 64 (74 MB) 21 / 20, 64 x
+// 300 (74 MB) 24 / 26, 16 x 2400 (147 MB) 23 / 29.
+constexpr long long kShareBytes = 150ll << 20;
 
 size_t counters(int sms) { return (size_t)sms * kSplitRows / 2; }
 
@@ -49,6 +53,8 @@ struct Groups {
     const int32_t *group, *shared;
     int n;
 };
+
+long long share_bytes(const sd_attn_ws* ws, const AttendArgs& a) { return a.dtype == SD_F32 ? ws->share_bytes / 2 : ws->share_bytes; }
 
 // The requests of a group are served together where that saves enough.  It costs a launch of its own, and joining the
 // parts; whether the lengths are worth it is known on the device only, but not where all of the table is not.
@@ -59,7 +65,7 @@ bool share(const sd_attn_ws* ws, const AttendArgs& a, int hd, const Groups& grou
     const float s = fabsf(a.scale);
     if (!(s >= 0x1p-60f && s <= 0x1p60f)) return false;
     if ((int64_t)a.B * a.H > kSharedRows) return false;
-    return 4.0 * hd * a.Hkv * (a.B - 1) * (double)a.max_len >= (double)ws->share_bytes;
+    return 4.0 * hd * a.Hkv * (a.B - 1) * (double)a.max_len >= (double)share_bytes(ws, a);
 }
 
 int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream, const Groups& groups = {}) {
@@ -88,7 +94,7 @@ int launch(const char* who, sd_attn_ws* ws, AttendArgs& a, int hd, void* stream,
         a.desc = ws->desc;
         a.shared = reinterpret_cast<int32_t*>(ws->desc + kSharedRows);
         bool shared = false;
-        e = launch_attend_shared(a, groups.group, groups.shared, groups.n, hd, ws->sms, st, ws->share_bytes / (4 * hd), &shared);
+        e = launch_attend_shared(a, groups.group, groups.shared, groups.n, hd, ws->sms, st, share_bytes(ws, a) / (4 * hd), &shared);
         if (!shared) a.shared = nullptr;
         if (shared && e == cudaSuccess) e = launch_attend_own(a, hd, st);
         if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
