@@ -9,10 +9,11 @@
 // best entries through distributed shared memory.
 //
 // The first n entries of (z descending, index ascending): every entry is the 64-bit key (order of z, ~index), 0 if it is
-// no alternative.  The best keys of groups of threads are ranked among each other.  The n-th of them is a bound: at least
-// n keys reach it, and only keys of the n groups whose best one does.  Those read their part again (from a cache), collect
-// what reaches the bound (a few more than n) and rank it.
-// Where too many reach it (adversarial order), the n best are taken one after the other.
+// no alternative.  The best keys of groups of threads in the first batch, which is spread over the whole part, are ranked
+// among each other.  The n-th of them is a bound: at least n keys reach it.  What reaches it, a few n, is collected as the
+// row passes, and ranked at the end.  Where too much reaches it (a rising row, a mask over most of the batch), the bound is
+// taken of the whole part and the groups that reach it read theirs again; where that is still too much, the n best
+// are taken one after the other.
 //
 // Bound by the one read where rows are many, by the chain of exchanges where they are few.
 #include <algorithm>
@@ -166,16 +167,31 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     const T* z = static_cast<const T*>(a.z) + row * a.stride;
     const int lead = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));     // elements between a 16-byte boundary and the row
 
-    // ---- this thread's vectors: v0 + tid, v0 + tid + kThreads, ... of the row; vector v begins with element v kN - lead
+    // ---- this block's vectors v0, v0 + 1, ..., nv of them; vector v begins with element v kN - lead.  A thread takes vector
+    // tid of every kThreads, those of its first batch from the whole of the block's part.
     const int all = (a.V + lead + kN - 1) / kN, each = (all + C - 1) / C, v0 = c * each, nv = min(each, all - v0);
     const int whole = (a.V + lead) / kN;                   // vectors [lead > 0, whole) lie within the row
+    const int turns = max((nv + kThreads - 1) / kThreads, 0), batches = (turns + kBatch - 1) / kBatch;
     auto vector = [&](int i) {
         const int v = v0 + i;
-        return v >= (lead > 0) && v < whole && aligned(z + (v * kN - lead),16,0) ? *reinterpret_cast<const uint4*>(z + (v * kN - lead)) : load_edge(z, v * kN - lead, a.V);
+        return v >= (lead > 0) && v < whole && aligned(z + (v * kN - lead), 16, 0) ? *reinterpret_cast<const uint4*>(z + (v * kN - lead)) : load_edge(z, v * kN - lead, a.V);
     };
-    const int32_t token = a.token && aligned(a.token+row,4,1) ? a.token[row] : -1;
+    auto index_of = [&](int i) { return (v0 + i) * kN - lead; };   // of the vector's first element
+    // vector x (< kBatch) of batch b: batches take turns over the part
+    auto place = [&](int b, int x) { return (x * batches + b) * kThreads + tid; };
+    auto load = [&](int b, uint4 (&w)[kBatch]) {
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const int i = place(b, x);
+            w[x] = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
+            if (b < batches && i < nv) w[x] = vector(i);
+        }
+    };
+    uint4 w[kBatch];
+    load(0, w);
+    const int32_t token = a.token && aligned(a.token + row, 4, 1) ? a.token[row] : -1;
     const bool given = (uint32_t)token < (uint32_t)a.V;
-    const float zt = given && aligned(z+token,sizeof(T),2) ? number(z[token]) : -INFINITY;
+    const float zt = given && aligned(z + token, sizeof(T), 2) ? number(z[token]) : -INFINITY;
 
     // ---- running maximum and sums, and how many entries are ahead of the token.  The difference to the maximum is formed
     // first: exact where it counts, whatever the logits' size.  Nothing 200 / c below it counts, which keeps it finite.
@@ -183,9 +199,11 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     float m = -INFINITY, S = 0.f, D = 0.f;
     int ahead = 0, best_j = 0;
     uint4 best = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
-    auto add = [&](const uint4& w, int j) {
-        uint32_t mw = max_words<T>(max_words<T>(w.x, w.y), max_words<T>(w.z, w.w));
-        const float top = sizeof(T) == 4 ? __uint_as_float(mw) : fmaxf(element<T>(make_uint4(mw, 0, 0, 0), 0), element<T>(make_uint4(mw, 0, 0, 0), 1));
+    auto largest = [&](const uint4& w) {
+        const uint32_t mw = max_words<T>(max_words<T>(w.x, w.y), max_words<T>(w.z, w.w));
+        return sizeof(T) == 4 ? __uint_as_float(mw) : fmaxf(element<T>(make_uint4(mw, 0, 0, 0), 0), element<T>(make_uint4(mw, 0, 0, 0), 1));
+    };
+    auto add = [&](const uint4& w, int j, float top) {
         if (top > m) {
             const float by = fmaxf(m - top, least), f = ex2_(by * a.c);
             D = (D + S * by) * f;
@@ -201,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
             S += p;
             D = fmaf(d, p, D);
         }
+        if (!given) return;
         if (j > token) {
 #pragma unroll
             for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) > zt;
@@ -215,36 +234,78 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
             }
         }
     };
-    for (int i = tid; i < nv; i += kThreads * kBatch) {
-        uint4 w[kBatch];
+    // What reaches the bound tau into the list.  (Its value decides first: most vectors have nothing.)
+    auto collect = [&](const uint4& w, int j, Key tau, float bound) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (i + b * kThreads < nv) w[b] = vector(i + b * kThreads);
+        for (int e = 0; e < kN; ++e) {
+            const float x = element<T>(w, e);
+            if (!(x >= bound)) continue;
+            const Key k = key_of(x, j + e);
+            if (k >= tau) {
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kList && aligned(s_list + at, 8, 6)) s_list[at] = k;
+            }
+        }
+    };
+    // The n-th of the groups' best keys so far, 1 if there are fewer: at least n entries reach it, or all do
+    auto bound_of = [&]() -> Key {
+        int at = 0;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (i + b * kThreads < nv) add(w[b], (v0 + i + b * kThreads) * kN - lead);
+        for (int e = kN - 1; e >= 0; --e) at = element<T>(best, e) == m ? best_j + e : at;
+        Key mine = key_of(m, at);
+        mine = max_key(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+        mine = max_key(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+        if ((tid & 3) == 0 && aligned(s_best + (tid >> 2), 8, 4)) s_best[tid >> 2] = mine;
+        if (tid == 0) {
+            s_count = 0;
+            s_tau = 0;
+        }
+        if (tid < kMaxTop && aligned(s_top + tid, 8, 5)) s_top[tid] = 0;
+        __syncthreads();
+        // group tid / 4 against a quarter of the groups
+        const Key key = s_best[tid >> 2];
+        int before = 0;
+#pragma unroll 8
+        for (int g = 0; g < kGroups / 4; ++g) before += s_best[g * 4 + (tid & 3)] > key;
+        before += __shfl_xor_sync(0xffffffffu, before, 1);
+        before += __shfl_xor_sync(0xffffffffu, before, 2);
+        if ((tid & 3) == 0 && key && before == a.top - 1) s_tau = key;          // keys are distinct
+        __syncthreads();
+        return max_key(s_tau, 1);
+    };
+    auto value_bound = [&](Key tau) { return tau > 1 ? value_of((uint32_t)(tau >> 32)) : -INFINITY; };
+
+    Key tau = 0;
+    float bound = INFINITY;                                // nothing is collected without `top`
+#pragma unroll 1
+    for (int b = 0; b < batches; ++b) {
+        uint4 ahead_w[kBatch];
+        load(b + 1, ahead_w);
+        float top[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            top[x] = largest(w[x]);
+            if (place(b, x) < nv) add(w[x], index_of(place(b, x)), top[x]);
+        }
+        if (a.top) {
+            if (b == 0) {
+                tau = bound_of();
+                bound = value_bound(tau);
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x)
+                if (top[x] >= bound && place(b, x) < nv) collect(w[x], index_of(place(b, x)), tau, bound);
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) w[x] = ahead_w[x];
     }
+    if (!batches && a.top) bound_of();                     // a block without a part: nothing is in its lists
 
     // ---- the block's maximum, and its sums
     float mb = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    if (lane == 0 && aligned(s_max+warp,4,3)) s_max[warp] = mb;
-    if (a.top) {
-        // the best key of four threads
-        int at = 0;
-#pragma unroll
-        for (int e = kN - 1; e >= 0; --e) at = element<T>(best, e) == m ? best_j + e : at;
-        Key key = key_of(m, at);
-        key = max_key(key, __shfl_xor_sync(0xffffffffu, key, 1));
-        key = max_key(key, __shfl_xor_sync(0xffffffffu, key, 2));
-        if ((tid & 3) == 0 && aligned(s_best+(tid>>2),8,4)) s_best[tid >> 2] = key;
-        if (tid == 0) {
-            s_count = 0;
-            s_tau = 0;
-        }
-        if (tid < kMaxTop && aligned(s_top+tid,8,5)) s_top[tid] = 0;
-    }
+    if (lane == 0 && aligned(s_max + warp, 4, 3)) s_max[warp] = mb;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mb = fmaxf(mb, s_max[w]);
@@ -267,43 +328,28 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
 
     // ---- the block's first entries
     if (a.top) {
-        // group tid / 4 against a quarter of the groups
-        const Key key = s_best[tid >> 2];
-        int before = 0;
-#pragma unroll 8
-        for (int g = 0; g < kGroups / 4; ++g) before += s_best[g * 4 + (tid & 3)] > key;
-        before += __shfl_xor_sync(0xffffffffu, before, 1);
-        before += __shfl_xor_sync(0xffffffffu, before, 2);
-        if ((tid & 3) == 0 && key && before == a.top - 1) s_tau = key;          // keys are distinct
-        __syncthreads();
-        const Key tau = max_key(s_tau, 1);                 // fewer groups than n with an entry: all entries
-        if (key >= tau) {
-            const float bound = tau > 1 ? value_of((uint32_t)(tau >> 32)) : -INFINITY;
+        int n = s_count;
+        if (n > kList) {
+            // the first batch's bound let too many through (few entries there, or a rising row): the whole part's bound
+            __syncthreads();
+            tau = bound_of();
+            bound = value_bound(tau);
             if (m >= bound) {
 #pragma unroll 2
                 for (int i = tid; i < nv; i += kThreads) {
-                    const uint4 w = vector(i);
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) {
-                        const float x = element<T>(w, e);
-                        if (!(x >= bound)) continue;
-                        const Key k = key_of(x, (v0 + i) * kN - lead + e);
-                        if (k >= tau) {
-                            const int at = atomicAdd(&s_count, 1);
-                            if (at < kList && aligned(s_list+at,8,6)) s_list[at] = k;
-                        }
-                    }
+                    const uint4 x = vector(i);
+                    if (largest(x) >= bound) collect(x, index_of(i), tau, bound);
                 }
             }
+            __syncthreads();
+            n = s_count;
         }
-        __syncthreads();
-        const int n = s_count;
         if (n <= kList) {
             for (int i = tid; i < n; i += kThreads) {
                 const Key x = s_list[i];
                 int r = 0;
                 for (int j = 0; j < n; ++j) r += s_list[j] > x;
-                if (r < a.top && aligned(s_top+r,8,7)) s_top[r] = x;
+                if (r < a.top && aligned(s_top + r, 8, 7)) s_top[r] = x;
             }
         } else {
             Key last = ~(Key)0;
@@ -313,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
                     const uint4 w = vector(i);
 #pragma unroll
                     for (int e = 0; e < kN; ++e) {
-                        const Key x = key_of(element<T>(w, e), (v0 + i) * kN - lead + e);
+                        const Key x = key_of(element<T>(w, e), index_of(i) + e);
                         if (x < last) most = max_key(most, x);
                     }
                 }
@@ -469,12 +515,13 @@ cudaError_t launch(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
 template <typename T>
 cudaError_t choose(const ScoreArgs& a, int rows, int sms, cudaStream_t st) {
     const int64_t bytes = ((int64_t)a.V + 2 * Type<T>::kN - 2) / Type<T>::kN * 16;      // a row may begin and end inside a vector
+    // Few rows: over more SMs, as long as a block keeps 16 KB.  The part of a block is streamed, whatever its length.
     int C = 1;
-    while (C < kMaxCluster && bytes > (int64_t)C * 65536) C *= 2;
-    // few rows: over more SMs, as long as a block keeps 16 KB
-    while (C < kMaxCluster && (int64_t)rows * C * 2 <= sms && bytes > (int64_t)C * 16384) C *= 2;
+    while (C < kMaxCluster && (int64_t)rows * C * 2 <= 2 * sms && bytes > (int64_t)C * 16384) C *= 2;
     if ((int64_t)rows * C > INT32_MAX) return cudaErrorInvalidValue;
-    return bytes <= 16384 && rows > 2 * sms ? launch<T, 128>(a, rows, C, st) : launch<T, 512>(a, rows, C, st);
+    const int64_t part = bytes / C, blocks = (int64_t)rows * C;
+    if (part <= 8192 && blocks > 2 * sms) return launch<T, 128>(a, rows, C, st);
+    return part <= 65536 && blocks > 2 * sms ? launch<T, 256>(a, rows, C, st) : launch<T, 512>(a, rows, C, st);
 }
 
 }  // namespace
