@@ -64,6 +64,27 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 __device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o); }
 
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 add2_(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2_(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2_(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+
 using Key = unsigned long long;
 __device__ __forceinline__ Key key_of(float x, int32_t index) {
     const uint32_t o = order_of(x);
@@ -130,6 +151,26 @@ __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
     }
 }
 
+// The number of the type before x (x above -inf)
+template <typename T>
+__device__ __forceinline__ float before_of(float x) {
+    constexpr uint32_t kStep = sizeof(T) == 4 ? 1u : Type<T>::kBf ? 0x10000u : 0;
+    if constexpr (kStep != 0) {
+        const uint32_t b = __float_as_uint(x);
+        if (x == 0.f) return __uint_as_float(0x80000000u | kStep);
+        return __uint_as_float((b >> 31) ? b + kStep : b - kStep);
+    } else {
+        const unsigned short b = __half_as_ushort(__float2half_rn(x));
+        if (x == 0.f) return __half2float(__ushort_as_half(0x8001));
+        return __half2float(__ushort_as_half((unsigned short)((b >> 15) ? b + 1 : b - 1)));
+    }
+}
+// A number of the type twice
+template <typename T>
+__device__ __forceinline__ typename Type<T>::Pair pair_of(float x) {
+    if constexpr (Type<T>::kBf) return __float2bfloat162_rn(x);
+    else return __float2half2_rn(x);
+}
 __device__ __forceinline__ float number(float x) { return x; }
 __device__ __forceinline__ float number(__half x) { return __half2float(x); }
 __device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -151,14 +192,16 @@ __device__ __forceinline__ uint4 load_edge(const T* row, int first, int32_t V) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kBatch = 4;                                  // vectors of a thread in flight
+constexpr int kStages = 8;                                 // vectors of a thread in flight, in shared memory
+constexpr int kFirst = 4;                                  // of which the bound is taken
 
 template <typename T, int kThreads, bool kCluster>
-__global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const ScoreArgs a) {
     constexpr int kN = Type<T>::kN, kWarps = kThreads / 32, kGroups = kThreads / 4;
     __shared__ Key s_best[kGroups], s_list[kList], s_top[kMaxTop], s_tau;
     __shared__ float s_max[kWarps], s_S[kWarps], s_D[kWarps], s_mine[3];           // s_mine: this block's maximum, S, D
     __shared__ int s_ahead[kWarps], s_mine_ahead, s_count;
+    extern __shared__ uint4 s_ring[];                      // [kStages][kThreads]: a thread reads back only what it copied
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -168,27 +211,47 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     const int lead = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));     // elements between a 16-byte boundary and the row
 
     // ---- this block's vectors v0, v0 + 1, ..., nv of them; vector v begins with element v kN - lead.  A thread takes vector
-    // tid of every kThreads, those of its first batch from the whole of the block's part.
+    // tid of every kThreads; the first kFirst of its turns are from all over the part.  The row's ragged ends are an extra
+    // vector of two threads.
     const int all = (a.V + lead + kN - 1) / kN, each = (all + C - 1) / C, v0 = c * each, nv = min(each, all - v0);
-    const int whole = (a.V + lead) / kN;                   // vectors [lead > 0, whole) lie within the row
-    const int turns = max((nv + kThreads - 1) / kThreads, 0), batches = (turns + kBatch - 1) / kBatch;
-    auto vector = [&](int i) {
-        const int v = v0 + i;
-        return v >= (lead > 0) && v < whole && aligned(z + (v * kN - lead), 16, 0) ? *reinterpret_cast<const uint4*>(z + (v * kN - lead)) : load_edge(z, v * kN - lead, a.V);
-    };
-    auto index_of = [&](int i) { return (v0 + i) * kN - lead; };   // of the vector's first element
-    // vector x (< kBatch) of batch b: batches take turns over the part
-    auto place = [&](int b, int x) { return (x * batches + b) * kThreads + tid; };
-    auto load = [&](int b, uint4 (&w)[kBatch]) {
+    const int inner = lead > 0, whole = (a.V + lead) / kN; // vectors [inner, whole) lie within the row
+    const int turns = max((nv + kThreads - 1) / kThreads, 0), quarter = (turns + kFirst - 1) / kFirst;
+    const int low = max(v0, inner), count_v = max(min(whole, v0 + nv) - low, 0);
+    // vector of turn x (< kFirst) of round q, and whether it is a whole one of this part
+    auto vector_of = [&](int q, int x) { return v0 + (x * quarter + q) * kThreads + tid; };
+    auto there = [&](int v) { return (uint32_t)(v - low) < (uint32_t)count_v; };
+    auto index_of = [&](int v) { return v * kN - lead; };  // of a vector's first element
+    static_assert(kStages == 2 * kFirst, "two rounds in flight");
+    auto slot = [&](int q, int x) { return s_ring + ((q & 1) * kFirst + x) * kThreads + tid; };
+    // a round's vectors; places without one hold -inf
+    const bool sound = count_v == 0 || aligned(z + index_of(low), 16, 0);
+    auto copy = [&](int q) {
+        if (q < quarter) {
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const int i = place(b, x);
-            w[x] = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
-            if (b < batches && i < nv) w[x] = vector(i);
+            for (int x = 0; x < kFirst; ++x) {
+                const int v = vector_of(q, x);
+                if (there(v) && sound)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(slot(q, x))), "l"(z + index_of(v)) : "memory");
+                else
+                    *slot(q, x) = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint4 w[kBatch];
-    load(0, w);
+    copy(0);
+    copy(1);
+    uint4 edge = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
+    int edge_j = 0;
+    bool has_edge = false;
+    {
+        const int v = tid == 0 && inner ? 0 : tid == 1 && whole * kN < a.V + lead ? whole : -1;
+        // a row within one vector: its end is its beginning
+        if (v >= v0 && v < v0 + nv && !(v == whole && tid == 1 && whole == 0 && inner)) {
+            edge_j = index_of(v);
+            edge = load_edge(z, edge_j, a.V);
+            has_edge = true;
+        }
+    }
     const int32_t token = a.token && aligned(a.token + row, 4, 1) ? a.token[row] : -1;
     const bool given = (uint32_t)token < (uint32_t)a.V;
     const float zt = given && aligned(z + token, sizeof(T), 2) ? number(z[token]) : -INFINITY;
@@ -196,42 +259,62 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     // ---- running maximum and sums, and how many entries are ahead of the token.  The difference to the maximum is formed
     // first: exact where it counts, whatever the logits' size.  Nothing 200 / c below it counts, which keeps it finite.
     const float least = -200.f / a.c;
-    float m = -INFINITY, S = 0.f, D = 0.f;
-    int ahead = 0, best_j = 0;
-    uint4 best = make_uint4(Type<T>::kLow, Type<T>::kLow, Type<T>::kLow, Type<T>::kLow);
+    float m = -INFINITY, S = 0.f, D = 0.f;                 // m: what the sums are relative to
+    int ahead = 0;
     auto largest = [&](const uint4& w) {
         const uint32_t mw = max_words<T>(max_words<T>(w.x, w.y), max_words<T>(w.z, w.w));
         return sizeof(T) == 4 ? __uint_as_float(mw) : fmaxf(element<T>(make_uint4(mw, 0, 0, 0), 0), element<T>(make_uint4(mw, 0, 0, 0), 1));
     };
-    auto add = [&](const uint4& w, int j, float top) {
-        if (top > m) {
-            const float by = fmaxf(m - top, least), f = ex2_(by * a.c);
-            D = (D + S * by) * f;
-            S *= f;
-            m = top;
-            best = w;
-            best_j = j;
+    // the sums of a vector whose largest entry m has seen: two fp32 operations an instruction
+    float2 S2 = make_float2(0.f, 0.f), D2 = S2;
+    auto add = [&](const uint4& w, float2 ref) {
+        const float2 c2 = make_float2(a.c, a.c);
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+            float2 d = add2_(make_float2(element<T>(w, e), element<T>(w, e + 1)), ref);
+            d.x = max_nan_(d.x, least);
+            d.y = max_nan_(d.y, least);
+            float2 p = mul2_(d, c2);
+            p.x = ex2_(p.x);
+            p.y = ex2_(p.y);
+            S2 = add2_(S2, p);
+            D2 = fma2_(d, p, D2);
         }
-        const float ref = m == -INFINITY ? 0.f : m;
+    };
+    // entries of a vector, the first of them entry j, that are ahead of the token.  16-bit ones two at a time: 1 or 0 each,
+    // added up in their own type (at most 4 a vector and half, 33 vectors before they are taken out: bf16 holds whole numbers up to 256)
+    using Pair = typename Type<T>::Pair;
+    Pair ahead2 = {};
+    // x >= zt is x > (what comes before zt in the type): entries before the token and behind it differ in one number
+    const float before_zt = before_of<T>(zt);
+    const Pair zt2 = pair_of<T>(zt), before_zt2 = pair_of<T>(before_zt);
+    auto count = [&](const uint4& w, int j) {
+        const bool behind = j > token, before = j >= 0 && j + kN <= token && zt > -INFINITY;
+        if (behind || before) {
+            if constexpr (sizeof(T) == 4) {
+                const float x = behind ? zt : before_zt;
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const float d = max_nan_(element<T>(w, e) - ref, least), p = ex2_(d * a.c);
-            S += p;
-            D = fmaf(d, p, D);
-        }
-        if (!given) return;
-        if (j > token) {
+                for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) > x;
+            } else {
+                const Pair x = behind ? zt2 : before_zt2;
 #pragma unroll
-            for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) > zt;
-        } else if (j >= 0 && j + kN <= token) {
-#pragma unroll
-            for (int e = 0; e < kN; ++e) ahead += element<T>(w, e) >= zt;
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t u = word_of(w, e);
+                    ahead2 = __hadd2(ahead2, __hgt2(*reinterpret_cast<const Pair*>(&u), x));
+                }
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 const float x = element<T>(w, e);
                 ahead += x > zt || (x == zt && (uint32_t)(j + e) < (uint32_t)token);
             }
+        }
+    };
+    auto flush = [&]() {
+        if constexpr (sizeof(T) == 2) {
+            ahead += (int)(__low2float(ahead2) + __high2float(ahead2));
+            ahead2 = Pair{};
         }
     };
     // What reaches the bound tau into the list.  (Its value decides first: most vectors have nothing.)
@@ -248,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
         }
     };
     // The n-th of the groups' best keys so far, 1 if there are fewer: at least n entries reach it, or all do
-    auto bound_of = [&]() -> Key {
+    auto bound_of = [&](const uint4& best, int best_j, float m) -> Key {
         int at = 0;
 #pragma unroll
         for (int e = kN - 1; e >= 0; --e) at = element<T>(best, e) == m ? best_j + e : at;
@@ -275,31 +358,72 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     };
     auto value_bound = [&](Key tau) { return tau > 1 ? value_of((uint32_t)(tau >> 32)) : -INFINITY; };
 
+    // The sums are relative to the block's largest entry among the first turns.  Where a larger one comes, what was summed
+    // shrinks.
+    auto raise = [&](float top) {
+        const float by = fmaxf(m - top, least), f = ex2_(by * a.c);
+        D = (D + D2.x + D2.y + (S + S2.x + S2.y) * by) * f;
+        S = (S + S2.x + S2.y) * f;
+        S2 = D2 = make_float2(0.f, 0.f);
+        m = top;
+    };
+    auto ring = [&](int q, int x) { return *slot(q, x); };
     Key tau = 0;
     float bound = INFINITY;                                // nothing is collected without `top`
+    {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        uint4 best = edge;
+        int best_j = edge_j;
+        float top = largest(edge);
 #pragma unroll 1
-    for (int b = 0; b < batches; ++b) {
-        uint4 ahead_w[kBatch];
-        load(b + 1, ahead_w);
-        float top[kBatch];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            top[x] = largest(w[x]);
-            if (place(b, x) < nv) add(w[x], index_of(place(b, x)), top[x]);
-        }
-        if (a.top) {
-            if (b == 0) {
-                tau = bound_of();
-                bound = value_bound(tau);
+        for (int x = 0; x < kFirst && quarter; ++x) {
+            const uint4 w = ring(0, x);
+            const float y = largest(w);
+            if (y > top || !(top > -INFINITY)) {
+                best = w;
+                best_j = index_of(vector_of(0, x));
+                top = y;
             }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x)
-                if (top[x] >= bound && place(b, x) < nv) collect(w[x], index_of(place(b, x)), tau, bound);
         }
+        if (!(top > -INFINITY)) top = -INFINITY;
+        m = top;
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) w[x] = ahead_w[x];
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0 && aligned(s_max + warp, 4, 3)) s_max[warp] = m;
+        if (a.top) tau = bound_of(best, best_j, top);
+        else __syncthreads();
+        if (a.top) bound = value_bound(tau);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_max[w]);
+        __syncthreads();                                   // s_max is used again
     }
-    if (!batches && a.top) bound_of();                     // a block without a part: nothing is in its lists
+    float watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+    auto visit = [&](const uint4& w, int j) {
+        const float top = largest(w);
+        if (top >= watch) {                                // most vectors have nothing to be looked at
+            if (top > m) raise(top);
+            if (given && top >= zt) count(w, j);
+            if (top >= bound) collect(w, j, tau, bound);
+            watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+        }
+        const float ref = m == -INFINITY ? 0.f : -m;
+        add(w, make_float2(ref, ref));
+    };
+    if (has_edge) visit(edge, edge_j);
+#pragma unroll 1
+    for (int q = 0; q < quarter; ++q) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll 1
+        for (int x = 0; x < kFirst; ++x) {
+            const int v = vector_of(q, x);
+            if (there(v)) visit(ring(q, x), index_of(v));
+        }
+        copy(q + 2);
+        if ((q & 7) == 7) flush();
+    }
+    flush();
+    S += S2.x + S2.y;
+    D += D2.x + D2.y;
 
     // ---- the block's maximum, and its sums
     float mb = m;
@@ -332,13 +456,30 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
         if (n > kList) {
             // the first batch's bound let too many through (few entries there, or a rising row): the whole part's bound
             __syncthreads();
-            tau = bound_of();
+            uint4 best = edge;
+            int best_j = edge_j;
+            float top = largest(edge);
+#pragma unroll 1
+            for (int v = v0 + tid; v < v0 + nv; v += kThreads) {
+                if (!there(v)) continue;
+                const uint4 x = *reinterpret_cast<const uint4*>(z + index_of(v));
+                const float y = largest(x);
+                if (y > top || !(top > -INFINITY)) {
+                    best = x;
+                    best_j = index_of(v);
+                    top = y;
+                }
+            }
+            if (!(top > -INFINITY)) top = -INFINITY;
+            tau = bound_of(best, best_j, top);
             bound = value_bound(tau);
-            if (m >= bound) {
-#pragma unroll 2
-                for (int i = tid; i < nv; i += kThreads) {
-                    const uint4 x = vector(i);
-                    if (largest(x) >= bound) collect(x, index_of(i), tau, bound);
+            if (top >= bound) {
+                if (largest(edge) >= bound) collect(edge, edge_j, tau, bound);
+#pragma unroll 1
+                for (int v = v0 + tid; v < v0 + nv; v += kThreads) {
+                    if (!there(v)) continue;
+                    const uint4 x = *reinterpret_cast<const uint4*>(z + index_of(v));
+                    if (largest(x) >= bound) collect(x, index_of(v), tau, bound);
                 }
             }
             __syncthreads();
@@ -355,11 +496,14 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
             Key last = ~(Key)0;
             for (int k = 0; k < a.top; ++k) {
                 Key most = 0;
-                for (int i = tid; i < nv; i += kThreads) {
-                    const uint4 w = vector(i);
+#pragma unroll 1
+                for (int v = v0 + tid - kThreads; v < v0 + nv; v += kThreads) {
+                    const bool first = v < v0 + tid;       // the extra vector
+                    if (!first && !there(v)) continue;
+                    const uint4 w = first ? edge : *reinterpret_cast<const uint4*>(z + index_of(v));
 #pragma unroll
                     for (int e = 0; e < kN; ++e) {
-                        const Key x = key_of(element<T>(w, e), index_of(i) + e);
+                        const Key x = key_of(element<T>(w, e), (first ? edge_j : index_of(v)) + e);
                         if (x < last) most = max_key(most, x);
                     }
                 }
@@ -451,51 +595,52 @@ __global__ void __launch_bounds__(kThreads) k_score(const ScoreArgs a) {
     };
     if constexpr (!kCluster) {
         if (tid < a.top) put(tid, s_top[tid]);
-        return;
-    }
-    // keys of all blocks: the place in the own list, and how many of each other list are ahead
-    for (int i = tid; i < C * a.top; i += kThreads) {
-        const int r = i / a.top, k = i - r * a.top;
-        const Key x = s_all[r * kMaxTop + k];
-        if (!x) continue;
-        int place = k;
-        for (int q = 0; q < C && place < a.top; ++q) {
-            if (q == r) continue;
-            int lo = 0, hi = a.top;                        // sorted, falling
+    } else {
+        // keys of all blocks: the place in the own list, and how many of each other list are ahead
+        for (int i = tid; i < C * a.top; i += kThreads) {
+            const int r = i / a.top, k = i - r * a.top;
+            const Key x = s_all[r * kMaxTop + k];
+            if (!x) continue;
+            int place = k;
+            for (int q = 0; q < C && place < a.top; ++q) {
+                if (q == r) continue;
+                int lo = 0, hi = a.top;                        // sorted, falling
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_all[q * kMaxTop + mid] > x) lo = mid + 1;
+                    else hi = mid;
+                }
+                place += lo;
+            }
+            if (place < a.top) put(place, x);
+        }
+        // places that no entry takes
+        int have = 0;
+        for (int q = 0; q < C; ++q) {
+            int lo = 0, hi = a.top;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (s_all[q * kMaxTop + mid] > x) lo = mid + 1;
+                if (s_all[q * kMaxTop + mid]) lo = mid + 1;
                 else hi = mid;
             }
-            place += lo;
+            have += lo;
         }
-        if (place < a.top) put(place, x);
+        if (tid < a.top && tid >= have) put(tid, 0);
     }
-    // places that no entry takes
-    int have = 0;
-    for (int q = 0; q < C; ++q) {
-        int lo = 0, hi = a.top;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_all[q * kMaxTop + mid]) lo = mid + 1;
-            else hi = mid;
-        }
-        have += lo;
-    }
-    if (tid < a.top && tid >= have) put(tid, 0);
 }
 
 template <typename T, int kThreads, bool kCluster>
 cudaError_t launch_as(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
     auto kernel = k_score<T, kThreads, kCluster>;
-    if (!kCluster) return launch_k(kernel, dim3((unsigned)rows), dim3(kThreads), 0, st, a);
-    if (C > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr int kSmem = kStages * kThreads * 16;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (!kCluster) return launch_k(kernel, dim3((unsigned)rows), dim3(kThreads), kSmem, st, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)rows * C));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeClusterDimension;
