@@ -211,28 +211,50 @@ __device__ __forceinline__ int64_t pass_take(const RowArgs& a, int64_t lo, int64
     return before;
 }
 
-// ---- places in bit maps
+// ---- places in bit maps.  A block has kWords words of a map, a thread four of their pages; how many bits lie before them,
+// every block counts for itself.
 
-// The free list: what is left of the old one, then the pages of old rows that no new row names.  A block's part: words
-// [lo, hi) and the entries of the old list that fall to it.
-__device__ __forceinline__ void pass_release(const RowArgs& a, int64_t need, int64_t lo, int64_t hi, Team t, int64_t* s_sum) {
+constexpr int kThreads = 256, kWords = 32;                // threads of a block of a pass
+struct Words {
+    uint32_t word[kWords];
+    int64_t before[kWords];                                // bits before the word
+};
+// The block's words, `x` those of thread < kWords, with `at` bits before the first
+__device__ __forceinline__ void lay_words(Words& s, uint32_t x, int64_t at) {
+    if (threadIdx.x < kWords) {
+        int n = __popc(x);
+        const int own = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, n, o);
+            if ((int)threadIdx.x >= o) n += y;
+        }
+        s.word[threadIdx.x] = x;
+        s.before[threadIdx.x] = at + n - own;
+    }
+    __syncthreads();
+}
+
+// The free list: what is left of the old one, then the pages of old rows that no new row names.
+__device__ __forceinline__ void pass_release(const RowArgs& a, int64_t need, Team t, Words& s, int64_t* s_sum) {
     const int64_t taken = min(need, (int64_t)a.n_free), left = a.n_free - taken;
     for (int64_t i = t.thread; i < left; i += t.threads)
         if (i < a.n_pages) a.free_out[i] = a.free_list[taken + i];
-    auto word = [&](int64_t w) { return __ldcg(a.old_bits + w) & ~__ldcg(a.new_bits + w); };
+    auto word = [&](int64_t w) { return w < a.words ? __ldcg(a.old_bits + w) & ~__ldcg(a.new_bits + w) : 0u; };
+    const int64_t lo = (int64_t)blockIdx.x * kWords;
+    const uint32_t x = threadIdx.x < kWords ? word(lo + threadIdx.x) : 0;
     int64_t mine = 0, at;
-    for (int64_t w = threadIdx.x; w < lo; w += blockDim.x) mine += __popc(word(w));
+    for (int64_t w = threadIdx.x; w < lo; w += kThreads) mine += __popc(word(w));
     block_sum(mine, s_sum, &at);
     at += left;
-    for (int64_t w0 = lo; w0 < hi; w0 += blockDim.x) {
-        const int64_t w = w0 + threadIdx.x;
-        uint32_t x = w < hi ? word(w) : 0;
-        int64_t all, k = at + block_sum(__popc(x), s_sum, &all) - __popc(x);
-        for (; x; x &= x - 1, ++k)
-            if (k < a.n_pages) a.free_out[k] = (int32_t)(w * 32 + __ffs(x) - 1);
-        at += all;
+    lay_words(s, x, at);
+    for (int i = threadIdx.x; i < kWords * 32; i += kThreads) {
+        const uint32_t bits = s.word[i >> 5];
+        const int64_t k = s.before[i >> 5] + __popc(bits & ((1u << (i & 31)) - 1));
+        if (((bits >> (i & 31)) & 1) && k < a.n_pages) a.free_out[k] = (int32_t)(lo * 32 + i);
     }
-    if (hi == a.words && threadIdx.x == 0) {
+    if (lo + kWords >= a.words && threadIdx.x == 0) {
+        at = s.before[kWords - 1] + __popc(s.word[kWords - 1]);
         a.info[0] = (int32_t)taken;
         a.info[1] = (int32_t)min(at, (int64_t)a.n_pages);
         a.info[2] = __ldcg(a.word + W_FLAGS) | (need > a.n_free ? BIT_FREE : 0);
@@ -240,51 +262,41 @@ __device__ __forceinline__ void pass_release(const RowArgs& a, int64_t need, int
     }
 }
 
-// Pages in use: all, and below word `w` ( < words ) of the map
-__device__ __forceinline__ int64_t count_live(const RowArgs& a, int64_t w, int64_t* below, int64_t* s_sum) {
-    int64_t all = 0, low = 0, total;
-    for (int64_t x = threadIdx.x; x < a.words; x += blockDim.x) {
-        const int n = __popc(__ldcg(a.old_bits + x));
+// Where pages move
+__device__ __forceinline__ void pass_places(const RowArgs& a, Team t, Words& s, int64_t* s_sum) {
+    const int64_t lo = (int64_t)blockIdx.x * kWords;
+    const uint32_t x = threadIdx.x < kWords && lo + threadIdx.x < a.words ? __ldcg(a.old_bits + lo + threadIdx.x) : 0;
+    int64_t all = 0, low = 0, live, at;
+    for (int64_t w = threadIdx.x; w < a.words; w += kThreads) {
+        const int n = __popc(__ldcg(a.old_bits + w));
         all += n;
-        if (x < w) low += n;
+        if (w < lo) low += n;
     }
-    block_sum(all, s_sum, &total);
-    block_sum(low, s_sum, below);
-    return total;
-}
-
-// Where pages move: words [lo, hi) of the map, one block's
-__device__ __forceinline__ void pass_places(const RowArgs& a, int64_t lo, int64_t hi, Team t, int64_t* s_sum) {
-    int64_t at;                                            // pages in use before the word
-    const int64_t live = count_live(a, lo, &at, s_sum);
+    block_sum(all, s_sum, &live);
+    block_sum(low, s_sum, &at);
     // pages in use below `live`, which stay
     int64_t mine = 0, stay;
-    for (int64_t x = threadIdx.x; x <= live >> 5 && x < a.words; x += blockDim.x)
-        mine += __popc(__ldcg(a.old_bits + x) & (x < live >> 5 ? 0xffffffffu : (1u << (live & 31)) - 1));
+    for (int64_t w = threadIdx.x; w <= live >> 5 && w < a.words; w += kThreads)
+        mine += __popc(__ldcg(a.old_bits + w) & (w < live >> 5 ? 0xffffffffu : (1u << (live & 31)) - 1));
     block_sum(mine, s_sum, &stay);
-    for (int64_t w0 = lo; w0 < hi; w0 += blockDim.x) {
-        const int64_t w = w0 + threadIdx.x;
-        const uint32_t x = w < hi ? __ldcg(a.old_bits + w) : 0;
-        int64_t all, k = at + block_sum(__popc(x), s_sum, &all) - __popc(x);
-        at += all;
-        if (w >= hi) continue;
-        for (int b = 0; b < 32; ++b) {
-            const int64_t id = w * 32 + b;
-            if (id >= a.n_pages) break;
-            if ((x >> b) & 1) {
-                if (id >= live) {                          // the (k - stay)-th that moves
-                    a.place[id] = (int32_t)(k - stay);
-                    a.copies[3 * (k - stay)] = (int32_t)id;
-                    a.copies[3 * (k - stay) + 2] = (int32_t)a.ps;
-                }
-                ++k;
-            } else if (id < live) {
-                a.copies[3 * (id - k) + 1] = (int32_t)id;  // the (id - k)-th that is free
+    lay_words(s, x, at);
+    for (int i = threadIdx.x; i < kWords * 32; i += kThreads) {
+        const int64_t id = lo * 32 + i;
+        if (id >= a.n_pages) break;
+        const uint32_t bits = s.word[i >> 5];
+        const int64_t k = s.before[i >> 5] + __popc(bits & ((1u << (i & 31)) - 1));
+        if ((bits >> (i & 31)) & 1) {
+            if (id >= live) {                              // the (k - stay)-th that moves
+                a.place[id] = (int32_t)(k - stay);
+                a.copies[3 * (k - stay)] = (int32_t)id;
+                a.copies[3 * (k - stay) + 2] = (int32_t)a.ps;
             }
+        } else if (id < live) {
+            a.copies[3 * (id - k) + 1] = (int32_t)id;      // the (id - k)-th that is free
         }
+        if (id >= live) a.free_out[id - live] = (int32_t)id;
     }
-    for (int64_t i = t.thread; i < a.n_pages - live; i += t.threads) a.free_out[i] = (int32_t)(live + i);
-    if (hi == a.words && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.info[0] = (int32_t)(live - stay);
         a.info[1] = (int32_t)(a.n_pages - live);
         a.info[2] = __ldcg(a.word + W_FLAGS);
@@ -321,7 +333,7 @@ __device__ __forceinline__ void pass_rename(const RowArgs& a, Team t, int64_t li
 
 // ---- kernels
 
-constexpr int kThreads = 256, kOne = 1024;                 // of a block of a pass; of the block that does all of them
+constexpr int kOne = 1024;                                 // threads of the block that does all passes
 
 __device__ __forceinline__ Team grid_team() {
     return {blockIdx.x * (int64_t)blockDim.x + threadIdx.x, gridDim.x * (int64_t)blockDim.x};
@@ -352,54 +364,243 @@ __global__ void __launch_bounds__(kThreads) k_fork_fill(const RowArgs a, int tak
 }
 __global__ void __launch_bounds__(kThreads) k_fork_release(const RowArgs a) {
     __shared__ int64_t s_sum[kThreads / 32];
+    __shared__ Words s;
     pdl_trigger();
     pdl_wait();
-    const int64_t lo = (int64_t)blockIdx.x * kThreads, hi = min(lo + kThreads, (int64_t)a.words);
-    pass_release(a, __ldcg(reinterpret_cast<const long long*>(a.word + 2)), lo, hi, grid_team(), s_sum);
+    pass_release(a, __ldcg(reinterpret_cast<const long long*>(a.word + 2)), grid_team(), s, s_sum);
 }
 __global__ void __launch_bounds__(kThreads) k_compact_places(const RowArgs a) {
     __shared__ int64_t s_sum[kThreads / 32];
+    __shared__ Words s;
     pdl_trigger();
     pdl_wait();
-    const int64_t lo = (int64_t)blockIdx.x * kThreads, hi = min(lo + kThreads, (int64_t)a.words);
-    pass_places(a, lo, hi, grid_team(), s_sum);
+    pass_places(a, grid_team(), s, s_sum);
 }
 __global__ void __launch_bounds__(kThreads) k_compact_rename(const RowArgs a) {
     pdl_trigger();
     pdl_wait();
     pass_rename(a, grid_team(), __ldcg(a.info + 3));
 }
-__global__ void __launch_bounds__(kOne) k_fork_one(const RowArgs a) {
-    __shared__ int64_t s_sum[kOne / 32];
-    pdl_trigger();
-    pdl_wait();
-    const Team t = {threadIdx.x, kOne};
-    pass_clear(a, t);
+// ---- all passes in one block: counts, bits and lowest rows in shared memory, so that the only things waited for in turn are
+// lengths and parents, table entries, and the free list
+
+constexpr int kOneRows = 2048, kOnePages = 4096;           // old and new rows; pages
+struct One {
+    uint32_t old_bits[kOnePages / 32], new_bits[kOnePages / 32];
+    int32_t ref[kOnePages], sum[kOne / 32], flags, longest;
+};
+
+// Inclusive sum over the block's threads; *total of all
+__device__ __forceinline__ int32_t one_sum(int32_t x, int32_t* s_sum, int32_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
     __syncthreads();
-    pass_mark(a, t);
+    if (lane == 31) s_sum[warp] = x;
     __syncthreads();
-    const int64_t need = pass_take(a, 0, a.N, s_sum);
-    pass_fill(a, t);
-    __syncthreads();
-    pass_release(a, need, 0, a.words, t, s_sum);
+    int32_t y = s_sum[lane];                               // as many warps as lanes
+    const int32_t own = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    *total = __shfl_sync(0xffffffffu, y, 31);
+    return x + __shfl_sync(0xffffffffu, y - own, warp);
 }
-__global__ void __launch_bounds__(kOne) k_compact_one(const RowArgs a) {
-    __shared__ int64_t s_sum[kOne / 32];
+static_assert(kOne == 1024, "as many warps as lanes");
+
+// Bits of the pages that the rows name, from a warp for each 256 entries
+__device__ __forceinline__ void one_mark(const RowArgs& a, One& s, const int32_t* s_len) {
+    const int lane = threadIdx.x & 31;
+    const int chunks = (a.width + kChunk - 1) / kChunk;
+    for (int w = threadIdx.x >> 5; w < a.R * chunks; w += kOne / 32) {
+        const int r = w / chunks, c = (w - r * chunks) * kChunk;
+        const Row row = row_of(a, s_len[r]);
+        int32_t flags = c == 0 ? row.flags : 0;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int j = c + e * 32 + lane;
+            if (j >= row.used) break;
+            const int32_t id = a.table[(int64_t)r * a.width + j];
+            if ((uint32_t)id < (uint32_t)a.n_pages) atomicOr(s.old_bits + (id >> 5), 1u << (id & 31));
+            else flags |= BIT_ID;
+        }
+        if (flags) atomicOr(&s.flags, flags);
+    }
+}
+__device__ __forceinline__ void one_clear(const RowArgs& a, One& s) {
+    for (int i = threadIdx.x; i < a.n_pages; i += kOne) s.ref[i] = 0;
+    for (int i = threadIdx.x; i < kOnePages / 32; i += kOne) s.old_bits[i] = s.new_bits[i] = 0;
+    if (threadIdx.x == 0) s.flags = s.longest = 0;
+}
+
+__global__ void __launch_bounds__(kOne) k_fork_one(const RowArgs a) {
+    __shared__ One s;
+    extern __shared__ int32_t s_rows[];                    // [R] lengths, [R] lowest new rows
+    int32_t *s_len = s_rows, *s_first = s_rows + a.R;
     pdl_trigger();
     pdl_wait();
-    const Team t = {threadIdx.x, kOne};
-    pass_clear(a, t);
+    const int tid = threadIdx.x, lane = tid & 31;
+    int32_t parent[kOneRows / kOne];
+#pragma unroll
+    for (int x = 0; x < kOneRows / kOne; ++x) parent[x] = tid + x * kOne < a.N ? parent_of(a, tid + x * kOne) : -1;
+    for (int i = tid; i < a.R; i += kOne) {
+        s_len[i] = a.len[i];
+        s_first[i] = INT32_MAX;
+    }
+    one_clear(a, s);
     __syncthreads();
-    pass_mark(a, t);
+#pragma unroll
+    for (int x = 0; x < kOneRows / kOne; ++x)
+        if (parent[x] >= 0) atomicMin(s_first + parent[x], tid + x * kOne);
+    one_mark(a, s, s_len);
     __syncthreads();
-    pass_places(a, 0, a.words, t, s_sum);
+    // ---- lengths, and the pages taken anew
+    int32_t need_all = 0;
+#pragma unroll
+    for (int x = 0; x < kOneRows / kOne; ++x) {
+        if (x * kOne >= a.N) break;
+        const int i = tid + x * kOne, p = parent[x];
+        Row row = {};
+        if (p >= 0) row = row_of(a, s_len[p]);
+        const bool need = row.rest > 0 && s_first[p] != i;
+        int32_t all;
+        const int32_t k = need_all + one_sum(need, s.sum, &all) - need;
+        need_all += all;
+        if (need) {
+            const bool have = k < a.n_free;
+            int32_t page = have ? a.free_list[k] : -1, from = a.table[(int64_t)p * a.width + row.full];
+            if (have && (uint32_t)page >= (uint32_t)a.n_pages) {
+                page = -1;
+                atomicOr(&s.flags, BIT_ID);
+            }
+            if ((uint32_t)from >= (uint32_t)a.n_pages) from = -1;
+            a.out[(int64_t)i * a.width + row.full] = page;
+            if (page >= 0) {
+                atomicAdd(s.ref + page, 1);
+                atomicOr(s.new_bits + (page >> 5), 1u << (page & 31));
+            } else {
+                row.len -= row.rest;
+            }
+            if (have) {
+                a.copies[3 * k] = from;
+                a.copies[3 * k + 1] = page;
+                a.copies[3 * k + 2] = row.rest;
+            }
+        }
+        if (i < a.N) a.len_out[i] = row.len;
+        if (row.len) atomicMax(&s.longest, row.len);
+    }
+    // ---- the new rows but for those pages
+    const int chunks = (a.width + kChunk - 1) / kChunk;
+    for (int w = tid >> 5; w < a.N * chunks; w += kOne / 32) {
+        const int i = w / chunks, c = (w - i * chunks) * kChunk;
+        const int32_t p = parent_of(a, i);
+        Row row = {};
+        bool fresh = false;
+        if (p >= 0) {
+            row = row_of(a, s_len[p]);
+            fresh = row.rest > 0 && s_first[p] != i;
+        }
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int j = c + e * 32 + lane;
+            if (j >= a.width) break;
+            if (fresh && j == row.full) continue;
+            int32_t id = j < row.used ? a.table[(int64_t)p * a.width + j] : -1;
+            if ((uint32_t)id >= (uint32_t)a.n_pages) id = -1;
+            a.out[(int64_t)i * a.width + j] = id;
+            if (id >= 0) {
+                atomicAdd(s.ref + id, 1);
+                atomicOr(s.new_bits + (id >> 5), 1u << (id & 31));
+            }
+        }
+    }
     __syncthreads();
-    pass_rename(a, t, __ldcg(a.info + 3));
+    // ---- counts and the free list
+    const int taken = min(need_all, a.n_free), left = a.n_free - taken;
+    for (int i = tid; i < a.n_pages; i += kOne) a.ref[i] = s.ref[i];
+    for (int i = tid; i < min(left, a.n_pages); i += kOne) a.free_out[i] = a.free_list[taken + i];
+    const uint32_t back = tid < kOnePages / 32 ? s.old_bits[tid] & ~s.new_bits[tid] : 0;
+    int32_t all;
+    int32_t k = left + one_sum(__popc(back), s.sum, &all) - __popc(back);
+    for (uint32_t x = back; x; x &= x - 1, ++k)
+        if (k < a.n_pages) a.free_out[k] = tid * 32 + __ffs(x) - 1;
+    if (tid == 0) {
+        a.info[0] = taken;
+        a.info[1] = min(left + all, a.n_pages);
+        a.info[2] = s.flags | (need_all > a.n_free ? BIT_FREE : 0);
+        a.info[3] = s.longest;
+    }
+}
+
+__global__ void __launch_bounds__(kOne) k_compact_one(const RowArgs a) {
+    __shared__ One s;
+    __shared__ int32_t s_before[kOnePages / 32];           // pages in use before a word
+    extern __shared__ int32_t s_rows[];                    // [R] lengths, [n_pages / 2] where pages move
+    int32_t *s_len = s_rows, *s_to = s_rows + a.R;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < a.R; i += kOne) s_len[i] = a.len[i];
+    one_clear(a, s);
+    __syncthreads();
+    one_mark(a, s, s_len);
+    __syncthreads();
+    const uint32_t word = tid < kOnePages / 32 ? s.old_bits[tid] : 0;
+    int32_t live;
+    const int32_t before = one_sum(__popc(word), s.sum, &live) - __popc(word);
+    if (tid < kOnePages / 32) s_before[tid] = before;
+    __syncthreads();
+    // pages in use below id
+    auto rank = [&](int id) { return s_before[id >> 5] + __popc(s.old_bits[id >> 5] & ((1u << (id & 31)) - 1)); };
+    const int32_t stay = live < kOnePages ? rank(live) : live;             // in use below `live`
+    for (int id = tid; id < a.n_pages; id += kOne) {
+        const bool used = (s.old_bits[id >> 5] >> (id & 31)) & 1;
+        if (used && id >= live) {                          // the k-th that moves
+            const int k = rank(id) - stay;
+            a.copies[3 * k] = id;
+            a.copies[3 * k + 2] = (int32_t)a.ps;
+        } else if (!used && id < live) {                   // the k-th that is free
+            const int k = id - rank(id);
+            a.copies[3 * k + 1] = id;
+            s_to[k] = id;
+        }
+        if (id >= live) a.free_out[id - live] = id;
+    }
+    __syncthreads();
+    const int chunks = (a.width + kChunk - 1) / kChunk;
+    for (int w = tid >> 5; w < a.R * chunks; w += kOne / 32) {
+        const int r = w / chunks, c = (w - r * chunks) * kChunk;
+        const Row row = row_of(a, s_len[r]);
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int j = c + e * 32 + lane;
+            if (j >= a.width) break;
+            int32_t id = j < row.used ? a.table[(int64_t)r * a.width + j] : -1;
+            if ((uint32_t)id >= (uint32_t)a.n_pages) id = -1;
+            if (id >= live) id = s_to[rank(id) - stay];
+            a.out[(int64_t)r * a.width + j] = id;
+            if (id >= 0) atomicAdd(s.ref + id, 1);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < a.n_pages; i += kOne) a.ref[i] = s.ref[i];
+    if (tid == 0) {
+        a.info[0] = live - stay;
+        a.info[1] = a.n_pages - live;
+        a.info[2] = s.flags;
+        a.info[3] = live;
+    }
 }
 
 // One block does all passes where each of its threads has a few entries.
 bool one_block(const RowArgs& a) {
-    return ((int64_t)a.R + a.N) * a.width <= 8 * kOne && a.n_pages <= 8 * kOne && a.n_free <= 8 * kOne && a.N <= 2 * kOne;
+    return ((int64_t)a.R + a.N) * a.width <= 8 * kOne && a.n_pages <= kOnePages && a.n_free <= kOnePages && a.N <= kOneRows && a.R <= kOneRows;
 }
 int blocks_for(int64_t items, int64_t each) { return (int)std::min<int64_t>(std::max<int64_t>((items + each - 1) / each, 1), 2048); }
 
@@ -458,7 +659,7 @@ int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (one_block(a)) {
-        e = launch_k(k_fork_one, dim3(1), dim3(kOne), 0, st, a);
+        e = launch_k(k_fork_one, dim3(1), dim3(kOne), sizeof(int32_t) * 2 * a.R, st, a);
     } else {
         const int64_t chunks = ((int64_t)a.width + kChunk - 1) / kChunk;
         const int takers = std::max((N + kThreads - 1) / kThreads, 1);
@@ -468,7 +669,7 @@ int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* 
         if (e == cudaSuccess)
             e = launch_k(k_fork_fill, dim3(takers + blocks_for(N * chunks, kThreads / 32)), dim3(kThreads), 0, st, a, takers);
         if (e == cudaSuccess)
-            e = launch_k(k_fork_release, dim3((a.words + kThreads - 1) / kThreads), dim3(kThreads), 0, st, a);
+            e = launch_k(k_fork_release, dim3((a.words + kWords - 1) / kWords), dim3(kThreads), 0, st, a);
     }
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
     return SD_OK;
@@ -493,13 +694,13 @@ int sd_page_compact(const int32_t* table_dev, int32_t table_stride, const int32_
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (one_block(a)) {
-        e = launch_k(k_compact_one, dim3(1), dim3(kOne), 0, st, a);
+        e = launch_k(k_compact_one, dim3(1), dim3(kOne), sizeof(int32_t) * (a.R + a.n_pages / 2), st, a);
     } else {
         const int64_t chunks = ((int64_t)a.width + kChunk - 1) / kChunk;
         e = launch_k(k_rows_clear, dim3(blocks_for(a.n_pages, 4 * kThreads)), dim3(kThreads), 0, st, a);
         if (e == cudaSuccess) e = launch_k(k_rows_mark, dim3(blocks_for(R * chunks, kThreads / 32)), dim3(kThreads), 0, st, a);
         if (e == cudaSuccess)
-            e = launch_k(k_compact_places, dim3((a.words + kThreads - 1) / kThreads), dim3(kThreads), 0, st, a);
+            e = launch_k(k_compact_places, dim3((a.words + kWords - 1) / kWords), dim3(kThreads), 0, st, a);
         if (e == cudaSuccess) e = launch_k(k_compact_rename, dim3(blocks_for(R * chunks, kThreads / 32)), dim3(kThreads), 0, st, a);
     }
     if (e != cudaSuccess) return op_fail(SD_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
