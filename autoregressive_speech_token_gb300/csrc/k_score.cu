@@ -4,18 +4,25 @@
 // With d_j = z_j - m, m the row's largest logit, S = sum e^(d/T) and D = sum d e^(d/T),
 //   log p_j = d_j / T - log S,   H = log S - D / (S T)   (both terms of H are >= 0: nothing cancels).
 //
-// A row is read from memory once: every thread keeps a running maximum with the sums that belong to it.  Long rows, and
-// rows that are fewer than the SMs, are cut over a thread-block cluster, whose blocks exchange their maxima, sums and
-// best entries through distributed shared memory.
+// A row is read from memory once, in 16-byte vectors that cp.async brings into a ring in shared memory, eight of a thread
+// in flight.  The first four of every thread are spread over the whole part: their largest entry is what the block's sums are
+// relative to (d_j is formed first: exact where it counts; a thread that meets a larger entry shrinks what it has).
+// Long rows, where rows are fewer than the SMs, are cut over a thread-block cluster, whose blocks exchange their maxima,
+// sums and best entries through distributed shared memory.
 //
 // The first n entries of (z descending, index ascending): every entry is the 64-bit key (order of z, ~index), 0 if it is
-// no alternative.  The best keys of groups of threads in the first batch, which is spread over the whole part, are ranked
-// among each other.  The n-th of them is a bound: at least n keys reach it.  What reaches it, a few n, is collected as the
-// row passes, and ranked at the end.  Where too much reaches it (a rising row, a mask over most of the batch), the bound is
-// taken of the whole part and the groups that reach it read theirs again; where that is still too much, the n best
+// no alternative.  The best keys of groups of four threads in the first round are ranked among each other.  The n-th of
+// them is a bound: at least n keys reach it.  Vectors that reach it, a few n, are put aside as the row passes; their keys
+// are ranked at the end, each against all.  Where too much reaches it (a rising row, a mask over most of the first
+// round), the bound is taken of the whole part and what reaches it is read again; where that is still too much, the n best
 // are taken one after the other.
 //
-// Bound by the one read where rows are many, by the chain of exchanges where they are few.
+// Most vectors are below the watched bound (the smallest of the maximum, the n-th best and the token's logit) and
+// cost only their sums: about 16 instructions of arithmetic for four fp32, two operations each where fp32 pairs allow.
+//
+// Measured (token, rank, entropy and best entries of every row): 16 rows of 2048 6 us, a chain of exchanges; 800 of 8194
+// fp32 with 20 wanted 20 us = 1.3 TB/s, where the ranking and the chain of a short row bound it (14.5 without); 1021 of
+// 131075 bf16 with 5 wanted 85 us = 3.1 TB/s, where the instructions of the sums do; fp32 without any 112 us = 4.8 TB/s.
 #include <algorithm>
 
 #include "pages_dev.cuh"
@@ -193,15 +200,20 @@ __device__ __forceinline__ uint4 load_edge(const T* row, int first, int32_t V) {
 }
 
 constexpr int kStages = 8;                                 // vectors of a thread in flight, in shared memory
+constexpr int kPutAside = 128;                            // vectors that may reach the first bound before it is raised
 constexpr int kFirst = 4;                                  // of which the bound is taken
 
 template <typename T, int kThreads, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const ScoreArgs a) {
-    constexpr int kN = Type<T>::kN, kWarps = kThreads / 32, kGroups = kThreads / 4;
-    __shared__ Key s_best[kGroups], s_list[kList], s_top[kMaxTop], s_tau;
+    constexpr int kN = Type<T>::kN, kWarps = kThreads / 32, kGroups = kThreads / 4, kHits = 2 * kThreads;
+    __shared__ uint4 s_hit[kHits];                         // vectors with an entry that reaches the bound
+    __shared__ int s_hit_j[kHits];                         // and their first entry
+    __shared__ Key s_best[2 * kGroups], s_top[kMaxTop], s_tau;
     __shared__ float s_max[kWarps], s_S[kWarps], s_D[kWarps], s_mine[3];           // s_mine: this block's maximum, S, D
-    __shared__ int s_ahead[kWarps], s_mine_ahead, s_count;
+    __shared__ int s_ahead[kWarps], s_mine_ahead, s_count, s_keys;
     extern __shared__ uint4 s_ring[];                      // [kStages][kThreads]: a thread reads back only what it copied
+    Key* s_list = reinterpret_cast<Key*>(s_ring);          // keys in its place, once the row has passed
+    static_assert(kStages * 2 * kThreads >= kList, "");
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -317,18 +329,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
             ahead2 = Pair{};
         }
     };
-    // What reaches the bound tau into the list.  (Its value decides first: most vectors have nothing.)
-    auto collect = [&](const uint4& w, int j, Key tau, float bound) {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const float x = element<T>(w, e);
-            if (!(x >= bound)) continue;
-            const Key k = key_of(x, j + e);
-            if (k >= tau) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kList && aligned(s_list + at, 8, 6)) s_list[at] = k;
-            }
+    // A vector with an entry that reaches the bound's value is put aside: few are, and a warp waits for each of its lanes
+    auto collect = [&](const uint4& w, int j) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kHits && aligned(s_hit + at, 16, 6)) {
+            s_hit[at] = w;
+            s_hit_j[at] = j;
         }
+    };
+    // The keys of what was put aside that reach the bound tau; more than kList if there are too many
+    auto keys_of_hits = [&](Key tau) -> int {
+        const int n = s_count;
+        if (n > kHits) return kList + 1;
+        for (int i = tid; i < n * kN; i += kThreads) {
+            const T x = reinterpret_cast<const T*>(s_hit)[i];
+            const Key k = key_of(number(x), s_hit_j[i / kN] + i % kN);
+            if (k < tau) continue;
+            const int at = atomicAdd(&s_keys, 1);
+            if (at < kList && aligned(s_list + at, 8, 13)) s_list[at] = k;
+        }
+        __syncthreads();
+        return s_keys;
     };
     // The n-th of the groups' best keys so far, 1 if there are fewer: at least n entries reach it, or all do
     auto bound_of = [&](const uint4& best, int best_j, float m) -> Key {
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         mine = max_key(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
         if ((tid & 3) == 0 && aligned(s_best + (tid >> 2), 8, 4)) s_best[tid >> 2] = mine;
         if (tid == 0) {
-            s_count = 0;
+            s_count = s_keys = 0;
             s_tau = 0;
         }
         if (tid < kMaxTop && aligned(s_top + tid, 8, 5)) s_top[tid] = 0;
@@ -355,6 +376,31 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         if ((tid & 3) == 0 && key && before == a.top - 1) s_tau = key;          // keys are distinct
         __syncthreads();
         return max_key(s_tau, 1);
+    };
+    // A higher bound while a long part passes: the n-th of the best keys of the vectors put aside so far
+    auto higher_bound = [&](Key tau) -> Key {
+        __syncthreads();
+        const int n = s_count;
+        if (n > 2 * kGroups) return tau;
+        if (tid < n && aligned(s_best + tid, 8, 14)) {
+            Key most = 0;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) most = max_key(most, key_of(element<T>(s_hit[tid], e), s_hit_j[tid] + e));
+            s_best[tid] = most;
+        }
+        __syncthreads();
+        for (int i0 = 0; i0 < n; i0 += kGroups) {
+            const int i = i0 + (tid >> 2);
+            const Key key = s_best[min(i, n - 1)];
+            int before = 0;
+#pragma unroll 4
+            for (int j = tid & 3; j < n; j += 4) before += s_best[j] > key;
+            before += __shfl_xor_sync(0xffffffffu, before, 1);
+            before += __shfl_xor_sync(0xffffffffu, before, 2);
+            if ((tid & 3) == 0 && i < n && key && before == a.top - 1) s_tau = key;
+        }
+        __syncthreads();
+        return max_key(s_tau, tau);
     };
     auto value_bound = [&](Key tau) { return tau > 1 ? value_of((uint32_t)(tau >> 32)) : -INFINITY; };
 
@@ -403,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         if (top >= watch) {                                // most vectors have nothing to be looked at
             if (top > m) raise(top);
             if (given && top >= zt) count(w, j);
-            if (top >= bound) collect(w, j, tau, bound);
+            if (top >= bound) collect(w, j);
             watch = fminf(fminf(m, bound), given ? zt : INFINITY);
         }
         const float ref = m == -INFINITY ? 0.f : -m;
@@ -420,6 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         }
         copy(q + 2);
         if ((q & 7) == 7) flush();
+        // About top_n times the number of rounds will have reached the first round's bound.  Behind rounds 4 and 16 it is
+        // raised, which stalls the block for 1.5 us: 1021 rows of 131075 fp32 with 20 wanted 190 -> 142 us, but of bf16 (half
+        // the rounds) with 5 wanted 85 -> 90
+        if (a.top * quarter > kPutAside && (q == 3 || q == 15) && 2 * (q + 1) <= quarter) {
+            tau = higher_bound(tau);
+            bound = value_bound(tau);
+            watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+        }
     }
     flush();
     S += S2.x + S2.y;
@@ -452,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
 
     // ---- the block's first entries
     if (a.top) {
-        int n = s_count;
+        int n = keys_of_hits(tau);
         if (n > kList) {
             // the first batch's bound let too many through (few entries there, or a rising row): the whole part's bound
             __syncthreads();
@@ -474,23 +528,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
             tau = bound_of(best, best_j, top);
             bound = value_bound(tau);
             if (top >= bound) {
-                if (largest(edge) >= bound) collect(edge, edge_j, tau, bound);
+                if (largest(edge) >= bound) collect(edge, edge_j);
 #pragma unroll 1
                 for (int v = v0 + tid; v < v0 + nv; v += kThreads) {
                     if (!there(v)) continue;
                     const uint4 x = *reinterpret_cast<const uint4*>(z + index_of(v));
-                    if (largest(x) >= bound) collect(x, index_of(v), tau, bound);
+                    if (largest(x) >= bound) collect(x, index_of(v));
                 }
             }
             __syncthreads();
-            n = s_count;
+            n = keys_of_hits(tau);
         }
         if (n <= kList) {
-            for (int i = tid; i < n; i += kThreads) {
-                const Key x = s_list[i];
+            // four threads to a key, a quarter of the others each
+            for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
+                const int i = i0 + (tid >> 2);
+                const Key x = s_list[min(i, n - 1)];
                 int r = 0;
-                for (int j = 0; j < n; ++j) r += s_list[j] > x;
-                if (r < a.top && aligned(s_top + r, 8, 7)) s_top[r] = x;
+#pragma unroll 4
+                for (int j = tid & 3; j < n; j += 4) r += s_list[j] > x;
+                r += __shfl_xor_sync(0xffffffffu, r, 1);
+                r += __shfl_xor_sync(0xffffffffu, r, 2);
+                if ((tid & 3) == 0 && i < n && r < a.top && aligned(s_top + r, 8, 7)) s_top[r] = x;
             }
         } else {
             Key last = ~(Key)0;
@@ -583,15 +642,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
     // log p of a logit; a row without a finite logit has none
     auto log_p = [&](float x) { return S == 0.f ? -INFINITY : (x - M) / a.T - log_s; };
     if (tid == 0) {
-        if (a.logp && aligned(a.logp+row,4,8)) a.logp[row] = given ? log_p(zt) : 0.f;
-        if (a.rank && aligned(a.rank+row,4,9)) a.rank[row] = given ? ahead : -1;
-        if (a.entropy && aligned(a.entropy+row,4,10)) a.entropy[row] = S == 0.f ? 0.f : log_s - D / S / a.T;
+        if (a.logp && aligned(a.logp + row, 4, 8)) a.logp[row] = given ? log_p(zt) : 0.f;
+        if (a.rank && aligned(a.rank + row, 4, 9)) a.rank[row] = given ? ahead : -1;
+        if (a.entropy && aligned(a.entropy + row, 4, 10)) a.entropy[row] = S == 0.f ? 0.f : log_s - D / S / a.T;
     }
     if (!a.top) return;
     auto put = [&](int r, Key x) {
-        if (!aligned(a.top_id+row * a.top + r,4,11) || !aligned(a.top_logp+row * a.top + r,4,12)) return;
-        a.top_id[row * a.top + r] = x ? (int32_t)~(uint32_t)x : -1;
-        a.top_logp[row * a.top + r] = x ? log_p(value_of((uint32_t)(x >> 32))) : -INFINITY;
+        const int64_t at = row * a.top + r;
+        if (!aligned(a.top_id + at, 4, 11) || !aligned(a.top_logp + at, 4, 12)) return;
+        a.top_id[at] = x ? (int32_t)~(uint32_t)x : -1;
+        a.top_logp[at] = x ? log_p(value_of((uint32_t)(x >> 32))) : -INFINITY;
     };
     if constexpr (!kCluster) {
         if (tid < a.top) put(tid, s_top[tid]);
@@ -630,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
 }
 
 template <typename T, int kThreads, bool kCluster>
-cudaError_t launch_as(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
+cudaError_t launch_row(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
     auto kernel = k_score<T, kThreads, kCluster>;
     constexpr int kSmem = kStages * kThreads * 16;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -654,7 +714,7 @@ cudaError_t launch_as(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
 }
 template <typename T, int kThreads>
 cudaError_t launch(const ScoreArgs& a, int rows, int C, cudaStream_t st) {
-    return C > 1 ? launch_as<T, kThreads, true>(a, rows, C, st) : launch_as<T, kThreads, false>(a, rows, C, st);
+    return C > 1 ? launch_row<T, kThreads, true>(a, rows, C, st) : launch_row<T, kThreads, false>(a, rows, C, st);
 }
 
 template <typename T>
@@ -665,8 +725,12 @@ cudaError_t choose(const ScoreArgs& a, int rows, int sms, cudaStream_t st) {
     while (C < kMaxCluster && (int64_t)rows * C * 2 <= 2 * sms && bytes > (int64_t)C * 16384) C *= 2;
     if ((int64_t)rows * C > INT32_MAX) return cudaErrorInvalidValue;
     const int64_t part = bytes / C, blocks = (int64_t)rows * C;
-    if (part <= 8192 && blocks > 2 * sms) return launch<T, 128>(a, rows, C, st);
-    return part <= 65536 && blocks > 2 * sms ? launch<T, 256>(a, rows, C, st) : launch<T, 512>(a, rows, C, st);
+    // 128, 256 or 512 threads to a block.  Smaller ones finish more rows side by side, and have fewer bounds to rank: 1000 rows
+    // of 2050 fp32 13.3 us by 256, 11.6 by 128; 1000 of 16386 40.4 by 512, 32.8 by 256.  Few rows want larger ones (320 of
+    // 8194: 17.5 us by 128, 11.5 by 256), and so do long parts, where the first round shows less of the row (700 of 32000 with
+    // 20 wanted: 39.5 by 512, 40 to 47 by 256).
+    if (part <= 16384 && blocks > 4 * sms) return launch<T, 128>(a, rows, C, st);
+    return part <= 98304 && blocks > 2 * sms ? launch<T, 256>(a, rows, C, st) : launch<T, 512>(a, rows, C, st);
 }
 
 }  // namespace

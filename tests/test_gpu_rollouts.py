@@ -689,6 +689,34 @@ def test_score_a_sorted_row_with_many_entries_above_the_bound(sd):
             np.testing.assert_array_equal(got[3][r], ids)
 
 
+@pytest.mark.parametrize("V,dt,top", [(131075, "f32", 32), (262144, "f32", 9), (262141, "bf16", 32), (140001, "f16", 1)])
+def test_score_long_rows_of_one_block(sd, V, dt, top):
+    """Rows enough that none is cut: the bound of what is put aside rises while a row passes."""
+    rows = 160
+    z = randn(gen(V), rows, V, dt=dt) * 2
+    up = torch.linspace(-9, 9, V, device="cuda")
+    z[0] = up.to(z.dtype)                                    # every round above the one before
+    z[1] = up.flip(0).to(z.dtype)
+    z[2] = 0.5                                               # all alike
+    z[3] = float("-inf")                                     # nothing in the first round but one
+    z[3, 17] = -3.0
+    z[3, V // 2 + 100:V // 2 + 160] = up[:60].to(z.dtype)
+    z[4] = torch.finfo(DT[dt]).min
+    z[5, :V // 8] -= 40                                      # the best behind the first eighth of each quarter
+    token = np.random.default_rng(V).integers(0, V, rows)
+    got, again = run_score(sd, z, 1.1, token, top), run_score(sd, z, 1.1, token, top)
+    assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(got, again))
+    # S: V / 1024 terms in each half of a thread's pair, 32 additions behind, exp2 and its argument as in `near`
+    tol = (V / 1024 + 96) * 2.0 ** -24
+    ok = lambda a, b: np.isneginf(a) if b < -3.4028235e38 else abs(a - b) <= tol + 4 * 2.0 ** -24 * (2 * abs(b) + 13)
+    for r in (*range(7), 80, rows - 1):
+        lp, rank, H, ids, lps = score_ref(z[r], 1.1, int(token[r]), top)
+        assert ok(got[0][r], lp) and got[1][r] == rank, r
+        assert abs(got[2][r] - H) <= 2 * tol * (1 + H), r
+        np.testing.assert_array_equal(got[3][r], ids)
+        assert all(ok(a, b) for a, b in zip(got[4][r], lps)), r
+
+
 @pytest.mark.parametrize("V", [100, 60000])
 def test_score_rows_without_a_distribution(sd, V):
     z = torch.zeros(4, V, device="cuda")
