@@ -222,6 +222,55 @@ def test_fork_again_and_again_keeps_every_page(sd):
         assert not named & set(free.tolist()) and len(named) + len(free) == n_pages
 
 
+@pytest.mark.parametrize("R,N", [(6, 20), (2500, 2400)])
+def test_fork_and_compact_captured_and_on_two_streams(sd, R, N):
+    """Two streams, a workspace each, replay a fork and a compaction of what it gave; the inputs change between the replays."""
+    ps, n_pages, width = 8, 40000, 12
+    new = lambda *s: torch.full(s, -7, dtype=torch.int32, device="cuda")
+    work = max(sd.sd_page_work(R, N, n_pages), sd.sd_page_work(N, 0, n_pages))
+    sides = []
+    for _ in range(2):
+        x = dict(table=new(R, width), n=new(R), parent=new(N), free=new(30000), out=new(N, width), length=new(N), copies=new(N, 3),
+                 ref=new(n_pages), free_out=new(n_pages), info=new(4), work=new(work), stream=torch.cuda.Stream(),
+                 out2=new(N, width), moves=new(n_pages // 2, 3), ref2=new(n_pages), free2=new(n_pages), info2=new(4))
+        torch.cuda.synchronize()
+        x["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(x["graph"], stream=x["stream"]):
+            s = x["stream"].cuda_stream
+            sd.sd_page_fork(x["table"], width, x["n"], R, x["parent"], N, x["free"], 30000, ps, n_pages, x["out"], x["length"],
+                            x["copies"], x["ref"], x["free_out"], x["info"], x["work"], s)
+            sd.sd_page_compact(x["out"], width, x["length"], N, ps, n_pages, x["out2"], x["moves"], x["ref2"], x["free2"],
+                               x["info2"], x["work"], s)
+        sides.append(x)
+    rng = np.random.default_rng(N)
+    for _ in range(3):
+        want = []
+        for x in sides:
+            lens = rng.integers(0, width * ps + 1, R)
+            ids = rng.permutation(n_pages)
+            table, free = ids[:10000][rng.integers(0, 10000, (R, width))], ids[10000:]
+            parent = rng.integers(-1, R, N)
+            want.append(fork_ref(table, lens.tolist(), parent.tolist(), free, ps, n_pages))
+            for name, v in (("table", table), ("n", lens), ("parent", parent), ("free", free)):
+                x[name].copy_(i32(v))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for x in sides:
+                with torch.cuda.stream(x["stream"]):
+                    x["graph"].replay()
+        torch.cuda.synchronize()
+        for x, w in zip(sides, want):
+            np.testing.assert_array_equal(x["info"].cpu(), w[5])
+            np.testing.assert_array_equal(x["out"].cpu(), w[0])
+            np.testing.assert_array_equal(x["length"].cpu(), w[1])
+            np.testing.assert_array_equal(x["ref"].cpu(), w[3])
+            np.testing.assert_array_equal(x["free_out"][:len(w[4])].cpu(), w[4])
+            c = compact_ref(w[0], w[1], ps, n_pages)
+            np.testing.assert_array_equal(x["info2"].cpu(), c[3])
+            np.testing.assert_array_equal(x["out2"].cpu(), c[0])
+            np.testing.assert_array_equal(x["moves"][:len(c[1])].cpu(), np.asarray(c[1]).reshape(-1, 3))
+
+
 # ------------------------------------------------------------------ compact
 
 def compact_ref(table, ln, ps, n_pages):
