@@ -51,7 +51,7 @@ struct AttendArgs {
     float* recs;                     // shared pages
     SharedRow* desc;
     int32_t* shared;                 // 1: the kernels for shared pages serve this call, 0: the split kernel does; NULL: it does
-    long long stall;                 // test hook: block 0 waits as many cycles for a barrier that nothing arrives at
+    long long stall;                 // test hook: a block waits as many cycles for a barrier that nothing arrives at
 };
 
 constexpr int kSplitRows = 8;                                     // query rows of a unit

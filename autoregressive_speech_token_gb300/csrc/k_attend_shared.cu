@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_shared(const __grid_cons
                     const uint32_t e = 2 * (n + j) + op, slot = e % kSt, turn = e / kSt;
                     if (turn > 0) ok = warp_wait(smem_u32(&s_empty[slot]), (turn - 1) & 1, bad);
                     if (!ok) break;
-                    if (a.stall && blockIdx.x == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
+                    if (a.stall && it.i0 == 0 && it.g == 0) ok = warp_wait(smem_u32(&s_never), 0, bad, a.stall);
                     if (!ok) break;
                     last = e + 1;
                     const uint32_t mb = smem_u32(&s_full[slot]), dst = ring + slot * C::kTileBytes;

@@ -617,6 +617,52 @@ def test_shared_many_requests(sd, ws):
     assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("hd,dt", [(128, "f16"), (64, "f32")])
+def test_shared_expired_wait_is_reported_and_replays_give_nan(sd, monkeypatch, hd, dt):
+    """A test hook (SD_TEST_STALL_US) lets a load warp of the first uncaptured call wait 1 ms for a barrier that nothing
+    arrives at.  The next call with the workspace is refused; replays of a graph captured before give NaN; another
+    workspace works."""
+    g = gen(14)
+    kc, vc, table, rows, lens, starts, shared = build_groups(g, np.random.default_rng(14), [(60, [970 + 9 * i for i in range(12)])],
+                                                             [200], 2, hd, 16, "f16", "hnd")
+    q, cache, ld = randn(g, 13, 4, hd, dt=dt), sd.Pages.of(kc, vc), i32(lens)
+    monkeypatch.setenv("SD_SHARE_MIN_BYTES", "0")
+    good = sd.AttnWorkspace()
+    monkeypatch.setenv("SD_TEST_STALL_US", "1000")
+    w = sd.AttnWorkspace()
+    monkeypatch.delenv("SD_TEST_STALL_US")
+    out, lse = torch.zeros_like(q), torch.zeros(13, 4, device="cuda")
+
+    def call(x):
+        sd.sd_attend_shared(x, cache, table, table.shape[1], ld, 13, starts, shared, 1, sd.DTYPES[dt], q, 4 * hd, 4, 0.1, out,
+                            4 * hd, lse, torch.cuda.current_stream().cuda_stream)
+
+    call(good)
+    torch.cuda.synchronize()
+    want, want_lse = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(w)                                            # captured: leaves the hook to the next call
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    call(w)                                                # this one takes it
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with pytest.raises(sd.SdError) as e:
+            call(w)
+        assert e.value.code == -6
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.all(torch.isnan(out)) and torch.all(torch.isnan(lse))
+    call(good)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 # ------------------------------------------------------------------ scores
 
 def score_ref(z, T, token, top):
