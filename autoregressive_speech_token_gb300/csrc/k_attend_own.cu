@@ -7,6 +7,9 @@
 // takes chunks of 16 or 32 positions in turn with the others, by itself: its copies (cp.async into two stages, 0 where
 // no position is), scores and sums need no other warp until the unit ends.  The products are mma.sync in transposed form,
 // S^T = K q^T and O^T = V^T P^T, as in the split kernel, with the same precision.
+//
+// Measured: 30 us for 776 units of up to 500 positions of 128, 50 MB from memory (1.7 TB/s); 19 us for 1024 units of up to 125
+// positions of 64.  Bound by the chain of a unit: lengths, table, first copies, products, records, join.
 #include "mma_dev.cuh"
 
 namespace sd {

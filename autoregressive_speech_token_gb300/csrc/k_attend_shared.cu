@@ -15,6 +15,12 @@
 // Queries are written to shared memory by the warpgroups themselves, whatever their type and stride.  Where the
 // keys' type does not hold them (fp32, or the other 16-bit type) they enter as two parts, rows scaled by
 // a power of two, and so do the probabilities: three to four times the products, with 128 rows to an item.
+//
+// Measured: 8 groups of 2 to 32 requests behind 1000 to 16000 positions, 64 query and 8 kv heads of 128, bf16, 193 MB
+// read: 48 us of the call's 79, 4.0 TB/s and 27 % of the tensor pipe (the requests each by itself 105 us, mostly from L2).  64 rollouts
+// behind 2000 positions, 16 heads of 64, fp32: 20 of 29 us (66 each by itself).  What bounds it: the first 9000 cycles, until
+// a block knows its piece and the first keys are there, and the last block's record; in between a tile passes in
+// 1500 to 2000 cycles, the time from scores to exponentials to products.
 #include <algorithm>
 
 #include "tc_dev.cuh"

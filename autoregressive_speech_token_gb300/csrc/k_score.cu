@@ -22,7 +22,8 @@
 //
 // Measured (token, rank, entropy and best entries of every row): 16 rows of 2048 6 us, a chain of exchanges; 800 of 8194
 // fp32 with 20 wanted 20 us = 1.3 TB/s, where the ranking and the chain of a short row bound it (14.5 without); 1021 of
-// 131075 bf16 with 5 wanted 85 us = 3.1 TB/s, where the instructions of the sums do; fp32 without any 112 us = 4.8 TB/s.
+// 131075 bf16 with 8 wanted 87 us = 3.1 TB/s, where the issue of instructions does (78 % busy, 149 for a warp's
+// 32 vectors; the bound of exp2 is 28 us); fp32 without any 112 us = 4.8 TB/s.
 #include <algorithm>
 
 #include "pages_dev.cuh"
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         if ((q & 7) == 7) flush();
         // About top_n times the number of rounds will have reached the first round's bound.  Behind rounds 4 and 16 it is
         // raised, which stalls the block for 1.5 us: 1021 rows of 131075 fp32 with 20 wanted 190 -> 142 us, but of bf16 (half
-        // the rounds) with 5 wanted 85 -> 90
+        // the rounds) with 8 wanted 85 -> 90
         if (a.top * quarter > kPutAside && (q == 3 || q == 15) && 2 * (q + 1) <= quarter) {
             tau = higher_bound(tau);
             bound = value_bound(tau);

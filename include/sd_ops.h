@@ -258,7 +258,7 @@ int sd_rope_write_pages(const sd_rope* rope, const int32_t* pos_dev, int64_t pos
                         int64_t kv_stride, const sd_pages* cache, void* stream);
 
 /* Workspace of the attention entries below: the partial results of split
- * lengths, fixed at about 20 MB, allocated here on `device` (-1: the current one).
+ * lengths and of groups, fixed at about 80 MB, allocated here on `device` (-1: the current one).
  * Calls with one workspace, replays of graphs that captured one among them, must
  * not overlap: one workspace for each stream.  A kernel whose bounded waits (about
  * two seconds each) expire leaves its results unfinished; every later call with the
@@ -325,7 +325,7 @@ int sd_attend_cross(sd_attn_ws* ws, const sd_states* states, int32_t dtype, cons
  * (sd_attend_shared: of its workspace's device).  The buffers of a call must not overlap,
  * but for what is said. */
 
-/* int32 words of work_dev (8-byte aligned, any contents) for sd_page_fork with R rows, N new rows and n_pages
+/* int32 words of work_dev (8-byte aligned, any contents; one for each call that may run beside another) for sd_page_fork with R rows, N new rows and n_pages
  * pages, and for sd_page_compact (N 0).  0 for negative counts or n_pages below 1. */
 int64_t sd_page_work(int32_t R, int32_t N, int32_t n_pages);
 
@@ -382,7 +382,10 @@ int sd_page_copy(const sd_pages* caches, int32_t n_caches, const int32_t* copy_d
  * n_groups + 1 numbers, all on the device), whose table rows name the same pages in their first
  * shared_dev[x] entries; the page ids are taken from any of those rows.  A request in no group, or with shorter
  * length than the group's pages, is served too.  n_groups 0: sd_attend_pages.  Everything else as in sd_attend_pages.
- * (With SD_F32 queries an infinite key at a shared position may give NaN.) */
+ * (With SD_F32 queries an infinite key at a shared position may give NaN.)  Groups are served together where that saves
+ * reading enough: 150 MB of keys and values, 75 MB with SD_F32 queries (the device decides, from the groups).  Each
+ * request is served by itself below that, with SD_E4M3 pages, a scale of 0 or outside 2^-60 to 2^60, and
+ * more than 65536 query heads in all (R * n_head). */
 int sd_attend_shared(sd_attn_ws* ws, const sd_pages* cache, const int32_t* table_dev, int32_t table_stride,
                      const int32_t* len_dev, int32_t R, const int32_t* group_dev, const int32_t* shared_dev,
                      int32_t n_groups, int32_t dtype, const void* q_dev, int64_t q_stride, int32_t n_head, float scale,
