@@ -614,11 +614,17 @@ void lay_out_work(RowArgs& a, int32_t* work, int32_t R) {
     a.place = a.first + R;
 }
 
+// Every block of a pass counts for itself what lies before its part, so that work grows with the square of the new rows and of the
+// bit map's words: 2^20 rows and 2^26 pages are tenths of a second.  Entries of a row are counted in 32 bits, 256 at a time.
+constexpr int kMaxNew = 1 << 20, kMaxPages = 1 << 26, kMaxWidth = 1 << 30;
+
 int check_rows(const char* who, const void* table, int table_stride, const void* len, int R, int page_size, int n_pages) {
     if (R < 0 || table_stride < 1 || page_size < 1 || page_size > 65536 || n_pages < 1 ||
         (int64_t)n_pages * page_size > INT32_MAX)
         return op_fail(SD_ERR_INVALID_ARG, "%s: R %d, table_stride %d, page_size %d, n_pages %d", who, R, table_stride,
                        page_size, n_pages);
+    if (table_stride > kMaxWidth || n_pages > kMaxPages)
+        return op_fail(SD_ERR_UNSUPPORTED, "%s: table_stride %d (up to 2^30), n_pages %d (up to 2^26)", who, table_stride, n_pages);
     if (R > 0 && (!table || !len)) return op_fail(SD_ERR_INVALID_ARG, "%s: table_dev or len_dev is NULL", who);
     return SD_OK;
 }
@@ -641,6 +647,7 @@ int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* 
     static const char* who = "sd_page_fork";
     if (int rc = check_rows(who, table_dev, table_stride, len_dev, R, page_size, n_pages)) return rc;
     if (N < 0 || n_free < 0) return op_fail(SD_ERR_INVALID_ARG, "%s: N %d, n_free %d", who, N, n_free);
+    if (N > kMaxNew) return op_fail(SD_ERR_UNSUPPORTED, "%s: N %d (up to 2^20)", who, N);
     if (N > 0 && (!parent_dev || !table_out_dev || !len_out_dev || !copy_dev))
         return op_fail(SD_ERR_INVALID_ARG, "%s: parent_dev, table_out_dev, len_out_dev or copy_dev is NULL", who);
     if (n_free > 0 && !free_dev) return op_fail(SD_ERR_INVALID_ARG, "%s: free_dev is NULL", who);

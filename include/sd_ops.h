@@ -349,7 +349,8 @@ int64_t sd_page_work(int32_t R, int32_t N, int32_t n_pages);
  *  16 a page id outside [0, n_pages) in use or taken: -1 in the new row, counted nowhere; a copy
  *     from or to it names -1, and a row that took it ends before that page
  * A partly filled page belongs to one old row, and no free page is in use.  R, N and n_free may be 0 (the
- * pointers that belong to them may be NULL then).  page_size 1 to 65536, n_pages * page_size at most 2^31 - 1. */
+ * pointers that belong to them may be NULL then).  page_size 1 to 65536, n_pages * page_size at most 2^31 - 1,
+ * n_pages at most 2^26, N at most 2^20, table_stride at most 2^30. */
 int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* len_dev, int32_t R,
                  const int32_t* parent_dev, int32_t N, const int32_t* free_dev, int32_t n_free, int32_t page_size,
                  int32_t n_pages, int32_t* table_out_dev, int32_t* len_out_dev, int32_t* copy_dev, int32_t* ref_dev,
@@ -363,7 +364,8 @@ int sd_page_fork(const int32_t* table_dev, int32_t table_stride, const int32_t* 
  *                              rest stays as it was
  *   ref_dev [n_pages]          how many rows name the page now
  *   free_out_dev [n_pages]     L, L + 1, ..., n_pages - 1; the rest stays as it was
- *   info_dev [4]               moves; n_pages - L; bits 4, 8 and 16 as in sd_page_fork; L */
+ *   info_dev [4]               moves; n_pages - L; bits 4, 8 and 16 as in sd_page_fork; L
+ * Sizes as in sd_page_fork. */
 int sd_page_compact(const int32_t* table_dev, int32_t table_stride, const int32_t* len_dev, int32_t R,
                     int32_t page_size, int32_t n_pages, int32_t* table_out_dev, int32_t* copy_dev, int32_t* ref_dev,
                     int32_t* free_out_dev, int32_t* info_dev, int32_t* work_dev, void* stream);
@@ -378,7 +380,7 @@ int sd_page_copy(const sd_pages* caches, int32_t n_caches, const int32_t* copy_d
 
 /* sd_attend_pages for requests that share their first pages (rollouts of one prompt): the same results, with the
  * common keys and values read once for a group instead of once a request.  Group x is
- * requests group_dev[x] to group_dev[x + 1] - 1 (x < n_groups; ascending, between 0 and R; group_dev has
+ * requests group_dev[x] to group_dev[x + 1] - 1 (x < n_groups <= R; ascending, between 0 and R; group_dev has
  * n_groups + 1 numbers, all on the device), whose table rows name the same pages in their first
  * shared_dev[x] entries; the page ids are taken from any of those rows.  A request in no group, or with shorter
  * length than the group's pages, is served too.  n_groups 0: sd_attend_pages.  Everything else as in sd_attend_pages.

@@ -59,6 +59,18 @@ def test_compact_refusals(kw, words):
     refused(INVALID, words, pkg.sd_page_compact, *_compact(**kw))
 
 
+@pytest.mark.parametrize("kw,words", [
+    (dict(width=2 ** 30 + 1), "table_stride 1073741825"), (dict(width=2 ** 31 - 1), "2^30"),
+    (dict(page=1, n_pages=2 ** 26 + 1), "n_pages 67108865")])
+def test_sizes_beyond_what_the_passes_count(kw, words):
+    refused(UNSUPPORTED, words, pkg.sd_page_fork, *_fork(**kw))
+    refused(UNSUPPORTED, words, pkg.sd_page_compact, *_compact(**kw))
+
+
+def test_fork_of_too_many_rows():
+    refused(UNSUPPORTED, "N 1048577", pkg.sd_page_fork, *_fork(N=2 ** 20 + 1))
+
+
 def test_work_words():
     assert pkg.sd_page_work(-1, 0, 5) == 0 and pkg.sd_page_work(0, -1, 5) == 0 and pkg.sd_page_work(1, 1, 0) == 0
     assert pkg.sd_page_work(0, 0, 1) > 0
