@@ -164,6 +164,13 @@ def test_fork_against_plain(sd, R, N, ps, high, beams, spare):
     check_fork(sd, table, lens, parent, free, ps, n_pages)
 
 
+def test_fork_into_the_most_rows(sd):
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, 1000).tolist()
+    table, free, n_pages = rows_of(rng, lens, 16, 1 << 20)
+    check_fork(sd, table, lens, rng.integers(-1, 1000, 1 << 20).tolist(), free, 16, n_pages)
+
+
 @pytest.mark.parametrize("large", [False, True])
 @pytest.mark.parametrize("case", ["short", "none", "wide", "negative", "bad_page", "bad_free", "no_new", "no_old", "nothing"])
 def test_fork_when_things_go_wrong(sd, case, large):
@@ -324,6 +331,14 @@ def test_compact_against_plain(sd, R, ps, high, beams, spare):
     lens = np.repeat(rng.integers(0, high, -(-R // beams)), beams)[:R].tolist()
     table, _, n_pages = rows_of(rng, lens, ps, spare, beams=beams)
     check_compact(sd, table, lens, ps, max(n_pages, 1))
+
+
+def test_compact_the_largest_pool(sd):
+    rng = np.random.default_rng(9)
+    n_pages = 1 << 26
+    table = rng.integers(0, n_pages, (300, 7))
+    table[0, :3] = 0, n_pages - 1, 2000
+    check_compact(sd, table, rng.integers(0, 7 * 16 + 1, 300).tolist(), 16, n_pages)
 
 
 @pytest.mark.parametrize("n_pages", [40, 20000])
