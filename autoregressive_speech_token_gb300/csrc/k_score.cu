@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
     // x >= zt is x > (what comes before zt in the type): entries before the token and behind it differ in one number
     const float before_zt = before_of<T>(zt);
     const Pair zt2 = pair_of<T>(zt), before_zt2 = pair_of<T>(before_zt);
+    const int before_end = zt > -INFINITY ? token : -kN;   // (what lies before the row is -inf: not ahead of a finite logit)
     auto count = [&](const uint4& w, int j) {
-        const bool behind = j > token, before = j >= 0 && j + kN <= token && zt > -INFINITY;
+        const bool behind = j > token, before = j + kN <= before_end;
         if (behind || before) {
             if constexpr (sizeof(T) == 4) {
                 const float x = behind ? zt : before_zt;
@@ -444,16 +445,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_max[w]);
         __syncthreads();                                   // s_max is used again
     }
-    float watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+    // A token below the best entries has some ahead of it in most vectors: counted in all of them without a look
+    const bool often = given && zt < fminf(m, bound);
+    const float rare = given && !often ? zt : INFINITY;
+    float watch = fminf(fminf(m, bound), rare), ref = m == -INFINITY ? 0.f : -m;
     auto visit = [&](const uint4& w, int j) {
         const float top = largest(w);
+        if (often) count(w, j);
         if (top >= watch) {                                // most vectors have nothing to be looked at
-            if (top > m) raise(top);
-            if (given && top >= zt) count(w, j);
+            if (top > m) {
+                raise(top);
+                ref = -m;
+            }
+            if (top >= rare) count(w, j);
             if (top >= bound) collect(w, j);
-            watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+            watch = fminf(fminf(m, bound), rare);
         }
-        const float ref = m == -INFINITY ? 0.f : -m;
         add(w, make_float2(ref, ref));
     };
     if (has_edge) visit(edge, edge_j);
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_score(const Score
         if (a.top * quarter > kPutAside && (q == 3 || q == 15) && 2 * (q + 1) <= quarter) {
             tau = higher_bound(tau);
             bound = value_bound(tau);
-            watch = fminf(fminf(m, bound), given ? zt : INFINITY);
+            watch = fminf(fminf(m, bound), rare);
         }
     }
     flush();
